@@ -1,5 +1,6 @@
 // C-ABI entry points: argument checks, problem sizes, launches.
 // The semantics of every entry point are documented in include/ep.h.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -562,6 +563,176 @@ int ep_combine_two_level(const ep_problem *p, const uint16_t *y, const int64_t *
     pick_pieces(d, 256, a.pieces, a.piece_elems);
     cudaError_t e = ep::launch_combine_two_level(a, stage, (cudaStream_t)stream);
     return e ? cuda_fail(e, "ep_combine_two_level launch") : EP_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks what ep_route and ep_route_backward share and fills a.
+int prepare_route(const ep_problem *p, const ep_router *r, int dtype, const void *logits, int64_t stride,
+                  int32_t *dev_status, ep::RouteArgs &a) {
+    ep::Dims d;
+    if (!make_dims(p, d)) return EP_ERR_INVALID_ARG;
+    if (!r) return fail(EP_ERR_INVALID_ARG, "router is NULL");
+    if (r->scoring != EP_SCORE_SOFTMAX && r->scoring != EP_SCORE_SIGMOID)
+        return fail(EP_ERR_INVALID_ARG, "unknown scoring %d", r->scoring);
+    if (r->num_groups < 1 || d.E % r->num_groups)
+        return fail(EP_ERR_INVALID_ARG, "num_experts must be a multiple of num_groups >= 1");
+    if (r->topk_groups < 1 || r->topk_groups > r->num_groups)
+        return fail(EP_ERR_INVALID_ARG, "topk_groups must be in 1..num_groups");
+    if (r->group_best != 1 && r->group_best != 2) return fail(EP_ERR_INVALID_ARG, "group_best must be 1 or 2");
+    if (!std::isfinite(r->scale)) return fail(EP_ERR_INVALID_ARG, "scale must be finite");
+    if (dtype != EP_BF16 && dtype != EP_FP32) return fail(EP_ERR_INVALID_ARG, "logits must be EP_BF16 or EP_FP32");
+    if (stride < d.E) return fail(EP_ERR_INVALID_ARG, "logits_row_stride smaller than num_experts");
+    if (!aligned(dev_status, 4)) return fail(EP_ERR_INVALID_ARG, "dev_status misaligned");
+    if (d.T > 0 && (!logits || !aligned(logits, dtype == EP_BF16 ? 2 : 4)))
+        return fail(EP_ERR_INVALID_ARG, "logits NULL or misaligned");
+    a.T = d.T;
+    a.E = d.E;
+    a.k = d.k;
+    a.r = *r;
+    a.bf16 = dtype == EP_BF16;
+    a.logits = logits;
+    a.stride = stride;
+    a.dev_status = dev_status;
+    return EP_OK;
+}
+
+// Checks what ep_expert_gemm and ep_expert_swiglu share and fills a.
+int prepare_expert(const ep_problem *p, int64_t N, int64_t K, const uint8_t *act, const float *act_scales,
+                   const uint8_t *w, const float *w_scales, const int32_t *tokens_per_expert, int32_t *dev_status,
+                   ep::ExpertArgs &a) {
+    ep::Dims &d = a.d;
+    if (!make_dims(p, d)) return EP_ERR_INVALID_ARG;
+    if (K < 128 || K % 128 || K > (1 << 24))
+        return fail(EP_ERR_INVALID_ARG, "the product's channels must be a multiple of 128, at most 2^24");
+    if (N < 8 || N % 8 || N > (1 << 24))
+        return fail(EP_ERR_INVALID_ARG, "out_features must be a multiple of 8, at most 2^24");
+    if (d.T > 0 && d.E > INT32_MAX / d.T) return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens exceeds int32");
+    if (d.T > 0) {
+        if (!act || !aligned(act, 16) || !w || !aligned(w, 16))
+            return fail(EP_ERR_INVALID_ARG, "a / w NULL or not 16-byte aligned");
+        if (!act_scales || !aligned(act_scales, 4) || !w_scales || !aligned(w_scales, 4))
+            return fail(EP_ERR_INVALID_ARG, "a_scales / w_scales NULL or misaligned");
+        if (!tokens_per_expert || !aligned(tokens_per_expert, 4))
+            return fail(EP_ERR_INVALID_ARG, "tokens_per_expert NULL or misaligned");
+    }
+    if (!aligned(dev_status, 4)) return fail(EP_ERR_INVALID_ARG, "dev_status misaligned");
+    a.N = N;
+    a.K = K;
+    a.a = act;
+    a.a_scales = act_scales;
+    a.w = w;
+    a.w_scales = w_scales;
+    a.tokens_per_expert = tokens_per_expert;
+    a.dev_status = dev_status;
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ep_route(const ep_problem *p, const ep_router *r, int dtype, const void *logits, int64_t logits_row_stride,
+             const float *bias, int64_t *topk_idx, float *topk_weights, int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    ep::RouteArgs a{};
+    const int rc = prepare_route(p, r, dtype, logits, logits_row_stride, dev_status, a);
+    if (rc != EP_OK || a.T == 0) return rc;
+    if (!aligned(bias, 4)) return fail(EP_ERR_INVALID_ARG, "bias misaligned");
+    if (!topk_idx || !aligned(topk_idx, 8) || !topk_weights || !aligned(topk_weights, 4))
+        return fail(EP_ERR_INVALID_ARG, "topk_idx / topk_weights NULL or misaligned");
+    a.bias = bias;
+    a.topk_idx = topk_idx;
+    a.topk_weights = topk_weights;
+    cudaError_t e = ep::launch_route(a, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_route launch") : EP_OK;
+}
+
+int ep_route_backward(const ep_problem *p, const ep_router *r, int dtype, const void *logits,
+                      int64_t logits_row_stride, const int64_t *topk_idx, const float *grad_weights,
+                      void *grad_logits, int64_t grad_row_stride, int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    ep::RouteArgs a{};
+    const int rc = prepare_route(p, r, dtype, logits, logits_row_stride, dev_status, a);
+    if (rc != EP_OK) return rc;
+    if (grad_row_stride < a.E) return fail(EP_ERR_INVALID_ARG, "grad_row_stride smaller than num_experts");
+    if (a.T == 0) return EP_OK;
+    if (!topk_idx || !aligned(topk_idx, 8) || !grad_weights || !aligned(grad_weights, 4))
+        return fail(EP_ERR_INVALID_ARG, "topk_idx / grad_weights NULL or misaligned");
+    if (!grad_logits || !aligned(grad_logits, a.bf16 ? 2 : 4))
+        return fail(EP_ERR_INVALID_ARG, "grad_logits NULL or misaligned");
+    a.grad_weights = grad_weights;
+    a.grad_logits = grad_logits;
+    a.grad_stride = grad_row_stride;
+    cudaError_t e = ep::launch_route_backward(a, topk_idx, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_route_backward launch") : EP_OK;
+}
+
+int ep_combine_backward(const ep_problem *p, int layout, const uint16_t *grad_out, const uint16_t *y,
+                        const int64_t *topk_idx, const float *topk_weights, const int32_t *rank_slot,
+                        const int32_t *expert_slot, uint16_t *grad_y, float *grad_weights, int32_t *dev_status,
+                        ep_stream_t stream) {
+    g_err[0] = 0;
+    ep::Dims d;
+    if (!make_dims(p, d)) return EP_ERR_INVALID_ARG;
+    if (layout != EP_RANK_MAJOR && layout != EP_EXPERT_MAJOR)
+        return fail(EP_ERR_INVALID_ARG, "unknown layout %d", layout);
+    if (!aligned(dev_status, 4)) return fail(EP_ERR_INVALID_ARG, "dev_status misaligned");
+    if (d.T == 0 || (!grad_y && !grad_weights)) return EP_OK;
+    if (!grad_out || !aligned(grad_out, 16)) return fail(EP_ERR_INVALID_ARG, "grad_out NULL or not 16-byte aligned");
+    if (!aligned(grad_y, 16)) return fail(EP_ERR_INVALID_ARG, "grad_y not 16-byte aligned");
+    if (!aligned(grad_weights, 4)) return fail(EP_ERR_INVALID_ARG, "grad_weights misaligned");
+    if (grad_weights && (!y || !aligned(y, 16))) return fail(EP_ERR_INVALID_ARG, "y NULL or not 16-byte aligned");
+    if (!topk_idx || !aligned(topk_idx, 8) || !topk_weights || !aligned(topk_weights, 4))
+        return fail(EP_ERR_INVALID_ARG, "topk_idx / topk_weights NULL or misaligned");
+    if (layout == EP_RANK_MAJOR && (!rank_slot || !aligned(rank_slot, 4)))
+        return fail(EP_ERR_INVALID_ARG, "rank_slot NULL or misaligned");
+    if (layout == EP_EXPERT_MAJOR && (!expert_slot || !aligned(expert_slot, 4)))
+        return fail(EP_ERR_INVALID_ARG, "expert_slot NULL or misaligned");
+    ep::CombineArgs a{};
+    a.d = d;
+    a.y = y;
+    a.topk_idx = topk_idx;
+    a.topk_weights = topk_weights;
+    a.rank_slot = rank_slot;
+    a.expert_slot = expert_slot;
+    a.dev_status = dev_status;
+    cudaError_t e = ep::launch_combine_backward(layout, a, grad_out, grad_y, grad_weights, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_combine_backward launch") : EP_OK;
+}
+
+int ep_expert_gemm(const ep_problem *p, int64_t out_features, int64_t in_features, const uint8_t *act,
+                   const float *a_scales, const uint8_t *w, const float *w_scales,
+                   const int32_t *tokens_per_expert, uint16_t *y, int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    ep::ExpertArgs a{};
+    const int rc = prepare_expert(p, out_features, in_features, act, a_scales, w, w_scales, tokens_per_expert,
+                                  dev_status, a);
+    if (rc != EP_OK || a.d.T == 0) return rc;
+    if (!y || !aligned(y, 16)) return fail(EP_ERR_INVALID_ARG, "y NULL or not 16-byte aligned");
+    a.y = y;
+    cudaError_t e = ep::launch_expert(a, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_expert_gemm launch") : EP_OK;
+}
+
+int ep_expert_swiglu(const ep_problem *p, int64_t intermediate, const uint8_t *act, const float *a_scales,
+                     const uint8_t *w, const float *w_scales, const int32_t *tokens_per_expert, uint8_t *q,
+                     float *q_scales, int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    ep::ExpertArgs a{};
+    if (intermediate < 128 || intermediate % 128 || intermediate > (1 << 23))
+        return fail(EP_ERR_INVALID_ARG, "intermediate must be a multiple of 128, at most 2^23");
+    const int rc = prepare_expert(p, 2 * intermediate, p ? p->hidden : 0, act, a_scales, w, w_scales,
+                                  tokens_per_expert, dev_status, a);
+    if (rc != EP_OK || a.d.T == 0) return rc;
+    if (!q || !aligned(q, 16) || !q_scales || !aligned(q_scales, 4))
+        return fail(EP_ERR_INVALID_ARG, "q / q_scales NULL or misaligned");
+    a.q = q;
+    a.q_scales = q_scales;
+    cudaError_t e = ep::launch_expert(a, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_expert_swiglu launch") : EP_OK;
 }
 
 }  // extern "C"

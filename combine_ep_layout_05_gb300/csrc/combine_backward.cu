@@ -1,0 +1,102 @@
+// Combine, backward: the gradients of the expert rows and of the weights.
+//   grad_y[row(t, j)] = w_tj * grad_out[t]          (weights of a shared row summed)
+//   grad_w[t, j]      = <grad_out[t], y[row(t, j)]>
+// A CTA owns one token: a lane reads a 16-byte chunk of grad_out once, the
+// same chunk of up to 8 rows of y, adds to its part of each row's dot
+// product, and writes the scaled chunk to each row of grad_y.  The parts meet
+// in a fixed order (lanes by halving, then warps in order): no atomics.
+#include "combine_device.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kBackRows = 8;   // rows a pass keeps in flight
+
+template <int LAYOUT>
+__global__ void __launch_bounds__(kWarps * 32) combine_backward_kernel(CombineArgs a, const uint16_t *grad_out,
+                                                                      uint16_t *grad_y, float *grad_weights) {
+    __shared__ int64_t s_rows[kMaxTopk];
+    __shared__ float s_wts[kMaxTopk], s_dot[kWarps][kMaxTopk];
+    __shared__ int s_nd, s_entry[kMaxTopk];
+    const Dims &d = a.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = blockIdx.x, hc = d.H / 8;
+    if (warp == 0) {
+        int entry;
+        const int nd = resolve_sources<LAYOUT>(a, t, t / d.Tr, load_route<LAYOUT>(a, t), s_rows, s_wts, &entry);
+        s_entry[lane] = entry;
+        if (lane == 0) s_nd = nd;
+    }
+    __syncthreads();
+    const int nd = s_nd;
+    const uint4 *go = reinterpret_cast<const uint4 *>(grad_out) + t * hc;
+    const uint4 *y = reinterpret_cast<const uint4 *>(a.y);
+    uint4 *gy = reinterpret_cast<uint4 *>(grad_y);
+    for (int g0 = 0; g0 < nd; g0 += kBackRows) {
+        float dot[kBackRows] = {};
+        for (int64_t c = threadIdx.x; c < hc; c += kWarps * 32) {
+            uint4 v[kBackRows];
+            if (grad_weights) {
+#pragma unroll
+                for (int i = 0; i < kBackRows; ++i)
+                    if (g0 + i < nd) v[i] = ld_stream(y + s_rows[g0 + i] * hc + c);
+            }
+            const uint4 o4 = go[c];
+            const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
+            float o[8];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) { o[2 * h] = bf16_lo(ow[h]); o[2 * h + 1] = bf16_hi(ow[h]); }
+#pragma unroll
+            for (int i = 0; i < kBackRows; ++i) {
+                if (g0 + i >= nd) continue;
+                if (grad_weights) {
+                    const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        dot[i] = __fmaf_rn(o[2 * h], bf16_lo(q[h]), dot[i]);
+                        dot[i] = __fmaf_rn(o[2 * h + 1], bf16_hi(q[h]), dot[i]);
+                    }
+                }
+                if (grad_y) {
+                    const float w = s_wts[g0 + i];
+                    st_v4(gy + s_rows[g0 + i] * hc + c,
+                          make_uint4(pack_bf16x2(w * o[0], w * o[1]), pack_bf16x2(w * o[2], w * o[3]),
+                                     pack_bf16x2(w * o[4], w * o[5]), pack_bf16x2(w * o[6], w * o[7])));
+                }
+            }
+        }
+        if (grad_weights) {
+#pragma unroll
+            for (int i = 0; i < kBackRows; ++i) {
+                float v = dot[i];
+#pragma unroll
+                for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(kFull, v, s);
+                if (lane == 0 && g0 + i < kMaxTopk) s_dot[warp][g0 + i] = v;
+            }
+        }
+    }
+    if (!grad_weights) return;
+    __syncthreads();
+    if (threadIdx.x < d.k) {
+        const int i = s_entry[threadIdx.x];
+        float v = 0.f;
+        if (i >= 0)
+            for (int w = 0; w < kWarps; ++w) v += s_dot[w][i];
+        grad_weights[t * d.k + threadIdx.x] = v;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_combine_backward(int layout, const CombineArgs &a, const uint16_t *grad_out, uint16_t *grad_y,
+                                    float *grad_weights, cudaStream_t st) {
+    const unsigned grid = (unsigned)a.d.T, block = kWarps * 32;
+    if (layout == EP_RANK_MAJOR)
+        combine_backward_kernel<EP_RANK_MAJOR><<<grid, block, 0, st>>>(a, grad_out, grad_y, grad_weights);
+    else
+        combine_backward_kernel<EP_EXPERT_MAJOR><<<grid, block, 0, st>>>(a, grad_out, grad_y, grad_weights);
+    return cudaGetLastError();
+}
+
+}  // namespace ep

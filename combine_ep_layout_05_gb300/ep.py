@@ -21,12 +21,15 @@ LIB_PATH = os.path.join(_HERE, "libep.so")
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CUDA, EP_ERR_DEVICE = 0, 1, 2, 3
 EP_STATUS_BAD_EXPERT, EP_STATUS_DUP_EXPERT, EP_STATUS_BAD_SLOT, EP_STATUS_TIMEOUT = 1, 2, 4, 8
+EP_STATUS_BAD_LOGIT = 16
 EP_RANK_MAJOR, EP_EXPERT_MAJOR = 0, 1
-EP_BF16, EP_FP8_E4M3 = 0, 1
+EP_BF16, EP_FP8_E4M3, EP_FP32 = 0, 1, 2
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_WIRE_MXFP8, EP_WIRE_NVFP4 = 1, 2
 WIRES = {"mxfp8": EP_WIRE_MXFP8, "nvfp4": EP_WIRE_NVFP4}
 
 LAYOUTS = {"rank_major": EP_RANK_MAJOR, "expert_major": EP_EXPERT_MAJOR}
+SCORINGS = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
 DTYPES = {"bf16": EP_BF16, "fp8_e4m3": EP_FP8_E4M3}
 
 # every symbol include/ep.h declares
@@ -34,7 +37,8 @@ EXPORTS = ("ep_last_error_string", "ep_get_status", "ep_recv_rows", "ep_layout_w
            "ep_rdma_token_count", "ep_rdma_physical_formula", "ep_dispatch", "ep_combine",
            "ep_dequant_fp8", "ep_layout_noalloc", "ep_layout_dispatch_workspace_bytes", "ep_layout_dispatch",
            "ep_selftest_wait_timeout", "ep_combine_quantize", "ep_combine_wire", "ep_stage_rows",
-           "ep_dispatch_two_level", "ep_combine_two_level")
+           "ep_dispatch_two_level", "ep_combine_two_level", "ep_route", "ep_route_backward",
+           "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu")
 
 
 class EpError(RuntimeError):
@@ -55,6 +59,19 @@ class ep_problem(ctypes.Structure):
     @property
     def N(self):
         return self.num_ranks // self.gpus_per_node
+
+
+class ep_router(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def router(scoring: str = "softmax", num_groups: int = 1, topk_groups: int = 1, group_best: int = 1,
+           renormalize: bool = True, scale: float = 1.0) -> ep_router:
+    """How ep_route scores and chooses: "softmax" or "sigmoid" scores; the best `topk_groups` of `num_groups`
+    groups, each scored by the sum of its best `group_best` keys; weights divided by their sum or not, times
+    `scale`."""
+    return ep_router(SCORINGS[scoring], num_groups, topk_groups, group_best, int(renormalize), scale)
 
 
 def problem(T: int, H: int, k: int, E: int, R: int, G: int | None = None) -> ep_problem:
@@ -105,6 +122,17 @@ def _load():
     lib.ep_dispatch_two_level.restype = i
     lib.ep_combine_two_level.argtypes = [pp, P, P, P, P, P, P, P, P, P]
     lib.ep_combine_two_level.restype = i
+    rp = ctypes.POINTER(ep_router)
+    lib.ep_route.argtypes = [pp, rp, i, P, i64, P, P, P, P, P]
+    lib.ep_route.restype = i
+    lib.ep_route_backward.argtypes = [pp, rp, i, P, i64, P, P, P, i64, P, P]
+    lib.ep_route_backward.restype = i
+    lib.ep_combine_backward.argtypes = [pp, i, P, P, P, P, P, P, P, P, P, P]
+    lib.ep_combine_backward.restype = i
+    lib.ep_expert_gemm.argtypes = [pp, i64, i64, P, P, P, P, P, P, P, P]
+    lib.ep_expert_gemm.restype = i
+    lib.ep_expert_swiglu.argtypes = [pp, i64, P, P, P, P, P, P, P, P, P]
+    lib.ep_expert_swiglu.restype = i
     return lib
 
 
@@ -371,6 +399,97 @@ def ep_combine_two_level(p: ep_problem, y, topk_idx, topk_weights, rank_slot, no
         _ptr(rank_slot, torch.int32, "rank_slot", T * R), _ptr(node_slot, torch.int32, "node_slot", T * N),
         _ptr(stage, torch.bfloat16, "stage", ep_stage_rows(p) * H), _ptr(out, torch.bfloat16, "out", T * H),
         _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+def _logits(t, p, name):
+    """(pointer, row stride, dtype code) of a [T, E] tensor whose rows are contiguous (any row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    T, E = p.num_tokens, p.num_experts
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != E:
+        raise ValueError(f"{name} must be [{T}, {E}], got {list(t.shape)}")
+    stride = t.stride(0) if T > 1 else E
+    if (E > 1 and t.stride(1) != 1) or stride < E:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), stride, EP_BF16 if t.dtype == torch.bfloat16 else EP_FP32
+
+
+def ep_route(p: ep_problem, r: ep_router, logits, bias, topk_idx, topk_weights, dev_status=None,
+             stream=None) -> None:
+    """Logits [T, E] (bf16 or fp32, any row stride) -> topk_idx and topk_weights; bias [E] fp32 or None."""
+    n = p.num_tokens * p.num_topk
+    ptr, stride, dt = _logits(logits, p, "logits")
+    return _call("ep_route", _lib.ep_route, (
+        ctypes.byref(p), ctypes.byref(r), dt, ptr, stride, _ptr(bias, torch.float32, "bias", p.num_experts),
+        _ptr(topk_idx, torch.int64, "topk_idx", n), _ptr(topk_weights, torch.float32, "topk_weights", n),
+        _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+def ep_route_backward(p: ep_problem, r: ep_router, logits, topk_idx, grad_weights, grad_logits, dev_status=None,
+                      stream=None) -> None:
+    """Gradient of ep_route's weights: writes all of grad_logits [T, E] (the logits' dtype, any row stride)."""
+    n = p.num_tokens * p.num_topk
+    ptr, stride, dt = _logits(logits, p, "logits")
+    gptr, gstride, gdt = _logits(grad_logits, p, "grad_logits")
+    if gdt != dt:
+        raise TypeError(f"grad_logits must have the logits' dtype {logits.dtype}, got {grad_logits.dtype}")
+    return _call("ep_route_backward", _lib.ep_route_backward, (
+        ctypes.byref(p), ctypes.byref(r), dt, ptr, stride, _ptr(topk_idx, torch.int64, "topk_idx", n),
+        _ptr(grad_weights, torch.float32, "grad_weights", n), gptr, gstride,
+        _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+def ep_combine_backward(p: ep_problem, layout: str, grad_out, y, topk_idx, topk_weights, rank_slot, expert_slot,
+                        grad_y=None, grad_weights=None, dev_status=None, stream=None) -> None:
+    """Gradients of ep_combine; an output that is None is not computed (y may be None without grad_weights)."""
+    rows, H, T, k = ep_recv_rows(p, layout), p.hidden, p.num_tokens, p.num_topk
+    return _call("ep_combine_backward", _lib.ep_combine_backward, (
+        ctypes.byref(p), LAYOUTS[layout], _ptr(grad_out, torch.bfloat16, "grad_out", T * H),
+        _ptr(y, torch.bfloat16, "y", rows * H), _ptr(topk_idx, torch.int64, "topk_idx", T * k),
+        _ptr(topk_weights, torch.float32, "topk_weights", T * k),
+        _ptr(rank_slot, torch.int32, "rank_slot", T * p.num_ranks),
+        _ptr(expert_slot, torch.int32, "expert_slot", T * k), _ptr(grad_y, torch.bfloat16, "grad_y", rows * H),
+        _ptr(grad_weights, torch.float32, "grad_weights", T * k), _ptr(dev_status, torch.int32, "dev_status", 1),
+        _stream(stream)))
+
+
+def _expert_shape(p, w, name):
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[0] != p.num_experts:
+        raise ValueError(f"{name} must be a tensor [{p.num_experts}, rows, channels]")
+    return w.shape[1], w.shape[2]
+
+
+def ep_expert_gemm(p: ep_problem, a, a_scales, w, w_scales, tokens_per_expert, y, dev_status=None,
+                   stream=None) -> None:
+    """y[row] = a[row] @ w[e].T over the rows tokens_per_expert names: e4m3 codes a [rows, K] (uint8) and
+    w [E, N, K] (uint8) with fp32 scales for 1 x 128 and 128 x 128 blocks, y [rows, N] bf16."""
+    N, K = _expert_shape(p, w, "w")
+    E, rows, u8, f32 = p.num_experts, p.num_experts * p.num_tokens, torch.uint8, torch.float32
+    return _call("ep_expert_gemm", _lib.ep_expert_gemm, (
+        ctypes.byref(p), N, K, _ptr(a, u8, "a", rows * K), _ptr(a_scales, f32, "a_scales", rows * (K // 128)),
+        _ptr(w, u8, "w"), _ptr(w_scales, f32, "w_scales", E * ((N + 127) // 128) * (K // 128)),
+        _ptr(tokens_per_expert, torch.int32, "tokens_per_expert", p.num_ranks * E),
+        _ptr(y, torch.bfloat16, "y", rows * N), _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+def ep_expert_swiglu(p: ep_problem, a, a_scales, w, w_scales, tokens_per_expert, q, q_scales, dev_status=None,
+                     stream=None) -> None:
+    """q, q_scales = FP8 cast of silu(gate) * up, gate and up the products of a's rows with the first and the
+    second half of w [E, 2 I, H]; operands as in ep_expert_gemm, q [rows, I] uint8, q_scales [rows, I / 128]."""
+    N, K = _expert_shape(p, w, "w")
+    if K != p.hidden or N % 2:
+        raise ValueError(f"w must be [E, 2 I, {p.hidden}], got {list(w.shape)}")
+    E, I, rows, u8, f32 = p.num_experts, N // 2, p.num_experts * p.num_tokens, torch.uint8, torch.float32
+    return _call("ep_expert_swiglu", _lib.ep_expert_swiglu, (
+        ctypes.byref(p), I, _ptr(a, u8, "a", rows * K), _ptr(a_scales, f32, "a_scales", rows * (K // 128)),
+        _ptr(w, u8, "w"), _ptr(w_scales, f32, "w_scales", E * (N // 128) * (K // 128)),
+        _ptr(tokens_per_expert, torch.int32, "tokens_per_expert", p.num_ranks * E), _ptr(q, u8, "q", rows * I),
+        _ptr(q_scales, f32, "q_scales", rows * (I // 128)), _ptr(dev_status, torch.int32, "dev_status", 1),
+        _stream(stream)))
 
 
 def ep_selftest_wait_timeout(words, polls: int, dev_status, stream=None) -> None:

@@ -1,5 +1,6 @@
 /*
- * ep.h - MoE expert-parallel dispatch layout, dispatch and combine on one GPU.
+ * ep.h - MoE expert-parallel routing, dispatch layout, dispatch, expert
+ * products and combine on one GPU.
  *
  * The R expert-parallel ranks (and N = R / G nodes of G GPUs) are logical
  * partitions of one GPU's memory.  Token t belongs to source rank
@@ -17,8 +18,8 @@
  *  - EP_ERR_CUDA: a launch failed; nothing more of the call was enqueued.
  *  - ep_last_error_string() describes the last failure on this thread.
  *  - Errors found by the kernels (bad expert id, repeated expert id, slot
- *    out of range, a bounded wait on an asynchronous copy that ran out:
- *    EP_STATUS_TIMEOUT) are OR-ed as EP_STATUS_* bits into *dev_status, an int32
+ *    out of range, NaN logit, a bounded wait that ran out: EP_STATUS_TIMEOUT)
+ *    are OR-ed as EP_STATUS_* bits into *dev_status, an int32
  *    in device memory that the caller zeroes and reads after synchronising
  *    (ep_get_status does both the synchronisation and the read, and
  *    returns EP_ERR_DEVICE when a bit is set).  dev_status may be NULL
@@ -56,10 +57,23 @@ typedef struct ep_problem {
 } ep_problem;
 
 enum { EP_OK = 0, EP_ERR_INVALID_ARG = 1, EP_ERR_CUDA = 2, EP_ERR_DEVICE = 3 };
-enum { EP_STATUS_BAD_EXPERT = 1, EP_STATUS_DUP_EXPERT = 2, EP_STATUS_BAD_SLOT = 4, EP_STATUS_TIMEOUT = 8 };
+enum { EP_STATUS_BAD_EXPERT = 1, EP_STATUS_DUP_EXPERT = 2, EP_STATUS_BAD_SLOT = 4, EP_STATUS_TIMEOUT = 8,
+       EP_STATUS_BAD_LOGIT = 16 };
 enum { EP_RANK_MAJOR = 0, EP_EXPERT_MAJOR = 1 };
 enum { EP_BF16 = 0, EP_FP8_E4M3 = 1 };
+enum { EP_FP32 = 2 };   /* routing logits only: EP_BF16 or EP_FP32 */
 enum { EP_WIRE_MXFP8 = 1, EP_WIRE_NVFP4 = 2 };
+enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
+
+/* How ep_route turns a token's logits into experts and weights. */
+typedef struct ep_router {
+    int32_t scoring;      /* EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID               */
+    int32_t num_groups;   /* g: experts are g equal consecutive groups; E % g == 0 */
+    int32_t topk_groups;  /* groups kept, 1..g                                  */
+    int32_t group_best;   /* a group's score: sum of its best 1 or 2 keys       */
+    int32_t renormalize;  /* nonzero: divide the weights by their sum           */
+    float scale;          /* factor on the weights, finite                      */
+} ep_router;
 
 /* Text for the last failing call on this thread ("" if none). */
 const char *ep_last_error_string(void);
@@ -372,6 +386,106 @@ int ep_layout_noalloc(const ep_problem *p, const int64_t *topk_idx,
  */
 int ep_selftest_wait_timeout(uint32_t *words, uint32_t polls, int32_t *dev_status,
                              ep_stream_t stream);
+
+/*
+ * ep_route - routing: logits -> topk_idx and topk_weights, as ep_layout,
+ * ep_dispatch and ep_combine read them.  (No counterpart on the pages, which
+ * draw the routing: an addition of this library.)
+ *
+ * x = logits[t, :] (fp32 or bf16, widened exactly), b = bias (fp32 [E], or
+ * NULL for zero).  All arithmetic is fp32.
+ *   key_e   = x_e + b_e (EP_SCORE_SOFTMAX) or 1 / (1 + exp(-x_e)) + b_e
+ *             (EP_SCORE_SIGMOID).  The bias moves the choice, never a weight.
+ *   Expert e is eligible if x_e and key_e are neither NaN nor -inf.  (A logit
+ *   of -inf takes an expert out; a row of them is a padding token.)  A NaN
+ *   logit or bias raises EP_STATUS_BAD_LOGIT.  A logit of +inf counts as the
+ *   largest finite number in a softmax.
+ *   Groups (num_groups > 1): a group's score is the sum of its best
+ *   group_best eligible keys; the topk_groups best groups stay, and a group
+ *   without an eligible expert never does.
+ *   topk_idx[t, :] = the k eligible experts with the largest keys, largest
+ *   first.  Every tie, between experts or groups, goes to the lowest index.
+ *   Entries beyond the eligible experts are -1 with weight 0.
+ *   s_e     = exp(x_e) / sum of exp(x_i) over the i of every group whose logit
+ *             is neither NaN nor -inf (softmax), or 1 / (1 + exp(-x_e)).
+ *   topk_weights[t, j] = scale * s_e, divided by the sum of the chosen s if
+ *   renormalize (0 if that sum is 0).
+ * logits: row t at logits + t * logits_row_stride elements (>= E), dtype
+ * EP_FP32 or EP_BF16.  topk_idx [T, k] int64, topk_weights [T, k] fp32.
+ * One kernel; identical outputs on every run.
+ */
+int ep_route(const ep_problem *p, const ep_router *r, int dtype, const void *logits, int64_t logits_row_stride,
+             const float *bias, int64_t *topk_idx, float *topk_weights, int32_t *dev_status, ep_stream_t stream);
+
+/*
+ * ep_route_backward - gradient of ep_route's weights with respect to its
+ * logits; the choice of experts is a constant (and the bias has no gradient).
+ *
+ * With s as above, c = scale, g_j = grad_weights[t, j] of the kept entries
+ * e_j (ids and repeats as in ep_layout; -1 is no entry) and S = sum_j s_j:
+ *   ds_j = c g_j, or c (g_j - sum_i g_i s_i / S) / S if renormalize (0 if
+ *   S = 0);
+ *   softmax: grad_logits_e = s_e (ds_e - sum_j ds_j s_j), ds_e = 0 for an
+ *   expert that was not chosen;   sigmoid: grad_logits_e = ds_e s_e (1 - s_e).
+ * An expert whose logit is NaN or -inf has gradient 0.  The scores are
+ * computed again from the logits.  grad_logits has the logits' dtype, rounded
+ * once, and its own row stride; all E entries of every row are written.
+ */
+int ep_route_backward(const ep_problem *p, const ep_router *r, int dtype, const void *logits,
+                      int64_t logits_row_stride, const int64_t *topk_idx, const float *grad_weights,
+                      void *grad_logits, int64_t grad_row_stride, int32_t *dev_status, ep_stream_t stream);
+
+/*
+ * ep_combine_backward - gradients of ep_combine (same layout, same handle).
+ *
+ * grad_out [T, H] bf16 is the gradient of out.  For every row the handle
+ * names, with entries j of token t reading it (one entry, or in EP_RANK_MAJOR
+ * all of the rank's):
+ *   grad_y[row] = bf16( fp32( (sum_j topk_weights[t, j], in j order) *
+ *   grad_out[t] ) ); rows the handle does not name are not written.
+ *   grad_weights[t, j] = sum_h grad_out[t, h] * y[row, h], fp32, summed in an
+ *   order that depends on H and k only; 0 for entries that are not kept.
+ * grad_y [rows, H] bf16 or NULL, grad_weights [T, k] fp32 or NULL (y may be
+ * NULL then): a NULL output is not computed.  grad_out, y and grad_y 16-byte
+ * aligned; grad_y must not overlap y.
+ */
+int ep_combine_backward(const ep_problem *p, int layout, const uint16_t *grad_out, const uint16_t *y,
+                        const int64_t *topk_idx, const float *topk_weights, const int32_t *rank_slot,
+                        const int32_t *expert_slot, uint16_t *grad_y, float *grad_weights, int32_t *dev_status,
+                        ep_stream_t stream);
+
+/*
+ * Expert products over the expert-major receive buffer, FP8 operands with a
+ * scale for each block of 128.
+ *
+ * Expert e's rows are (e * R + src) * Tr + i for i < tokens_per_expert[src, e]
+ * (ep_layout's output): exactly the rows an expert-major dispatch wrote.  No
+ * other row is read, and none is written.  A count outside [0, Tr] raises
+ * EP_STATUS_BAD_SLOT and is clamped.
+ *   a [rows, K] e4m3 codes, a_scales [rows, K / 128] fp32 (the format
+ *   ep_dispatch writes); w [E, N, K] e4m3 codes, w_scales
+ *   [E, ceil(N / 128), K / 128] fp32, one scale for each 128 x 128 block.
+ *   c[row, n] = sum over blocks b of a_scales[row, b] * w_scales[e, n / 128, b]
+ *               * (sum of a[row, i] * w[e, n, i] over the 128 channels i of b),
+ *   fp32 accumulation throughout.
+ *
+ * ep_expert_gemm: y [rows, N] bf16 = c, rounded once (the down product; with
+ *   the transposed matrix, also the gradient of a product's input).
+ *   K % 128 == 0, N % 8 == 0, N >= 8.
+ * ep_expert_swiglu: w [E, 2 I, K], gate rows 0 .. I-1 and up rows I .. 2I-1,
+ *   w_scales [E, 2 I / 128, K / 128], K = p->hidden;
+ *   h = gate / (1 + exp(-gate)) * up in fp32, then cast as ep_dispatch casts:
+ *   per row and 128 channels q = e4m3(h * inv), scale = amax / 448, ready to
+ *   be the a of ep_expert_gemm.  q [rows, I] e4m3, q_scales [rows, I / 128].
+ *   H % 128 == 0, I % 128 == 0.
+ * a, w, y and q 16-byte aligned; E * T < 2^31.
+ */
+int ep_expert_gemm(const ep_problem *p, int64_t out_features, int64_t in_features, const uint8_t *a,
+                   const float *a_scales, const uint8_t *w, const float *w_scales,
+                   const int32_t *tokens_per_expert, uint16_t *y, int32_t *dev_status, ep_stream_t stream);
+int ep_expert_swiglu(const ep_problem *p, int64_t intermediate, const uint8_t *a, const float *a_scales,
+                     const uint8_t *w, const float *w_scales, const int32_t *tokens_per_expert, uint8_t *q,
+                     float *q_scales, int32_t *dev_status, ep_stream_t stream);
 
 #ifdef __cplusplus
 }
