@@ -610,6 +610,9 @@ int prepare_expert(const ep_problem *p, int64_t N, int64_t K, const uint8_t *act
     if (N < 8 || N % 8 || N > (1 << 24))
         return fail(EP_ERR_INVALID_ARG, "out_features must be a multiple of 8, at most 2^24");
     if (d.T > 0 && d.E > INT32_MAX / d.T) return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens exceeds int32");
+    // tiles of 128 rows x 128 columns are counted in 32 bits
+    if (d.E * d.T / 128 + d.E > INT32_MAX / ((N + 127) / 128))
+        return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens * out_features exceeds 2^45");
     if (d.T > 0) {
         if (!act || !aligned(act, 16) || !w || !aligned(w, 16))
             return fail(EP_ERR_INVALID_ARG, "a / w NULL or not 16-byte aligned");
