@@ -29,25 +29,29 @@ namespace {
 constexpr int kBlock = 128;                     // channels, and matrix rows, of a scale; rows of a tile
 constexpr int kOperand = kBlock * kBlock;       // bytes of 128 rows x 128 channels
 constexpr int kExpertThreads = 384;             // warpgroup 0: copies and products; 1, 2: accumulation
-constexpr int kIssueRegs = 56, kAccRegs = 224;  // 56 + 2 * 224 = 3 * 168, the launch's registers
-constexpr int kLdBufs = 2;
+constexpr int kIssueRegs = 88, kAccRegs = 208;  // 88 + 2 * 208 = 3 * 168, the launch's registers
 constexpr int kTmemCols = 512;
 
 constexpr int kStages = 6;                      // operand buffers: 192 KB
+constexpr int kCopyWarps = 2;                   // warps that copy rows
+constexpr int kAhead = 4;                       // steps whose row copies are in flight
+static_assert(kAhead < kStages, "a buffer is waited for only after the step that empties it was announced");
+// Steps whose scales are kept.  The copies of a step wait until the products
+// kStages steps before are done, which waited for the accumulation two steps
+// before those: its scales may be overwritten from kStages + 2 steps on.
+constexpr int kScaleRing = 16;
+static_assert(kScaleRing > kStages + 2, "");
 constexpr int kPairRows = 2 * kBlock;           // rows of a pair's tile
-
-struct ExpertMaps {
-    CUtensorMap a[8];     // the rows, in boxes of 2^i rows
-    CUtensorMap w;        // the matrices, in boxes of 128 rows
-};
 
 struct ExpertShared {
     unsigned char buf[kStages][2 * kOperand];              // rows, then matrix rows
     uint64_t full[kStages], empty[kStages];                // operand buffers
     uint64_t tfull[2], tempty[2];                          // accumulators
     uint64_t joined;                                       // maxima of a unit are written
+    uint64_t sfull[kScaleRing];                            // scales of a step
+    float row_scale[kScaleRing][kBlock], w_scale[kScaleRing][2];
+    uint32_t off[kBlock];                                  // the rows' offsets in blocks of 128 channels
     float amax[2][2][kBlock];                              // [unit parity][warpgroup][row]
-    int2 box[kBlock];                                      // copies of a tile: first row; place and log2 height
     int first[kMaxExperts + 1];                            // row tiles of the experts before
     int rows[kMaxExperts];
     uint32_t tmem;
@@ -79,82 +83,39 @@ __device__ __forceinline__ Unit find_unit(const ExpertShared &s, int E, int col_
     return v;
 }
 
-// Lists the copies that bring rows [m0, m0 + n) of expert e (n <= 128) into a
-// tile; returns their number.  Called by a whole warp.
-__device__ __forceinline__ int list_boxes(ExpertShared &s, const ExpertArgs &a, int e, int m0, int n) {
+// Receive rows of rows m[] of expert e, for each lane (called by whole warps;
+// counts outside [0, Tr] are clamped).
+template <int N>
+__device__ __forceinline__ void receive_rows(const ExpertArgs &a, int e, const int (&m)[N], int (&row)[N]) {
     const Dims &d = a.d;
     const int lane = threadIdx.x & 31, R = (int)d.R, Tr = (int)d.Tr;
-    int before = 0, boxes = 0;
-    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = e * R * Tr + m[i];
+    int before = 0;
     for (int r0 = 0; r0 < R; r0 += 32) {
         const int r = r0 + lane;
-        const int c = r < R ? min(max(a.tokens_per_expert[(int64_t)r * d.E + e], 0), Tr) : 0;
-        int end = c;
+        int end = r < R ? min(max(a.tokens_per_expert[(int64_t)r * d.E + e], 0), Tr) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(kFull, end, o);
             if (lane >= o) end += v;
         }
-        end += before;
+        end += before;                // rows up to and with source r
+        const int last = min(32, R - r0);
+        for (int i = 0; i < last; ++i) {
+            const int to = __shfl_sync(kFull, end, i);
+            const int start = (e * R + r0 + i + 1) * Tr - to;   // of the next source's segment, less the rows before
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                if (to <= m[x]) row[x] = start + m[x];
+        }
         before = __shfl_sync(kFull, end, 31);
-        const int lo = max(end - c, m0), hi = min(end, m0 + n);
-        const int len = max(hi - lo, 0);
-        int at = __popc(len);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFull, at, o);
-            if (lane >= o) at += v;
-        }
-        const int last = __shfl_sync(kFull, at, 31);
-        at += boxes - __popc(len);
-        boxes += last;
-        int row = (e * R + r) * Tr + lo - (end - c), place = lo - m0;
-        for (int left = len; left;) {
-            const int lg = 31 - __clz(left);
-            s.box[at++] = make_int2(row, place | lg << 8);
-            row += 1 << lg;
-            place += 1 << lg;
-            left -= 1 << lg;
-        }
     }
-    __syncwarp();
-    return boxes;
-}
-
-// Receive row of each lane's m-th row of expert e (called by whole warps;
-// counts outside [0, Tr] are clamped).
-__device__ __forceinline__ int receive_row(const ExpertArgs &a, int e, int m) {
-    const Dims &d = a.d;
-    const int lane = threadIdx.x & 31, R = (int)d.R, Tr = (int)d.Tr;
-    int c[2], before = 0;
-    int src = 0, start = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h * 32 >= R) break;
-        const int r = h * 32 + lane;
-        c[h] = r < R ? min(max(a.tokens_per_expert[(int64_t)r * d.E + e], 0), Tr) : 0;
-        int sum = c[h];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFull, sum, o);
-            if (lane >= o) sum += v;
-        }
-        sum += before;                // rows up to and with source r
-        for (int i = 0; i < min(32, R - h * 32); ++i) {
-            const int end = __shfl_sync(kFull, sum, i);
-            if (end <= m) {
-                src = h * 32 + i + 1;
-                start = end;
-            }
-        }
-        before = __shfl_sync(kFull, sum, 31);
-    }
-    return (e * R + src) * Tr + (m - start);
 }
 
 template <bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
-    expert_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ ExpertMaps maps) {
+    expert_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ unsigned char raw[];
     ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
     constexpr int S = kStages, NB = 2;
@@ -182,7 +143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     if (bad && blockIdx.x == 0) raise_status(a.dev_status, EP_STATUS_BAD_SLOT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&s.full[i], 1);      // the first CTA's counts both CTAs' bytes
+            mbar_init(&s.full[i], 1 + 2 * kCopyWarps);   // the first CTA's: both CTAs' matrix bytes and copying warps
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -190,6 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             mbar_init(&s.tempty[i], 16);   // the first CTA's: the accumulating warps of both
         }
         mbar_init(&s.joined, 8);
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(&s.sfull[i], kCopyWarps);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -226,42 +188,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0) {
-            // ---- copies ----
-            int it = 0;
-            bool ok = true;
-            for (int u = first_unit; u < units && ok; u += step) {
-                const Unit v = find_unit(s, E, col_tiles, u);
-                const int m = v.m0 + rank * kBlock, n = min(max(v.rows - rank * kBlock, 0), kBlock);
-                const int boxes = list_boxes(s, a, v.e, m, n);
-                const int w_row = SWIGLU ? v.nb * kBlock + rank * n_cols : v.nb * tile_cols + rank * kBlock;
-                const uint32_t bytes = v.rows * kBlock + 2 * kOperand;   // of both CTAs
-                for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                    const int st = it % S;
-                    ok = mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort);
-                    if (!__all_sync(kFull, ok)) { ok = false; break; }
-                    unsigned char *buf = s.buf[st];
-                    const uint32_t bar = cluster_addr(&s.full[st], 0);
-                    if (lane == 0) {
-                        if (rank == 0) mbar_expect_tx(&s.full[st], bytes);
-                        tma_load_3d(buf + kOperand, &maps.w, kb * kBlock, w_row, v.e, bar);
+            // ---- matrix rows ----
+            if (lane == 0) {
+                int it = 0;
+                bool ok = true;
+                for (int u = first_unit; u < units && ok; u += step) {
+                    const Unit v = find_unit(s, E, col_tiles, u);
+                    const int w_row = SWIGLU ? v.nb * kBlock + rank * n_cols : v.nb * tile_cols + rank * kBlock;
+                    for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                        const int st = it % S;
+                        ok = mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort);
+                        if (!ok) break;
+                        if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kOperand);
+                        tma_load_3d(s.buf[st] + kOperand, &map_w, kb * kBlock, w_row, v.e, cluster_addr(&s.full[st], 0));
                     }
-                    for (int b = lane; b < boxes; b += 32) {
-                        const int2 x = s.box[b];
-                        tma_load_2d(buf + (x.y & 255) * kBlock, &maps.a[x.y >> 8], kb * kBlock, x.x, bar);
+                }
+                // No copy may land after the pair has left.  Only where something gave up is one still in flight
+                // then: the first CTA's barriers count all of them; the second gives its own a millisecond.
+                if (!ok) {
+                    if (rank == 0) {
+                        for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
+                    } else {
+                        const long long t0 = clock64();
+                        while (clock64() - t0 < (1 << 21)) {}
                     }
-                    __syncwarp();
                 }
             }
-            // No copy may land after the pair has left.  Only where something gave up is one still in flight then:
-            // the first CTA's barriers count all of them; the second gives its own a millisecond.
-            if (!ok) {
-                if (rank == 0) {
-                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
-                } else {
-                    const long long t0 = clock64();
-                    while (clock64() - t0 < (1 << 21)) {}
-                }
-            }
+            __syncwarp();
         } else if (warp == 1 && rank == 0) {
             // ---- products ----
             if (lane == 0) {
@@ -286,6 +239,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 if (!ok && it > 0) mbar_wait_bounded(&s.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1);
             }
             __syncwarp();
+        } else if (warp >= 4 - kCopyWarps) {
+            // ---- rows and scales: eight lanes copy a row's 128 bytes, a warp every other four rows ----
+            constexpr int kStep = kCopyWarps * 4, kMine = kBlock / kStep;
+            const int part = (warp - (4 - kCopyWarps)) * 4 + (lane >> 3), piece = lane & 7;
+            const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
+            int it = 0;
+            bool ok = true;
+            auto landed = [&](int i) {     // this thread's copies of step i are in shared memory
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s.sfull[i % kScaleRing]);
+                    mbar_arrive_cluster(cluster_addr(&s.full[i % S], 0));
+                }
+            };
+            for (int u = first_unit; u < units && ok; u += step) {
+                const Unit v = find_unit(s, E, col_tiles, u);
+                const int n = min(max(v.rows - rank * kBlock, 0), kBlock);
+                // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
+                int row[kMine];
+                {
+                    int m[kMine];
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) m[i] = v.m0 + rank * kBlock + i * kStep + part;
+                    receive_rows(a, v.e, m, row);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    row[i] *= kb_n;
+                    if (piece == 0) s.off[i * kStep + part] = row[i];
+                }
+                __syncwarp();
+                // scales: lane l has the warp's rows of places l and l + 32
+                const int place = (lane >> 2) * kStep + part - (lane >> 3) + (lane & 3);
+                static_assert(kMine == 16, "64 rows a warp");
+                const uint32_t sc0 = s.off[place], sc1 = s.off[place + 8 * kStep];
+                const int blk = SWIGLU ? v.nb : v.nb * NB;
+                uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
+                if (lane == 1) ws += SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;   // (zeros beyond N)
+                for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                    const int st = it % S, ring = it % kScaleRing;
+                    ok = __all_sync(kFull, mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort));
+                    if (!ok) break;
+                    const uint32_t dst = smem_addr(s.buf[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
+                    const uint8_t *src = a.a + kb * kBlock + piece * 16;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i)
+                        if (i * kStep < n - part)
+                            cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)row[i] * kBlock);
+                    const uint32_t sdst = smem_addr(&s.row_scale[ring][place]);
+                    if (place < n) cp_async4(sdst, a.a_scales + (sc0 + kb));
+                    if (place + 8 * kStep < n) cp_async4(sdst + 8 * kStep * 4, a.a_scales + (sc1 + kb));
+                    if (warp == 3 && lane < 2) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
+                    cp_async_commit();
+                    if (it >= kAhead) {
+                        cp_async_wait<kAhead>();
+                        landed(it - kAhead);
+                    }
+                }
+            }
+            cp_async_wait<0>();
+            for (int i = max(it - kAhead, 0); i < it; ++i) landed(i);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAccRegs));
@@ -293,7 +309,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         const int half = (warp - 4) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + half * 64;
-        const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
         int it = 0, unit = 0;
         bool ok = true;
         uint32_t tempty[2];
@@ -303,69 +318,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             const Unit v = find_unit(s, E, col_tiles, u);
             const bool some = rank * kBlock + quarter * 32 < v.rows;     // rows in this warp's lanes
             const bool live = rank * kBlock + r < v.rows;
-            const int row = receive_row(a, v.e, v.m0 + min(rank * kBlock + r, v.rows - 1));
-            // offsets of the row's and of the first block's scales (below 2^32: an operand in memory has 128 bytes a
-            // scale); to the second block's: none beyond N, where the products are zeros and not stored
-            const uint32_t as = (uint32_t)row * kb_n;
-            const int blk = SWIGLU ? v.nb : v.nb * NB;
-            const uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
-            const uint32_t ws2 = SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;
+            const int m[1] = {v.m0 + min(rank * kBlock + r, v.rows - 1)};
+            int rows[1];
+            receive_rows(a, v.e, m, rows);
+            const int row = rows[0];
             uint64_t acc[NB][32];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) acc[b][c] = 0;
-            // scales of the next two blocks are on their way while two blocks are accumulated
-            float sa_n[2], sw_n[NB][2];
-            auto load_scales = [&](int kb0) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int kb = min(kb0 + j, kb_n - 1);
-                    sa_n[j] = a.a_scales[as + kb];
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) sw_n[b][j] = a.w_scales[ws + b * ws2 + kb];
-                }
-            };
-            load_scales(0);
-            for (int kb0 = 0; kb0 < kb_n && ok; kb0 += 2) {
-                float sc[NB][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) sc[b][j] = sa_n[j] * sw_n[b][j];
-                load_scales(kb0 + 2);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (kb0 + j >= kb_n) break;
-                    const int p = it & 1;
-                    ok = mbar_wait_or_abort(&s.tfull[p], (it >> 1) & 1, abort);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    ++it;
-                    if (!some) {
-                        if (lane == 0) mbar_arrive_cluster(tempty[p]);
-                        continue;
-                    }
+            for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                const int p = it & 1, ring = it % kScaleRing;
+                ok = mbar_wait_or_abort(&s.sfull[ring], (it / kScaleRing) & 1, abort) &&
+                     mbar_wait_or_abort(&s.tfull[p], (it >> 1) & 1, abort);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                if (some) {
                     tmem_fence_after();
-                    constexpr int LB = kLdBufs;
-                    uint32_t t[LB][32];
+                    const float sr = s.row_scale[ring][r];
+                    const float2 sw = *reinterpret_cast<const float2 *>(s.w_scale[ring]);
+                    const float sc[2] = {sr * sw.x, sr * sw.y};
+                    // 64 columns at a time: the second block's loads wait only for the registers
+                    uint32_t t[2][32];
                     const uint32_t at = tm + p * 256;
-                    if (LB == 2) tmem_ld32(at, t[0]);
+                    tmem_ld32(at, t[0]);
+                    tmem_ld32(at + 32, t[1]);
+                    tmem_wait_ld(t[0], t[1]);
 #pragma unroll
-                    for (int q = 0; q < 2 * NB; ++q) {
-                        if (LB == 1) tmem_ld32(at + (q >> 1) * kBlock + (q & 1) * 32, t[0]);
-                        tmem_wait_ld(t[q % LB]);
-                        if (q + 1 == 2 * NB) {
-                            tmem_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(tempty[p]);
-                        } else if (LB == 2) {
-                            tmem_ld32(at + ((q + 1) >> 1) * kBlock + ((q + 1) & 1) * 32, t[(q + 1) % LB]);
-                        }
+                    for (int q = 0; q < 2; ++q) {
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
-                            fma2(acc[q >> 1][(q & 1) * 16 + c], t[q % LB][2 * c], t[q % LB][2 * c + 1], sc[q >> 1][j]);
+                            fma2(acc[0][q * 16 + c], t[q][2 * c], t[q][2 * c + 1], sc[0]);
+                        tmem_ld32(at + kBlock + q * 32, t[q]);
                     }
+                    tmem_wait_ld(t[0], t[1]);
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(tempty[p]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            fma2(acc[1][q * 16 + c], t[q][2 * c], t[q][2 * c + 1], sc[1]);
+                } else if (lane == 0) {
+                    mbar_arrive_cluster(tempty[p]);
                 }
             }
             if (!ok) break;
@@ -435,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
 }
 
 template <bool SWIGLU>
-cudaError_t launch(const ExpertArgs &a, const ExpertMaps &maps, cudaStream_t st) {
+cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t st) {
     constexpr int bytes = sizeof(ExpertShared) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
@@ -449,24 +445,19 @@ cudaError_t launch(const ExpertArgs &a, const ExpertMaps &maps, cudaStream_t st)
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
-    expert_kernel<SWIGLU><<<num_sms() & ~1, kExpertThreads, bytes, st>>>(a, maps);
+    expert_kernel<SWIGLU><<<num_sms() & ~1, kExpertThreads, bytes, st>>>(a, map_w);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st) {
-    ExpertMaps maps;
-    const cuuint64_t da[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.d.E * a.d.T)}, sa[1] = {(cuuint64_t)a.K};
-    for (int i = 0; i < 8; ++i) {
-        const cuuint32_t box[2] = {kBlock, 1u << i};
-        if (cudaError_t e = encode_map(&maps.a[i], 2, a.a, da, sa, box)) return e;
-    }
+    CUtensorMap map_w;
     const cuuint64_t dw[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.d.E};
     const cuuint64_t sw[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.N * a.K)};
     const cuuint32_t bw[3] = {kBlock, kBlock, 1};
-    if (cudaError_t e = encode_map(&maps.w, 3, a.w, dw, sw, bw)) return e;
-    return a.q ? launch<true>(a, maps, st) : launch<false>(a, maps, st);
+    if (cudaError_t e = encode_map(&map_w, 3, a.w, dw, sw, bw)) return e;
+    return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
 }
 
 }  // namespace ep
