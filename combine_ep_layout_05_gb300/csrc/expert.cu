@@ -4,21 +4,18 @@
 //
 //   c[row, n] = sum_b as[row, b] ws[n / 128, b] sum_{i in b} a[row, i] w[n, i]
 //
-// The inner sums are tensor-core products of 256 rows x 256 matrix rows x 128
-// channels on a CTA pair, into tensor memory; the scales are plain fp32
-// numbers (not powers of two), so every block's product is taken out of
-// tensor memory and added, times its scale, to fp32 registers.  Two
-// accumulators in tensor memory alternate: one is filled while the other is
-// taken out.
+// The inner sums are tensor-core products of 128 rows x 128 NB matrix rows x
+// 128 channels into tensor memory; the scales are plain fp32 numbers (not
+// powers of two), so every block's product is taken out of tensor memory and
+// added, times its scale, to fp32 registers.  Two accumulators in tensor
+// memory alternate: one is filled while the other is taken out.
 //
-// A persistent pair walks (expert, row tile, column tile) triples; each CTA
-// holds 128 of the tile's rows and 128 of its matrix rows.  An expert's rows
-// lie in R segments: the part of a segment that falls in the tile is copied
-// in boxes of 128, 64, .. 1 rows (one box where the segment covers the tile).
-// Warp 0 issues the copies, warp 1 of the first CTA the products, eight warps
-// of each CTA (two warpgroups, one for each half of the columns) scale,
-// accumulate and store; a thread owns a row, so its scale is one number a
-// block.
+// A persistent CTA walks (expert, row tile, column tile) triples.  Its warps:
+// warp 0 copies boxes of 128 matrix rows (TMA), warp 1 issues the products,
+// warps 4-7 copy the rows, which lie in R segments of any length, with 16-byte
+// asynchronous copies in the swizzle that the products expect, and the
+// scales; eight warps (two warpgroups, one for each half of the columns)
+// scale, accumulate and store: a thread owns a row.
 #include "tcgen05.cuh"
 #include "vec8.cuh"
 
@@ -28,29 +25,25 @@ namespace {
 
 constexpr int kBlock = 128;                     // channels, and matrix rows, of a scale; rows of a tile
 constexpr int kOperand = kBlock * kBlock;       // bytes of 128 rows x 128 channels
-constexpr int kExpertThreads = 384;             // warpgroup 0: copies and products; 1, 2: accumulation
-constexpr int kIssueRegs = 88, kAccRegs = 208;  // 88 + 2 * 208 = 3 * 168, the launch's registers
+constexpr int kExpertThreads = 512;             // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
+constexpr int kIssueRegs = 40, kCopyRegs = 40, kAccRegs = 216;   // 40 + 40 + 2 * 216 = 4 * 128, the launch's registers
 constexpr int kTmemCols = 512;
-
-constexpr int kStages = 6;                      // operand buffers: 192 KB
-constexpr int kCopyWarps = 2;                   // warps that copy rows
-constexpr int kAhead = 4;                       // steps whose row copies are in flight
-static_assert(kAhead < kStages, "a buffer is waited for only after the step that empties it was announced");
+template <int NB>
+constexpr int kStages = NB == 2 ? 4 : 6;        // operand buffers: 192 KB
+constexpr int kCopyWarps = 4;                   // warps that copy rows
 // Steps whose scales are kept.  The copies of a step wait until the products
 // kStages steps before are done, which waited for the accumulation two steps
 // before those: its scales may be overwritten from kStages + 2 steps on.
 constexpr int kScaleRing = 16;
-static_assert(kScaleRing > kStages + 2, "");
-constexpr int kPairRows = 2 * kBlock;           // rows of a pair's tile
 
+template <int NB>
 struct ExpertShared {
-    unsigned char buf[kStages][2 * kOperand];              // rows, then matrix rows
-    uint64_t full[kStages], empty[kStages];                // operand buffers
+    unsigned char buf[kStages<NB>][(1 + NB) * kOperand];   // rows, then matrix rows
+    uint64_t full[kStages<NB>], empty[kStages<NB>];        // operand buffers
     uint64_t tfull[2], tempty[2];                          // accumulators
     uint64_t joined;                                       // maxima of a unit are written
     uint64_t sfull[kScaleRing];                            // scales of a step
     float row_scale[kScaleRing][kBlock], w_scale[kScaleRing][2];
-    uint32_t off[kBlock];                                  // the rows' offsets in blocks of 128 channels
     float amax[2][2][kBlock];                              // [unit parity][warpgroup][row]
     int first[kMaxExperts + 1];                            // row tiles of the experts before
     int rows[kMaxExperts];
@@ -58,14 +51,15 @@ struct ExpertShared {
     int abort;
 };
 
-// One unit of work: the pair's tile
+// One unit of work
 struct Unit {
     int e, m0;        // expert and its first row
-    int rows;         // rows from m0 on (at most 256)
+    int rows;         // rows from m0 on (at most 128)
     int nb;           // column tile
 };
 
-__device__ __forceinline__ Unit find_unit(const ExpertShared &s, int E, int col_tiles, int u) {
+template <int NB>
+__device__ __forceinline__ Unit find_unit(const ExpertShared<NB> &s, int E, int col_tiles, int u) {
     // the last e with first[e] * col_tiles <= u (experts without rows share their successor's first tile)
     int lo = 0, hi = E;
     while (hi - lo > 1) {
@@ -78,8 +72,8 @@ __device__ __forceinline__ Unit find_unit(const ExpertShared &s, int E, int col_
     Unit v;
     v.e = lo;
     v.nb = r / tiles;                 // row tiles fastest: they share the matrix rows
-    v.m0 = (r % tiles) * kPairRows;
-    v.rows = min(kPairRows, s.rows[lo] - v.m0);
+    v.m0 = (r % tiles) * kBlock;
+    v.rows = min(kBlock, s.rows[lo] - v.m0);
     return v;
 }
 
@@ -113,20 +107,19 @@ __device__ __forceinline__ void receive_rows(const ExpertArgs &a, int e, const i
     }
 }
 
-template <bool SWIGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
+template <bool SWIGLU, int NB>
+__global__ void __launch_bounds__(kExpertThreads, 1)
     expert_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ unsigned char raw[];
-    ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
-    constexpr int S = kStages, NB = 2;
+    ExpertShared<NB> &s = *reinterpret_cast<ExpertShared<NB> *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    constexpr int S = kStages<NB>;
+    static_assert(kScaleRing > S + 2, "scales are still in use when they are overwritten");
     const Dims &d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = (int)d.E;
-    const int rank = (int)cluster_rank();                           // place in the pair
     const int kb_n = (int)(a.K / kBlock);
     const int n_cols = (int)(SWIGLU ? a.N / 2 : a.N);               // output columns
     const int tile_cols = SWIGLU ? kBlock : NB * kBlock;
     const int col_tiles = (n_cols + tile_cols - 1) / tile_cols;
-    const int first_unit = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     // rows of every expert
     bool bad = false;
@@ -143,29 +136,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     if (bad && blockIdx.x == 0) raise_status(a.dev_status, EP_STATUS_BAD_SLOT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&s.full[i], 1 + 2 * kCopyWarps);   // the first CTA's: both CTAs' matrix bytes and copying warps
+            mbar_init(&s.full[i], 1 + kCopyWarps * 32);   // the boxes' bytes and the copying threads
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 16);   // the first CTA's: the accumulating warps of both
+            mbar_init(&s.tempty[i], 8);
         }
         mbar_init(&s.joined, 8);
-        for (int i = 0; i < kScaleRing; ++i) mbar_init(&s.sfull[i], kCopyWarps);
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(&s.sfull[i], kCopyWarps * 32);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
                      "n"(kTmemCols)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     __syncthreads();
     if (warp == 0) {   // tiles of the experts before each
         int sum = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
-            const int t = e0 + lane < E ? (s.rows[e0 + lane] + kPairRows - 1) / kPairRows : 0;
+            const int t = e0 + lane < E ? (s.rows[e0 + lane] + kBlock - 1) / kBlock : 0;
             int inc = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -179,7 +172,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();    // the other CTA's barriers are there too
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
     const int units = s.first[E] * col_tiles;   // below 2^31: checked on the host
@@ -192,42 +184,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             if (lane == 0) {
                 int it = 0;
                 bool ok = true;
-                for (int u = first_unit; u < units && ok; u += step) {
+                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                     const Unit v = find_unit(s, E, col_tiles, u);
-                    const int w_row = SWIGLU ? v.nb * kBlock + rank * n_cols : v.nb * tile_cols + rank * kBlock;
+                    const int w_row = v.nb * tile_cols;
                     for (int kb = 0; kb < kb_n; ++kb, ++it) {
                         const int st = it % S;
                         ok = mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort);
                         if (!ok) break;
-                        if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kOperand);
-                        tma_load_3d(s.buf[st] + kOperand, &map_w, kb * kBlock, w_row, v.e, cluster_addr(&s.full[st], 0));
+                        mbar_expect_tx(&s.full[st], NB * kOperand);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            tma_load_3d(s.buf[st] + (1 + b) * kOperand, &map_w, kb * kBlock,
+                                        w_row + b * (SWIGLU ? n_cols : kBlock), v.e, &s.full[st]);
                     }
                 }
-                // No copy may land after the pair has left.  Only where something gave up is one still in flight
-                // then: the first CTA's barriers count all of them; the second gives its own a millisecond.
-                if (!ok) {
-                    if (rank == 0) {
-                        for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
-                    } else {
-                        const long long t0 = clock64();
-                        while (clock64() - t0 < (1 << 21)) {}
-                    }
-                }
+                // no copy may land after the CTA has left (only where something gave up is one still in flight)
+                if (!ok)
+                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
             }
             __syncwarp();
-        } else if (warp == 1 && rank == 0) {
+        } else if (warp == 1) {
             // ---- products ----
             if (lane == 0) {
-                constexpr uint32_t idesc = mma_idesc(kPairRows, NB * kBlock);
+                constexpr uint32_t idesc = mma_idesc(kBlock, NB * kBlock);
                 int it = 0;
                 bool ok = true;
-                for (int u = first_unit; u < units && ok; u += step) {
+                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                     for (int kb = 0; kb < kb_n && ok; ++kb, ++it) {
                         const int st = it % S, acc = it & 1;
                         ok = mbar_wait_or_abort(&s.tempty[acc], ((it >> 1) & 1) ^ 1, abort) &&
                              mbar_wait_or_abort(&s.full[st], (it / S) & 1, abort);
                         if (!ok) break;
                         tmem_fence_after();
+                        fence_async_shared();     // the rows were copied by threads
                         const uint64_t da = smem_desc(s.buf[st]), db = smem_desc(s.buf[st] + kOperand);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 channels a step
@@ -239,86 +228,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 if (!ok && it > 0) mbar_wait_bounded(&s.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1);
             }
             __syncwarp();
-        } else if (warp >= 4 - kCopyWarps) {
-            // ---- rows and scales: eight lanes copy a row's 128 bytes, a warp every other four rows ----
-            constexpr int kStep = kCopyWarps * 4, kMine = kBlock / kStep;
-            const int part = (warp - (4 - kCopyWarps)) * 4 + (lane >> 3), piece = lane & 7;
-            const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
-            int it = 0;
-            bool ok = true;
-            auto landed = [&](int i) {     // this thread's copies of step i are in shared memory
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&s.sfull[i % kScaleRing]);
-                    mbar_arrive_cluster(cluster_addr(&s.full[i % S], 0));
-                }
-            };
-            for (int u = first_unit; u < units && ok; u += step) {
-                const Unit v = find_unit(s, E, col_tiles, u);
-                const int n = min(max(v.rows - rank * kBlock, 0), kBlock);
-                // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
-                int row[kMine];
-                {
-                    int m[kMine];
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) m[i] = v.m0 + rank * kBlock + i * kStep + part;
-                    receive_rows(a, v.e, m, row);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    row[i] *= kb_n;
-                    if (piece == 0) s.off[i * kStep + part] = row[i];
-                }
-                __syncwarp();
-                // scales: lane l has the warp's rows of places l and l + 32
-                const int place = (lane >> 2) * kStep + part - (lane >> 3) + (lane & 3);
-                static_assert(kMine == 16, "64 rows a warp");
-                const uint32_t sc0 = s.off[place], sc1 = s.off[place + 8 * kStep];
-                const int blk = SWIGLU ? v.nb : v.nb * NB;
-                uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
-                if (lane == 1) ws += SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;   // (zeros beyond N)
-                for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                    const int st = it % S, ring = it % kScaleRing;
-                    ok = __all_sync(kFull, mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort));
-                    if (!ok) break;
-                    const uint32_t dst = smem_addr(s.buf[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
-                    const uint8_t *src = a.a + kb * kBlock + piece * 16;
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i)
-                        if (i * kStep < n - part)
-                            cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)row[i] * kBlock);
-                    const uint32_t sdst = smem_addr(&s.row_scale[ring][place]);
-                    if (place < n) cp_async4(sdst, a.a_scales + (sc0 + kb));
-                    if (place + 8 * kStep < n) cp_async4(sdst + 8 * kStep * 4, a.a_scales + (sc1 + kb));
-                    if (warp == 3 && lane < 2) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
-                    cp_async_commit();
-                    if (it >= kAhead) {
-                        cp_async_wait<kAhead>();
-                        landed(it - kAhead);
-                    }
-                }
-            }
-            cp_async_wait<0>();
-            for (int i = max(it - kAhead, 0); i < it; ++i) landed(i);
         }
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        // ---- rows and scales: eight lanes copy a row's 128 bytes, warp w rows 4 w .. 4 w + 3 of every 16 ----
+        constexpr int kStep = kCopyWarps * 4, kMine = kBlock / kStep;
+        static_assert(kMine == 8, "32 rows a warp: one scale a lane");
+        const int part = (warp - 4) * 4 + (lane >> 3), piece = lane & 7;
+        const int place = (lane >> 2) * kStep + (warp - 4) * 4 + (lane & 3);      // the row whose scale this lane copies
+        const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
+        int it = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit v = find_unit(s, E, col_tiles, u);
+            // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
+            int m[kMine + 1], row[kMine + 1];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) m[i] = v.m0 + i * kStep + part;
+            m[kMine] = v.m0 + place;
+            receive_rows(a, v.e, m, row);
+#pragma unroll
+            for (int i = 0; i <= kMine; ++i) row[i] *= kb_n;
+            const int blk = SWIGLU ? v.nb : v.nb * NB;
+            uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
+            if (lane == 1) ws += SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;   // (zeros beyond N)
+            for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                const int st = it % S, ring = it % kScaleRing;
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort));
+                if (!ok) break;
+                const uint32_t dst = smem_addr(s.buf[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
+                const uint8_t *src = a.a + kb * kBlock + piece * 16;
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (i * kStep < v.rows - part)
+                        cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)row[i] * kBlock);
+                if (place < v.rows)
+                    cp_async4(smem_addr(&s.row_scale[ring][place]), a.a_scales + (uint32_t)(row[kMine] + kb));
+                if (warp == 4 && lane < 2) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
+                cp_async_arrive(&s.full[st]);
+                cp_async_arrive(&s.sfull[ring]);
+            }
+        }
+        cp_async_wait_all();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAccRegs));
         // ---- accumulation: thread = row, warpgroup = 64 of each block's 128 columns ----
-        const int half = (warp - 4) >> 2, quarter = warp & 3;
+        const int half = (warp - 8) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + half * 64;
         int it = 0, unit = 0;
         bool ok = true;
-        uint32_t tempty[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) tempty[i] = cluster_addr(&s.tempty[i], 0);
-        for (int u = first_unit; u < units && ok; u += step, ++unit) {
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
             const Unit v = find_unit(s, E, col_tiles, u);
-            const bool some = rank * kBlock + quarter * 32 < v.rows;     // rows in this warp's lanes
-            const bool live = rank * kBlock + r < v.rows;
-            const int m[1] = {v.m0 + min(rank * kBlock + r, v.rows - 1)};
+            const bool some = quarter * 32 < v.rows;     // rows in this warp's lanes
+            const bool live = r < v.rows;
+            const int m[1] = {v.m0 + min(r, v.rows - 1)};
             int rows[1];
             receive_rows(a, v.e, m, rows);
             const int row = rows[0];
@@ -337,31 +301,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                     tmem_fence_after();
                     const float sr = s.row_scale[ring][r];
                     const float2 sw = *reinterpret_cast<const float2 *>(s.w_scale[ring]);
-                    const float sc[2] = {sr * sw.x, sr * sw.y};
-                    // 64 columns at a time: the second block's loads wait only for the registers
-                    uint32_t t[2][32];
-                    const uint32_t at = tm + p * 256;
-                    tmem_ld32(at, t[0]);
-                    tmem_ld32(at + 32, t[1]);
-                    tmem_wait_ld(t[0], t[1]);
+                    const uint32_t s0 = __float_as_uint(sr * sw.x), s1 = __float_as_uint(sr * sw.y);
+                    const uint64_t sc[2] = {pair2(s0, s0), pair2(s1, s1)};
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int b = 0; b < NB; ++b) {
+                        uint32_t t[64];
+                        tmem_ld64(tm + p * 256 + b * kBlock, t);
+                        if (b == NB - 1) {
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s.tempty[p]);
+                        }
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            fma2(acc[0][q * 16 + c], t[q][2 * c], t[q][2 * c + 1], sc[0]);
-                        tmem_ld32(at + kBlock + q * 32, t[q]);
+                        for (int c = 0; c < 32; ++c) fma2(acc[b][c], pair2(t[2 * c], t[2 * c + 1]), sc[b]);
                     }
-                    tmem_wait_ld(t[0], t[1]);
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(tempty[p]);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            fma2(acc[1][q * 16 + c], t[q][2 * c], t[q][2 * c + 1], sc[1]);
                 } else if (lane == 0) {
-                    mbar_arrive_cluster(tempty[p]);
+                    mbar_arrive(&s.tempty[p]);
                 }
             }
             if (!ok) break;
@@ -422,30 +377,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();    // nothing of the other CTA arrives here, or reads from here, any more
     if (warp == 1) {
         tmem_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
     }
     if (threadIdx.x == 0 && s.abort) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, int NB>
 cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t st) {
-    constexpr int bytes = sizeof(ExpertShared) + 1024;
+    constexpr int bytes = sizeof(ExpertShared<NB>) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
     cached_per_device(ready, [&](int) {
-        e = cudaFuncSetAttribute(expert_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(expert_kernel<SWIGLU, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         // the warpgroups' register shares are drawn from what the block was launched with
         cudaFuncAttributes f{};
-        if (!e) e = cudaFuncGetAttributes(&f, expert_kernel<SWIGLU>);
-        if (!e && f.numRegs * 3 < kIssueRegs + 2 * kAccRegs) e = cudaErrorInvalidDeviceFunction;
+        if (!e) e = cudaFuncGetAttributes(&f, expert_kernel<SWIGLU, NB>);
+        if (!e && f.numRegs * 4 < kIssueRegs + kCopyRegs + 2 * kAccRegs) e = cudaErrorInvalidDeviceFunction;
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
-    expert_kernel<SWIGLU><<<num_sms() & ~1, kExpertThreads, bytes, st>>>(a, map_w);
+    expert_kernel<SWIGLU, NB><<<num_sms(), kExpertThreads, bytes, st>>>(a, map_w);
     return cudaGetLastError();
 }
 
@@ -457,7 +411,7 @@ cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st) {
     const cuuint64_t sw[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.N * a.K)};
     const cuuint32_t bw[3] = {kBlock, kBlock, 1};
     if (cudaError_t e = encode_map(&map_w, 3, a.w, dw, sw, bw)) return e;
-    return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
+    return a.q ? launch<true, 2>(a, map_w, st) : launch<false, 2>(a, map_w, st);
 }
 
 }  // namespace ep
