@@ -4,18 +4,23 @@
 //
 //   c[row, n] = sum_b as[row, b] ws[n / 128, b] sum_{i in b} a[row, i] w[n, i]
 //
-// The inner sums are tensor-core products of 128 rows x 128 NB matrix rows x
-// 128 channels into tensor memory; the scales are plain fp32 numbers (not
-// powers of two), so every block's product is taken out of tensor memory and
-// added, times its scale, to fp32 registers.  Two accumulators in tensor
-// memory alternate: one is filled while the other is taken out.
+// The inner sums are tensor-core products of 256 rows x 256 matrix rows x 128
+// channels on a CTA pair, into tensor memory; the scales are plain fp32
+// numbers (not powers of two), so every block's product is taken out of
+// tensor memory and added, times its scale, to fp32 registers.  Two
+// accumulators in tensor memory alternate: one is filled while the other is
+// taken out.  A pair, because shared memory bounds these products: a CTA
+// alone (128 x 256) would write and read 96 KB of it for a block, 768 cycles
+// at 128 bytes each for 512 cycles of products; a CTA of a pair holds half of
+// the matrix rows, 64 KB.
 //
-// A persistent CTA walks (expert, row tile, column tile) triples.  Its warps:
-// warp 0 copies boxes of 128 matrix rows (TMA), warp 1 issues the products,
-// warps 4-7 copy the rows, which lie in R segments of any length, with 16-byte
-// asynchronous copies in the swizzle that the products expect, and the
-// scales; eight warps (two warpgroups, one for each half of the columns)
-// scale, accumulate and store: a thread owns a row.
+// A persistent pair walks (expert, row tile, column tile) triples; each CTA
+// holds 128 of the tile's rows and 128 of its matrix rows.  Warps: warp 0
+// copies boxes of 128 matrix rows (TMA), warp 1 of the first CTA issues the
+// products, warps 4-7 copy the rows, which lie in R segments of any length,
+// with 16-byte asynchronous copies in the swizzle that the products expect,
+// and the scales (warp 2 passes on that they are there); eight warps (two warpgroups, one for each half of the
+// columns) scale, accumulate and store: a thread owns a row.
 #include "tcgen05.cuh"
 #include "vec8.cuh"
 
@@ -28,21 +33,21 @@ constexpr int kOperand = kBlock * kBlock;       // bytes of 128 rows x 128 chann
 constexpr int kExpertThreads = 512;             // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
 constexpr int kIssueRegs = 40, kCopyRegs = 40, kAccRegs = 216;   // 40 + 40 + 2 * 216 = 4 * 128, the launch's registers
 constexpr int kTmemCols = 512;
-template <int NB>
-constexpr int kStages = NB == 2 ? 4 : 6;        // operand buffers: 192 KB
+constexpr int kStages = 6;                      // operand buffers: 192 KB
+constexpr int kPairRows = 2 * kBlock;           // rows of a pair's tile
 constexpr int kCopyWarps = 4;                   // warps that copy rows
 // Steps whose scales are kept.  The copies of a step wait until the products
 // kStages steps before are done, which waited for the accumulation two steps
 // before those: its scales may be overwritten from kStages + 2 steps on.
 constexpr int kScaleRing = 16;
+static_assert(kScaleRing > kStages + 2, "scales are still in use when they are overwritten");
 
-template <int NB>
 struct ExpertShared {
-    unsigned char buf[kStages<NB>][(1 + NB) * kOperand];   // rows, then matrix rows
-    uint64_t full[kStages<NB>], empty[kStages<NB>];        // operand buffers
-    uint64_t tfull[2], tempty[2];                          // accumulators
+    unsigned char buf[kStages][2 * kOperand];              // rows, then matrix rows
+    uint64_t rows_full[kStages], full[kStages];            // this CTA's rows and scales; all operands of both CTAs
+    uint64_t done[kStages];                                // a step's products: its buffers are free, its sums ready
+    uint64_t tempty[2];                                    // accumulators taken out
     uint64_t joined;                                       // maxima of a unit are written
-    uint64_t sfull[kScaleRing];                            // scales of a step
     float row_scale[kScaleRing][kBlock], w_scale[kScaleRing][2];
     float amax[2][2][kBlock];                              // [unit parity][warpgroup][row]
     int first[kMaxExperts + 1];                            // row tiles of the experts before
@@ -54,12 +59,11 @@ struct ExpertShared {
 // One unit of work
 struct Unit {
     int e, m0;        // expert and its first row
-    int rows;         // rows from m0 on (at most 128)
+    int rows;         // rows from m0 on (at most 256)
     int nb;           // column tile
 };
 
-template <int NB>
-__device__ __forceinline__ Unit find_unit(const ExpertShared<NB> &s, int E, int col_tiles, int u) {
+__device__ __forceinline__ Unit find_unit(const ExpertShared &s, int E, int col_tiles, int u) {
     // the last e with first[e] * col_tiles <= u (experts without rows share their successor's first tile)
     int lo = 0, hi = E;
     while (hi - lo > 1) {
@@ -72,8 +76,8 @@ __device__ __forceinline__ Unit find_unit(const ExpertShared<NB> &s, int E, int 
     Unit v;
     v.e = lo;
     v.nb = r / tiles;                 // row tiles fastest: they share the matrix rows
-    v.m0 = (r % tiles) * kBlock;
-    v.rows = min(kBlock, s.rows[lo] - v.m0);
+    v.m0 = (r % tiles) * kPairRows;
+    v.rows = min(kPairRows, s.rows[lo] - v.m0);
     return v;
 }
 
@@ -107,19 +111,20 @@ __device__ __forceinline__ void receive_rows(const ExpertArgs &a, int e, const i
     }
 }
 
-template <bool SWIGLU, int NB>
-__global__ void __launch_bounds__(kExpertThreads, 1)
+template <bool SWIGLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     expert_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ unsigned char raw[];
-    ExpertShared<NB> &s = *reinterpret_cast<ExpertShared<NB> *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
-    constexpr int S = kStages<NB>;
-    static_assert(kScaleRing > S + 2, "scales are still in use when they are overwritten");
+    ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    constexpr int S = kStages, NB = 2;
     const Dims &d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = (int)d.E;
+    const int rank = (int)cluster_rank();                           // place in the pair
     const int kb_n = (int)(a.K / kBlock);
     const int n_cols = (int)(SWIGLU ? a.N / 2 : a.N);               // output columns
     const int tile_cols = SWIGLU ? kBlock : NB * kBlock;
     const int col_tiles = (n_cols + tile_cols - 1) / tile_cols;
+    const int first_unit = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     // rows of every expert
     bool bad = false;
@@ -136,29 +141,26 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     if (bad && blockIdx.x == 0) raise_status(a.dev_status, EP_STATUS_BAD_SLOT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&s.full[i], 1 + kCopyWarps * 32);   // the boxes' bytes and the copying threads
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.rows_full[i], kCopyWarps * 32);
+            mbar_init(&s.full[i], 3);      // (the first CTA's) the bytes of both boxes, word of both CTAs' rows
+            mbar_init(&s.done[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 8);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&s.tempty[i], 16);   // (the first CTA's) the accumulating warps of both
         mbar_init(&s.joined, 8);
-        for (int i = 0; i < kScaleRing; ++i) mbar_init(&s.sfull[i], kCopyWarps * 32);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
                      "n"(kTmemCols)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     __syncthreads();
     if (warp == 0) {   // tiles of the experts before each
         int sum = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
-            const int t = e0 + lane < E ? (s.rows[e0 + lane] + kBlock - 1) / kBlock : 0;
+            const int t = e0 + lane < E ? (s.rows[e0 + lane] + kPairRows - 1) / kPairRows : 0;
             int inc = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -172,6 +174,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();    // the other CTA's barriers are there too
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
     const int units = s.first[E] * col_tiles;   // below 2^31: checked on the host
@@ -182,50 +185,74 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         if (warp == 0) {
             // ---- matrix rows ----
             if (lane == 0) {
-                int it = 0;
+                int st = 0, ph = 1, it = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                for (int u = first_unit; u < units && ok; u += step) {
                     const Unit v = find_unit(s, E, col_tiles, u);
-                    const int w_row = v.nb * tile_cols;
+                    const int w_row = SWIGLU ? v.nb * kBlock + rank * n_cols : v.nb * tile_cols + rank * kBlock;
                     for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                        const int st = it % S;
-                        ok = mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort);
+                        ok = mbar_wait_or_abort(&s.done[st], ph, abort);
                         if (!ok) break;
-                        mbar_expect_tx(&s.full[st], NB * kOperand);
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            tma_load_3d(s.buf[st] + (1 + b) * kOperand, &map_w, kb * kBlock,
-                                        w_row + b * (SWIGLU ? n_cols : kBlock), v.e, &s.full[st]);
+                        if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kOperand);
+                        tma_load_3d(s.buf[st] + kOperand, &map_w, kb * kBlock, w_row, v.e, cluster_addr(&s.full[st], 0));
+                        if (++st == S) { st = 0; ph ^= 1; }
                     }
                 }
-                // no copy may land after the CTA has left (only where something gave up is one still in flight)
-                if (!ok)
-                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
+                // No copy may land after the pair has left.  Only where something gave up is one still in flight
+                // then: the first CTA's barriers count both boxes; the second gives its own a millisecond.
+                if (!ok) {
+                    if (rank == 0) {
+                        for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
+                    } else {
+                        const long long t0 = clock64();
+                        while (clock64() - t0 < (1 << 21)) {}
+                    }
+                }
             }
             __syncwarp();
-        } else if (warp == 1) {
-            // ---- products ----
-            if (lane == 0) {
-                constexpr uint32_t idesc = mma_idesc(kBlock, NB * kBlock);
-                int it = 0;
-                bool ok = true;
-                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                    for (int kb = 0; kb < kb_n && ok; ++kb, ++it) {
-                        const int st = it % S, acc = it & 1;
-                        ok = mbar_wait_or_abort(&s.tempty[acc], ((it >> 1) & 1) ^ 1, abort) &&
-                             mbar_wait_or_abort(&s.full[st], (it / S) & 1, abort);
-                        if (!ok) break;
-                        tmem_fence_after();
-                        fence_async_shared();     // the rows were copied by threads
-                        const uint64_t da = smem_desc(s.buf[st]), db = smem_desc(s.buf[st] + kOperand);
+        } else if (warp == 1 && rank == 0) {
+            // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
+            constexpr uint32_t idesc = mma_idesc(kPairRows, NB * kBlock);
+            const bool issue = elect_one();
+            const uint64_t desc = smem_desc(s.buf[0]);
+            int st = 0, ph = 0, acc = 0, aph = 1, last = -1;
+            bool ok = true;
+            for (int u = first_unit; u < units && ok; u += step) {
+                for (int kb = 0; kb < kb_n; ++kb) {
+                    ok = mbar_wait_or_abort(&s.tempty[acc], aph, abort) && mbar_wait_or_abort(&s.full[st], ph, abort);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (issue) {
+                        const uint64_t da = desc + (uint32_t)(st * (2 * kOperand >> 4)), db = da + (kOperand >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 channels a step
                             mma_f8(tmem + acc * 256, da + k * 2, db + k * 2, idesc, k > 0);
-                        mma_commit(&s.empty[st]);
-                        mma_commit(&s.tfull[acc]);
+                        mma_commit(&s.done[st]);
+                    }
+                    last = st | ph << 8;
+                    if (++st == S) { st = 0; ph ^= 1; }
+                    acc ^= 1;
+                    aph ^= acc == 0;
+                }
+            }
+            if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---- word of this CTA's rows to the first CTA ----
+            if (lane == 0) {
+                const uint32_t full = cluster_addr(&s.full[0], 0);
+                int st = 0, ph = 0;
+                bool ok = true;
+                for (int u = first_unit; u < units && ok; u += step) {
+                    for (int kb = 0; kb < kb_n; ++kb) {
+                        ok = mbar_wait_or_abort(&s.rows_full[st], ph, abort);
+                        if (!ok) break;
+                        fence_async_shared();
+                        mbar_arrive_cluster(full + st * 8);
+                        if (++st == S) { st = 0; ph ^= 1; }
                     }
                 }
-                if (!ok && it > 0) mbar_wait_bounded(&s.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1);
             }
             __syncwarp();
         }
@@ -237,36 +264,37 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         const int part = (warp - 4) * 4 + (lane >> 3), piece = lane & 7;
         const int place = (lane >> 2) * kStep + (warp - 4) * 4 + (lane & 3);      // the row whose scale this lane copies
         const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
-        int it = 0;
+        int st = 0, ph = 1, ring = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = first_unit; u < units && ok; u += step) {
             const Unit v = find_unit(s, E, col_tiles, u);
             // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
             int m[kMine + 1], row[kMine + 1];
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) m[i] = v.m0 + i * kStep + part;
-            m[kMine] = v.m0 + place;
+            for (int i = 0; i < kMine; ++i) m[i] = v.m0 + rank * kBlock + i * kStep + part;
+            m[kMine] = v.m0 + rank * kBlock + place;
+            const int n = v.rows - rank * kBlock;     // this CTA's rows (128 or fewer, or none)
             receive_rows(a, v.e, m, row);
 #pragma unroll
             for (int i = 0; i <= kMine; ++i) row[i] *= kb_n;
             const int blk = SWIGLU ? v.nb : v.nb * NB;
             uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
             if (lane == 1) ws += SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;   // (zeros beyond N)
-            for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                const int st = it % S, ring = it % kScaleRing;
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.empty[st], ((it / S) & 1) ^ 1, abort));
+            for (int kb = 0; kb < kb_n; ++kb) {
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
                 if (!ok) break;
                 const uint32_t dst = smem_addr(s.buf[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
                 const uint8_t *src = a.a + kb * kBlock + piece * 16;
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
-                    if (i * kStep < v.rows - part)
+                    if (i * kStep < n - part)
                         cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)row[i] * kBlock);
-                if (place < v.rows)
+                if (place < n)
                     cp_async4(smem_addr(&s.row_scale[ring][place]), a.a_scales + (uint32_t)(row[kMine] + kb));
                 if (warp == 4 && lane < 2) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
-                cp_async_arrive(&s.full[st]);
-                cp_async_arrive(&s.sfull[ring]);
+                cp_async_arrive(&s.rows_full[st]);
+                if (++st == S) { st = 0; ph ^= 1; }
+                ring = (ring + 1) % kScaleRing;
             }
         }
         cp_async_wait_all();
@@ -276,13 +304,14 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         const int half = (warp - 8) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + half * 64;
-        int it = 0, unit = 0;
+        const uint32_t tempty = cluster_addr(&s.tempty[0], 0);
+        int st = 0, ph = 0, p = 0, ring = 0, unit = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
+        for (int u = first_unit; u < units && ok; u += step, ++unit) {
             const Unit v = find_unit(s, E, col_tiles, u);
-            const bool some = quarter * 32 < v.rows;     // rows in this warp's lanes
-            const bool live = r < v.rows;
-            const int m[1] = {v.m0 + min(r, v.rows - 1)};
+            const bool some = rank * kBlock + quarter * 32 < v.rows;     // rows in this warp's lanes
+            const bool live = rank * kBlock + r < v.rows;
+            const int m[1] = {v.m0 + min(rank * kBlock + r, v.rows - 1)};
             int rows[1];
             receive_rows(a, v.e, m, rows);
             const int row = rows[0];
@@ -291,11 +320,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) acc[b][c] = 0;
-            for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                const int p = it & 1, ring = it % kScaleRing;
-                ok = mbar_wait_or_abort(&s.sfull[ring], (it / kScaleRing) & 1, abort) &&
-                     mbar_wait_or_abort(&s.tfull[p], (it >> 1) & 1, abort);
-                ok = __all_sync(kFull, ok);
+            for (int kb = 0; kb < kb_n; ++kb) {
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
                 if (!ok) break;
                 if (some) {
                     tmem_fence_after();
@@ -310,14 +336,17 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
                         if (b == NB - 1) {
                             tmem_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&s.tempty[p]);
+                            if (lane == 0) mbar_arrive_cluster(tempty + p * 8);
                         }
 #pragma unroll
                         for (int c = 0; c < 32; ++c) fma2(acc[b][c], pair2(t[2 * c], t[2 * c + 1]), sc[b]);
                     }
                 } else if (lane == 0) {
-                    mbar_arrive(&s.tempty[p]);
+                    mbar_arrive_cluster(tempty + p * 8);
                 }
+                if (++st == S) { st = 0; ph ^= 1; }
+                p ^= 1;
+                ring = (ring + 1) % kScaleRing;
             }
             if (!ok) break;
             if (SWIGLU) {
@@ -377,29 +406,30 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();    // nothing of the other CTA arrives here, or reads from here, any more
     if (warp == 1) {
         tmem_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
     }
     if (threadIdx.x == 0 && s.abort) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
 }
 
-template <bool SWIGLU, int NB>
+template <bool SWIGLU>
 cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t st) {
-    constexpr int bytes = sizeof(ExpertShared<NB>) + 1024;
+    constexpr int bytes = sizeof(ExpertShared) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
     cached_per_device(ready, [&](int) {
-        e = cudaFuncSetAttribute(expert_kernel<SWIGLU, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(expert_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         // the warpgroups' register shares are drawn from what the block was launched with
         cudaFuncAttributes f{};
-        if (!e) e = cudaFuncGetAttributes(&f, expert_kernel<SWIGLU, NB>);
+        if (!e) e = cudaFuncGetAttributes(&f, expert_kernel<SWIGLU>);
         if (!e && f.numRegs * 4 < kIssueRegs + kCopyRegs + 2 * kAccRegs) e = cudaErrorInvalidDeviceFunction;
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
-    expert_kernel<SWIGLU, NB><<<num_sms(), kExpertThreads, bytes, st>>>(a, map_w);
+    expert_kernel<SWIGLU><<<num_sms() & ~1, kExpertThreads, bytes, st>>>(a, map_w);
     return cudaGetLastError();
 }
 
@@ -411,7 +441,7 @@ cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st) {
     const cuuint64_t sw[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.N * a.K)};
     const cuuint32_t bw[3] = {kBlock, kBlock, 1};
     if (cudaError_t e = encode_map(&map_w, 3, a.w, dw, sw, bw)) return e;
-    return a.q ? launch<true, 2>(a, map_w, st) : launch<false, 2>(a, map_w, st);
+    return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
 }
 
 }  // namespace ep
