@@ -170,7 +170,9 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);
 cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, cudaStream_t st);
 cudaError_t launch_combine_backward(int layout, const CombineArgs &a, const uint16_t *grad_out, uint16_t *grad_y,
                                     float *grad_weights, cudaStream_t st);
-cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st);
+cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st);        // chooses between
+cudaError_t launch_expert_many(const ExpertArgs &a, cudaStream_t st);
+cudaError_t launch_expert_few(const ExpertArgs &a, cudaStream_t st);
 
 // Sets the message ep_last_error_string() returns on this thread; returns code.
 int set_last_error(int code, const char *fmt, ...);

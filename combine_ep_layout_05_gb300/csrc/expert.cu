@@ -21,18 +21,16 @@
 // with 16-byte asynchronous copies in the swizzle that the products expect,
 // and the scales (warp 2 passes on that they are there); eight warps (two warpgroups, one for each half of the
 // columns) scale, accumulate and store: a thread owns a row.
-#include "tcgen05.cuh"
-#include "vec8.cuh"
+#include <cstddef>
+
+#include "expert_device.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kBlock = 128;                     // channels, and matrix rows, of a scale; rows of a tile
-constexpr int kOperand = kBlock * kBlock;       // bytes of 128 rows x 128 channels
 constexpr int kExpertThreads = 512;             // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
-constexpr int kIssueRegs = 40, kCopyRegs = 40, kAccRegs = 216;   // 40 + 40 + 2 * 216 = 4 * 128, the launch's registers
-constexpr int kTmemCols = 512;
+constexpr int kIssueRegs = 24, kCopyRegs = 56, kAccRegs = 216;   // 24 + 56 + 2 * 216 = 4 * 128, the launch's registers
 constexpr int kStages = 6;                      // operand buffers: 192 KB
 constexpr int kPairRows = 2 * kBlock;           // rows of a pair's tile
 constexpr int kCopyWarps = 4;                   // warps that copy rows
@@ -50,66 +48,10 @@ struct ExpertShared {
     uint64_t joined;                                       // maxima of a unit are written
     float row_scale[kScaleRing][kBlock], w_scale[kScaleRing][2];
     float amax[2][2][kBlock];                              // [unit parity][warpgroup][row]
-    int first[kMaxExperts + 1];                            // row tiles of the experts before
-    int rows[kMaxExperts];
+    WorkList list;
     uint32_t tmem;
     int abort;
 };
-
-// One unit of work
-struct Unit {
-    int e, m0;        // expert and its first row
-    int rows;         // rows from m0 on (at most 256)
-    int nb;           // column tile
-};
-
-__device__ __forceinline__ Unit find_unit(const ExpertShared &s, int E, int col_tiles, int u) {
-    // the last e with first[e] * col_tiles <= u (experts without rows share their successor's first tile)
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.first[mid] * col_tiles <= u) lo = mid;
-        else hi = mid;
-    }
-    const int tiles = s.first[lo + 1] - s.first[lo];
-    const int r = u - s.first[lo] * col_tiles;
-    Unit v;
-    v.e = lo;
-    v.nb = r / tiles;                 // row tiles fastest: they share the matrix rows
-    v.m0 = (r % tiles) * kPairRows;
-    v.rows = min(kPairRows, s.rows[lo] - v.m0);
-    return v;
-}
-
-// Receive rows of rows m[] of expert e, for each lane (called by whole warps;
-// counts outside [0, Tr] are clamped).
-template <int N>
-__device__ __forceinline__ void receive_rows(const ExpertArgs &a, int e, const int (&m)[N], int (&row)[N]) {
-    const Dims &d = a.d;
-    const int lane = threadIdx.x & 31, R = (int)d.R, Tr = (int)d.Tr;
-#pragma unroll
-    for (int i = 0; i < N; ++i) row[i] = e * R * Tr + m[i];
-    int before = 0;
-    for (int r0 = 0; r0 < R; r0 += 32) {
-        const int r = r0 + lane;
-        int end = r < R ? min(max(a.tokens_per_expert[(int64_t)r * d.E + e], 0), Tr) : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFull, end, o);
-            if (lane >= o) end += v;
-        }
-        end += before;                // rows up to and with source r
-        const int last = min(32, R - r0);
-        for (int i = 0; i < last; ++i) {
-            const int to = __shfl_sync(kFull, end, i);
-            const int start = (e * R + r0 + i + 1) * Tr - to;   // of the next source's segment, less the rows before
-#pragma unroll
-            for (int x = 0; x < N; ++x)
-                if (to <= m[x]) row[x] = start + m[x];
-        }
-        before = __shfl_sync(kFull, end, 31);
-    }
-}
 
 template <bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
@@ -117,6 +59,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     extern __shared__ unsigned char raw[];
     ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
     constexpr int S = kStages, NB = 2;
+    static_assert(offsetof(ExpertShared, rows_full) % 8 == 0 && offsetof(ExpertShared, w_scale) % 8 == 0, "");
     const Dims &d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = (int)d.E;
     const int rank = (int)cluster_rank();                           // place in the pair
@@ -126,19 +69,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     const int col_tiles = (n_cols + tile_cols - 1) / tile_cols;
     const int first_unit = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-    // rows of every expert
-    bool bad = false;
-    for (int e = threadIdx.x; e < E; e += kExpertThreads) {
-        int n = 0;
-        for (int r = 0; r < d.R; ++r) {
-            const int c = a.tokens_per_expert[(int64_t)r * E + e];
-            const int ok = min(max(c, 0), (int)d.Tr);
-            bad |= ok != c;
-            n += ok;
-        }
-        s.rows[e] = n;
-    }
-    if (bad && blockIdx.x == 0) raise_status(a.dev_status, EP_STATUS_BAD_SLOT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&s.rows_full[i], kCopyWarps * 32);
@@ -150,34 +80,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
-                     "n"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    }
-    __syncthreads();
-    if (warp == 0) {   // tiles of the experts before each
-        int sum = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int t = e0 + lane < E ? (s.rows[e0 + lane] + kPairRows - 1) / kPairRows : 0;
-            int inc = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kFull, inc, o);
-                if (lane >= o) inc += v;
-            }
-            if (e0 + lane < E) s.first[e0 + lane] = sum + inc - t;
-            sum += __shfl_sync(kFull, inc, 31);
-        }
-        if (lane == 0) s.first[E] = sum;
-    }
+    if (warp == 1) tmem_alloc<2>(&s.tmem);
+    make_list(s.list, a, kPairRows, kExpertThreads);
     tmem_fence_before();
     __syncthreads();
     cluster_sync();    // the other CTA's barriers are there too
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
-    const int units = s.first[E] * col_tiles;   // below 2^31: checked on the host
+    const int units = s.list.first[E] * col_tiles;   // below 2^31: checked on the host
     volatile int *abort = &s.abort;
 
     if (warp < 4) {
@@ -188,13 +98,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 int st = 0, ph = 1, it = 0;
                 bool ok = true;
                 for (int u = first_unit; u < units && ok; u += step) {
-                    const Unit v = find_unit(s, E, col_tiles, u);
+                    const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
                     const int w_row = SWIGLU ? v.nb * kBlock + rank * n_cols : v.nb * tile_cols + rank * kBlock;
                     for (int kb = 0; kb < kb_n; ++kb, ++it) {
                         ok = mbar_wait_or_abort(&s.done[st], ph, abort);
                         if (!ok) break;
                         if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kOperand);
-                        tma_load_3d(s.buf[st] + kOperand, &map_w, kb * kBlock, w_row, v.e, cluster_addr(&s.full[st], 0));
+                        tma_load_3d<2>(s.buf[st] + kOperand, &map_w, kb * kBlock, w_row, v.e, cluster_addr(&s.full[st], 0));
                         if (++st == S) { st = 0; ph ^= 1; }
                     }
                 }
@@ -227,8 +137,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                         const uint64_t da = desc + (uint32_t)(st * (2 * kOperand >> 4)), db = da + (kOperand >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 channels a step
-                            mma_f8(tmem + acc * 256, da + k * 2, db + k * 2, idesc, k > 0);
-                        mma_commit(&s.done[st]);
+                            mma_f8<2>(tmem + acc * 256, da + k * 2, db + k * 2, idesc, k > 0);
+                        mma_commit<2>(&s.done[st]);
                     }
                     last = st | ph << 8;
                     if (++st == S) { st = 0; ph ^= 1; }
@@ -267,7 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         int st = 0, ph = 1, ring = 0;
         bool ok = true;
         for (int u = first_unit; u < units && ok; u += step) {
-            const Unit v = find_unit(s, E, col_tiles, u);
+            const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
             // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
             int m[kMine + 1], row[kMine + 1];
 #pragma unroll
@@ -308,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         int st = 0, ph = 0, p = 0, ring = 0, unit = 0;
         bool ok = true;
         for (int u = first_unit; u < units && ok; u += step, ++unit) {
-            const Unit v = find_unit(s, E, col_tiles, u);
+            const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
             const bool some = rank * kBlock + quarter * 32 < v.rows;     // rows in this warp's lanes
             const bool live = rank * kBlock + r < v.rows;
             const int m[1] = {v.m0 + min(rank * kBlock + r, v.rows - 1)};
@@ -409,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     cluster_sync();    // nothing of the other CTA arrives here, or reads from here, any more
     if (warp == 1) {
         tmem_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+        tmem_free<2>(tmem);
     }
     if (threadIdx.x == 0 && s.abort) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
 }
@@ -435,12 +345,9 @@ cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st) {
+cudaError_t launch_expert_many(const ExpertArgs &a, cudaStream_t st) {
     CUtensorMap map_w;
-    const cuuint64_t dw[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.d.E};
-    const cuuint64_t sw[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.N * a.K)};
-    const cuuint32_t bw[3] = {kBlock, kBlock, 1};
-    if (cudaError_t e = encode_map(&map_w, 3, a.w, dw, sw, bw)) return e;
+    if (cudaError_t e = matrix_map(a, &map_w)) return e;
     return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
 }
 

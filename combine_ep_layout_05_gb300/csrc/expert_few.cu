@@ -1,0 +1,355 @@
+// Expert products for experts with few rows: the matrices are read once and
+// that is what takes the time.
+//
+// Same operation as expert.cu, with the operands' parts exchanged: 128 matrix
+// rows are the tensor core's M, the expert's rows its N (16, 32, 48 or 64, as
+// many as there are), so a step costs next to nothing beside the copy of its
+// matrix rows: SwiGLU 32 KB (128 gate and 128 up rows), else 16 KB, for which
+// an SM's share of the memory rate takes some 1400 and 700 cycles.  160 KB (128
+// KB) of operands in flight cover the memory's latency several times.
+//
+// An accumulator in tensor memory has a matrix row in each lane and the
+// expert's rows in its columns; four alternate.  A thread owns a matrix row:
+// the matrix's scale is one number, the rows' scales are read from shared
+// memory.  Warps as in expert.cu; SwiGLU's two warpgroups hold gate and up,
+// swap halves of their columns through shared memory at the end, and each
+// finishes its half.
+#include <cstddef>
+
+#include "expert_device.cuh"
+
+#ifndef EP_EXPERT_FEW_ROWS
+#define EP_EXPERT_FEW_ROWS 64   // most rows an expert, on average, for this kernel
+#endif
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 512;                   // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
+constexpr int kIssueRegs = 72, kCopyRegs = 88, kAccRegs = 176;   // 72 + 88 + 2 * 176 = 4 * 128, the launch's registers
+constexpr int kRows = 64;                       // rows of a tile
+constexpr int kCopyThreads = 128;
+constexpr int kAcc = 4;                         // accumulators
+template <bool SWIGLU>
+constexpr int kStages = SWIGLU ? 4 : 7;         // operand buffers
+// Steps whose scales are kept: a step's copies wait for the products kStages
+// steps before, those for the loads of the accumulation kAcc steps before
+// them, which may still be using that step's scales.
+constexpr int kScaleRing = 16;
+
+template <bool SWIGLU>
+struct FewShared {
+    unsigned char w[kStages<SWIGLU>][(SWIGLU ? 2 : 1) * kOperand];
+    unsigned char rows[kStages<SWIGLU>][kRows * kBlock];
+    uint64_t rows_full[kStages<SWIGLU>], full[kStages<SWIGLU>];   // rows and scales; all operands
+    uint64_t done[kStages<SWIGLU>];                               // a step's products: buffers free, sums ready
+    uint64_t tempty[kAcc];                                        // accumulators taken out
+    uint64_t swapped, joined;                                     // the ends of a SwiGLU unit
+    alignas(16) float row_scale[kScaleRing][kRows];               // (read 16 bytes at a time, as are the maxima)
+    float w_scale[kScaleRing][2];
+    float swap[SWIGLU ? 2 : 1][kRows / 2][kBlock];
+    alignas(16) uint32_t amax[kRows][4];
+    WorkList list;
+    uint32_t tmem;
+    int abort;
+};
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_few_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ unsigned char raw[];
+    FewShared<SWIGLU> &s = *reinterpret_cast<FewShared<SWIGLU> *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    constexpr int S = kStages<SWIGLU>, NB = SWIGLU ? 2 : 1;
+    static_assert(offsetof(FewShared<SWIGLU>, rows) % 1024 == 0 && offsetof(FewShared<SWIGLU>, rows_full) % 8 == 0, "");
+    static_assert(offsetof(FewShared<SWIGLU>, row_scale) % 16 == 0 && offsetof(FewShared<SWIGLU>, amax) % 16 == 0, "");
+    static_assert(kScaleRing > S + kAcc + 1, "scales are still in use when they are overwritten");
+    const Dims &d = a.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = (int)d.E;
+    const int kb_n = (int)(a.K / kBlock);
+    const int n_cols = (int)(SWIGLU ? a.N / 2 : a.N);               // output columns
+    const int col_tiles = (n_cols + kBlock - 1) / kBlock;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&s.rows_full[i], kCopyThreads);
+            mbar_init(&s.full[i], 2);          // the boxes' bytes, word of the rows
+            mbar_init(&s.done[i], 1);
+        }
+        for (int i = 0; i < kAcc; ++i) mbar_init(&s.tempty[i], 8);
+        mbar_init(&s.swapped, 8);
+        mbar_init(&s.joined, 8);
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<1>(&s.tmem);
+    make_list(s.list, a, kRows, kThreads);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s.tmem;
+    const int units = s.list.first[E] * col_tiles;   // below 2^31: checked on the host
+    volatile int *abort = &s.abort;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 0) {
+            // ---- matrix rows ----
+            if (lane == 0) {
+                int st = 0, ph = 1, it = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                    const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
+                    for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                        ok = mbar_wait_or_abort(&s.done[st], ph, abort);
+                        if (!ok) break;
+                        mbar_expect_tx(&s.full[st], NB * kOperand);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            tma_load_3d<1>(s.w[st] + b * kOperand, &map_w, kb * kBlock, v.nb * kBlock + b * n_cols, v.e,
+                                           smem_addr(&s.full[st]));
+                        if (++st == S) { st = 0; ph ^= 1; }
+                    }
+                }
+                // no copy may land after the CTA has left (only where something gave up is one still in flight)
+                if (!ok)
+                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
+            const bool issue = elect_one();
+            const uint64_t dw = smem_desc(s.w[0]), dr = smem_desc(s.rows[0]);
+            int st = 0, ph = 0, acc = 0, aph = 1, last = -1;
+            bool ok = true;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
+                const uint32_t idesc = mma_idesc(kBlock, (v.rows + 15) & ~15);
+                for (int kb = 0; kb < kb_n; ++kb) {
+                    ok = mbar_wait_or_abort(&s.tempty[acc], aph, abort) && mbar_wait_or_abort(&s.full[st], ph, abort);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (issue) {
+                        const uint64_t da = dw + (uint32_t)(st * (NB * kOperand >> 4));
+                        const uint64_t db = dr + (uint32_t)(st * (kRows * kBlock >> 4));
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)   // 32 channels a step
+                                mma_f8<1>(tmem + (acc * NB + b) * kRows, da + (b * (kOperand >> 4) + k * 2), db + k * 2, idesc,
+                                          k > 0);
+                        mma_commit<1>(&s.done[st]);
+                    }
+                    last = st | ph << 8;
+                    if (++st == S) { st = 0; ph ^= 1; }
+                    acc = (acc + 1) % kAcc;
+                    aph ^= acc == 0;
+                }
+            }
+            if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---- word of the rows ----
+            if (lane == 0) {
+                int st = 0, ph = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                    for (int kb = 0; kb < kb_n; ++kb) {
+                        ok = mbar_wait_or_abort(&s.rows_full[st], ph, abort);
+                        if (!ok) break;
+                        fence_async_shared();
+                        mbar_arrive(&s.full[st]);
+                        if (++st == S) { st = 0; ph ^= 1; }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        // ---- rows and scales: eight lanes copy a row's 128 bytes ----
+        constexpr int kStep = kCopyThreads / 8, kMine = kRows / kStep;
+        const int part = (threadIdx.x - 128) >> 3, piece = lane & 7;
+        const int place = (threadIdx.x - 128) & (kRows - 1);      // the row whose scale this thread copies, if below 64
+        const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
+        int st = 0, ph = 1, ring = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
+            // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
+            int m[kMine + 1], row[kMine + 1];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) m[i] = v.m0 + i * kStep + part;
+            m[kMine] = v.m0 + place;
+            receive_rows(a, v.e, m, row);
+#pragma unroll
+            for (int i = 0; i <= kMine; ++i) row[i] *= kb_n;
+            uint32_t ws = (uint32_t)(v.e * n_blocks + v.nb) * kb_n;
+            if (lane == 1) ws += n_blocks / 2 * kb_n;             // (SwiGLU: the up block's)
+            const bool has_scale = warp < 6 && place < v.rows;
+            for (int kb = 0; kb < kb_n; ++kb) {
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
+                if (!ok) break;
+                const uint32_t dst = smem_addr(s.rows[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
+                const uint8_t *src = a.a + kb * kBlock + piece * 16;
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (i * kStep + part < v.rows)
+                        cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)row[i] * kBlock);
+                if (has_scale) cp_async4(smem_addr(&s.row_scale[ring][place]), a.a_scales + (uint32_t)(row[kMine] + kb));
+                if (warp == 7 && lane < NB) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
+                cp_async_arrive(&s.rows_full[st]);
+                if (++st == S) { st = 0; ph ^= 1; }
+                ring = (ring + 1) % kScaleRing;
+            }
+        }
+        cp_async_wait_all();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAccRegs));
+        // ---- accumulation: thread = matrix row.  SwiGLU: a warpgroup has a block and all columns; else half of them ----
+        constexpr int kMine = SWIGLU ? kRows : kRows / 2;
+        const int half = (warp - 8) >> 2, quarter = warp & 3;
+        const int chan = quarter * 32 + lane;
+        const int c0 = SWIGLU ? 0 : half * kMine;                 // first column (row of the tile)
+        const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + (SWIGLU ? half * kRows : c0);
+        int st = 0, ph = 0, p = 0, ring = 0, unit = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
+            const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
+            uint64_t acc[kMine / 2];
+#pragma unroll
+            for (int c = 0; c < kMine / 2; ++c) acc[c] = 0;
+            for (int kb = 0; kb < kb_n; ++kb) {
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
+                if (!ok) break;
+                tmem_fence_after();
+                uint32_t t[kMine];
+#pragma unroll
+                for (int q = 0; q < kMine / 16; ++q)
+                    if (c0 + q * 16 < v.rows) tmem_ld16(tm + p * (NB * kRows) + q * 16, t + q * 16);
+                tmem_wait_ld<kMine>(t);
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.tempty[p]);
+                const uint32_t w32 = __float_as_uint(s.w_scale[ring][SWIGLU ? half : 0]);
+                const uint64_t sw = pair2(w32, w32);
+#pragma unroll
+                for (int q = 0; q < kMine / 16; ++q) {
+                    if (c0 + q * 16 >= v.rows) break;
+                    const ulonglong2 *sr = reinterpret_cast<const ulonglong2 *>(&s.row_scale[ring][c0 + q * 16]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const ulonglong2 x = sr[c];
+                        const int i = q * 16 + c * 4;
+                        fma2(acc[i / 2], pair2(t[i], t[i + 1]), mul2(x.x, sw));
+                        fma2(acc[i / 2 + 1], pair2(t[i + 2], t[i + 3]), mul2(x.y, sw));
+                    }
+                }
+                if (++st == S) { st = 0; ph ^= 1; }
+                p = (p + 1) % kAcc;
+                ring = (ring + 1) % kScaleRing;
+            }
+            if (!ok) break;
+            // receive rows of the tile: lane l has rows l and l + 32
+            const int m[2] = {v.m0 + min(lane, v.rows - 1), v.m0 + min(lane + 32, v.rows - 1)};
+            int row[2];
+            receive_rows(a, v.e, m, row);
+            if (SWIGLU) {
+                // The gate's warpgroup finishes columns 0-31 and hands over the gate of columns 32-63; the up's the
+                // other way round.  Its own values of the columns that it finishes end up in acc[0 .. 15].
+                constexpr int H = kRows / 2;
+                float *mine = &s.swap[half][0][chan];
+                const float *theirs = &s.swap[half ^ 1][0][chan];
+#pragma unroll
+                for (int c = 0; c < H / 2; ++c) {
+                    const uint64_t give = half ? acc[c] : acc[H / 2 + c];
+                    mine[(2 * c) * kBlock] = lo2(give);
+                    mine[(2 * c + 1) * kBlock] = hi2(give);
+                    if (half) acc[c] = acc[H / 2 + c];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.swapped);
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.swapped, unit & 1, abort));
+                if (!ok) break;
+                const int n = v.rows - half * H;       // rows among this warpgroup's columns
+#pragma unroll
+                for (int c = 0; c < H; ++c) {
+                    if (c >= n) break;
+                    const float own = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]), other = theirs[c * kBlock];
+                    const float g = half ? other : own, up = half ? own : other;
+                    const float h = g / (1.f + expf(-g)) * up;
+                    const uint32_t bits = __float_as_uint(h);
+                    acc[c / 2] = c & 1 ? (acc[c / 2] & 0xffffffffull) | (uint64_t)bits << 32
+                                       : (acc[c / 2] & ~0xffffffffull) | bits;
+                    const uint32_t top = __reduce_max_sync(kFull, bits & 0x7fffffffu);   // (NaN above all numbers)
+                    if (lane == 0) s.amax[half * H + c][quarter] = top;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.joined);
+                ok = __all_sync(kFull, mbar_wait_or_abort(&s.joined, unit & 1, abort));
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < H; ++c) {
+                    if (c >= n) break;
+                    const uint4 t4 = *reinterpret_cast<const uint4 *>(s.amax[half * H + c]);
+                    const float amax = __uint_as_float(max(max(t4.x, t4.y), max(t4.z, t4.w)));
+                    const float inv = amax > 0.f ? fminf(448.f / amax, 3.402823466e38f) : 0.f;
+                    const float h = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]);
+                    const int64_t at = __shfl_sync(kFull, half ? row[1] : row[0], c);
+                    a.q[at * n_cols + v.nb * kBlock + chan] = (uint8_t)pack_e4m3x2(h * inv, 0.f);
+                    if (chan == 0) a.q_scales[at * (n_cols / kBlock) + v.nb] = amax / 448.f;
+                }
+            } else {
+                const int col = v.nb * kBlock + chan;
+#pragma unroll
+                for (int c = 0; c < kMine; ++c) {
+                    if (c0 + c >= v.rows) break;
+                    const int64_t at = __shfl_sync(kFull, half ? row[1] : row[0], c);
+                    const float y = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]);
+                    if (col < n_cols) a.y[at * n_cols + col] = (uint16_t)pack_bf16x2(y, 0.f);
+                }
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tmem_fence_after();
+        tmem_free<1>(tmem);
+    }
+    if (threadIdx.x == 0 && s.abort) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+}
+
+template <bool SWIGLU>
+cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t st) {
+    constexpr int bytes = sizeof(FewShared<SWIGLU>) + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    static std::atomic<int> ready[kCacheDevices];
+    cudaError_t e = cudaSuccess;
+    cached_per_device(ready, [&](int) {
+        e = cudaFuncSetAttribute(expert_few_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        // the warpgroups' register shares are drawn from what the block was launched with
+        cudaFuncAttributes f{};
+        if (!e) e = cudaFuncGetAttributes(&f, expert_few_kernel<SWIGLU>);
+        if (!e && f.numRegs * 4 < kIssueRegs + kCopyRegs + 2 * kAccRegs) e = cudaErrorInvalidDeviceFunction;
+        return e == cudaSuccess ? 1 : 0;
+    });
+    if (e) return e;
+    expert_few_kernel<SWIGLU><<<num_sms(), kThreads, bytes, st>>>(a, map_w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_expert_few(const ExpertArgs &a, cudaStream_t st) {
+    CUtensorMap map_w;
+    if (cudaError_t e = matrix_map(a, &map_w)) return e;
+    return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
+}
+
+cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st) {
+    return a.d.T * a.d.k <= a.d.E * EP_EXPERT_FEW_ROWS ? launch_expert_few(a, st) : launch_expert_many(a, st);
+}
+
+}  // namespace ep
