@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                     for (int x = 0; x < 2; ++x) {
                         const float g = x ? hi2(acc[0][c]) : lo2(acc[0][c]);
                         const float up = x ? hi2(acc[NB - 1][c]) : lo2(acc[NB - 1][c]);
-                        h[x] = g / (1.f + expf(-g)) * up;
+                        h[x] = swiglu(g, up);
                         amax = fmaxf(amax, fabsf(h[x]));
                         nan |= h[x] != h[x];
                     }

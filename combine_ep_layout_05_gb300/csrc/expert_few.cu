@@ -50,6 +50,7 @@ struct FewShared {
     float w_scale[kScaleRing][2];
     float swap[SWIGLU ? 2 : 1][kRows / 2][kBlock];
     alignas(16) uint32_t amax[kRows][4];
+    int row[kScaleRing][kRows];                                   // a unit's receive rows (kept like the scales)
     WorkList list;
     uint32_t tmem;
     int abort;
@@ -173,9 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int part = (threadIdx.x - 128) >> 3, piece = lane & 7;
         const int place = (threadIdx.x - 128) & (kRows - 1);      // the row whose scale this thread copies, if below 64
         const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
-        int st = 0, ph = 1, ring = 0;
+        int st = 0, ph = 1, ring = 0, unit = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
             const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
             // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
             int m[kMine + 1], row[kMine + 1];
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kMine; ++i) m[i] = v.m0 + i * kStep + part;
             m[kMine] = v.m0 + place;
             receive_rows(a, v.e, m, row);
+            if (warp < 6) s.row[unit % kScaleRing][place] = row[kMine];   // (announced with the first step's copies)
 #pragma unroll
             for (int i = 0; i <= kMine; ++i) row[i] *= kb_n;
             uint32_t ws = (uint32_t)(v.e * n_blocks + v.nb) * kb_n;
@@ -207,12 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait_all();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAccRegs));
-        // ---- accumulation: thread = matrix row.  SwiGLU: a warpgroup has a block and all columns; else half of them ----
+        // ---- accumulation: thread = matrix row.  SwiGLU: a warpgroup has a block and all columns; else every other
+        // 16 columns (rows of the tile), so that both have work from 17 rows on ----
         constexpr int kMine = SWIGLU ? kRows : kRows / 2;
         const int half = (warp - 8) >> 2, quarter = warp & 3;
         const int chan = quarter * 32 + lane;
-        const int c0 = SWIGLU ? 0 : half * kMine;                 // first column (row of the tile)
-        const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + (SWIGLU ? half * kRows : c0);
+        const auto column = [&](int q) { return SWIGLU ? q * 16 : (q * 2 + half) * 16; };   // first of my q-th sixteen
+        const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + (SWIGLU ? half * kRows : 0);
         int st = 0, ph = 0, p = 0, ring = 0, unit = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t t[kMine];
 #pragma unroll
                 for (int q = 0; q < kMine / 16; ++q)
-                    if (c0 + q * 16 < v.rows) tmem_ld16(tm + p * (NB * kRows) + q * 16, t + q * 16);
+                    if (column(q) < v.rows) tmem_ld16(tm + p * (NB * kRows) + column(q), t + q * 16);
                 tmem_wait_ld<kMine>(t);
                 tmem_fence_before();
                 __syncwarp();
@@ -236,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t sw = pair2(w32, w32);
 #pragma unroll
                 for (int q = 0; q < kMine / 16; ++q) {
-                    if (c0 + q * 16 >= v.rows) break;
-                    const ulonglong2 *sr = reinterpret_cast<const ulonglong2 *>(&s.row_scale[ring][c0 + q * 16]);
+                    if (column(q) >= v.rows) break;
+                    const ulonglong2 *sr = reinterpret_cast<const ulonglong2 *>(&s.row_scale[ring][column(q)]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const ulonglong2 x = sr[c];
@@ -251,10 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ring = (ring + 1) % kScaleRing;
             }
             if (!ok) break;
-            // receive rows of the tile: lane l has rows l and l + 32
-            const int m[2] = {v.m0 + min(lane, v.rows - 1), v.m0 + min(lane + 32, v.rows - 1)};
-            int row[2];
-            receive_rows(a, v.e, m, row);
+            const int *rows = s.row[unit % kScaleRing];
             if (SWIGLU) {
                 // The gate's warpgroup finishes columns 0-31 and hands over the gate of columns 32-63; the up's the
                 // other way round.  Its own values of the columns that it finishes end up in acc[0 .. 15].
@@ -272,42 +272,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&s.swapped);
                 ok = __all_sync(kFull, mbar_wait_or_abort(&s.swapped, unit & 1, abort));
                 if (!ok) break;
-                const int n = v.rows - half * H;       // rows among this warpgroup's columns
+                const int n = min(v.rows - half * H, H);   // rows among this warpgroup's columns (may be negative)
+                uint32_t top = 0;                          // lane c: of column c
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
                     if (c >= n) break;
                     const float own = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]), other = theirs[c * kBlock];
-                    const float g = half ? other : own, up = half ? own : other;
-                    const float h = g / (1.f + expf(-g)) * up;
-                    const uint32_t bits = __float_as_uint(h);
+                    const uint32_t bits = __float_as_uint(half ? swiglu(other, own) : swiglu(own, other));
                     acc[c / 2] = c & 1 ? (acc[c / 2] & 0xffffffffull) | (uint64_t)bits << 32
                                        : (acc[c / 2] & ~0xffffffffull) | bits;
-                    const uint32_t top = __reduce_max_sync(kFull, bits & 0x7fffffffu);   // (NaN above all numbers)
-                    if (lane == 0) s.amax[half * H + c][quarter] = top;
+                    const uint32_t x = __reduce_max_sync(kFull, bits & 0x7fffffffu);   // (NaN above all numbers)
+                    if (lane == c) top = x;
                 }
+                if (lane < n) s.amax[half * H + lane][quarter] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.joined);
                 ok = __all_sync(kFull, mbar_wait_or_abort(&s.joined, unit & 1, abort));
                 if (!ok) break;
+                float inv = 0.f;                           // lane c: of column c
+                if (lane < n) {
+                    const uint4 t4 = *reinterpret_cast<const uint4 *>(s.amax[half * H + lane]);
+                    const float amax = __uint_as_float(max(max(t4.x, t4.y), max(t4.z, t4.w)));
+                    inv = amax > 0.f ? fminf(448.f / amax, 3.402823466e38f) : 0.f;
+                    if (quarter == 0)
+                        a.q_scales[(int64_t)rows[half * H + lane] * (n_cols / kBlock) + v.nb] = amax / 448.f;
+                }
+                uint8_t *q = a.q + v.nb * kBlock + chan;
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
                     if (c >= n) break;
-                    const uint4 t4 = *reinterpret_cast<const uint4 *>(s.amax[half * H + c]);
-                    const float amax = __uint_as_float(max(max(t4.x, t4.y), max(t4.z, t4.w)));
-                    const float inv = amax > 0.f ? fminf(448.f / amax, 3.402823466e38f) : 0.f;
                     const float h = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]);
-                    const int64_t at = __shfl_sync(kFull, half ? row[1] : row[0], c);
-                    a.q[at * n_cols + v.nb * kBlock + chan] = (uint8_t)pack_e4m3x2(h * inv, 0.f);
-                    if (chan == 0) a.q_scales[at * (n_cols / kBlock) + v.nb] = amax / 448.f;
+                    q[(int64_t)rows[half * H + c] * n_cols] = (uint8_t)pack_e4m3x2(h * __shfl_sync(kFull, inv, c), 0.f);
                 }
             } else {
                 const int col = v.nb * kBlock + chan;
+                uint16_t *y = a.y + col;
 #pragma unroll
                 for (int c = 0; c < kMine; ++c) {
-                    if (c0 + c >= v.rows) break;
-                    const int64_t at = __shfl_sync(kFull, half ? row[1] : row[0], c);
-                    const float y = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]);
-                    if (col < n_cols) a.y[at * n_cols + col] = (uint16_t)pack_bf16x2(y, 0.f);
+                    const int at = column(c >> 4) + (c & 15);
+                    if (at >= v.rows) break;
+                    const float f = c & 1 ? hi2(acc[c / 2]) : lo2(acc[c / 2]);
+                    if (col < n_cols) y[(int64_t)rows[at] * n_cols] = (uint16_t)pack_bf16x2(f, 0.f);
                 }
             }
         }

@@ -215,6 +215,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
+// x / (1 + exp(-x)) * y; the reciprocal is within one unit in the last place
+__device__ __forceinline__ float swiglu(float x, float y) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-x)));
+    return x * r * y;
+}
+
 // Tensor map of a byte tensor with rows of dims[0] bytes in the 128-byte
 // swizzle; strides in bytes of dimensions 1 and up.  The encoder is a host
 // function of the driver, found once through the runtime.
