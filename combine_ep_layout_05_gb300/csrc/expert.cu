@@ -9,18 +9,23 @@
 // numbers (not powers of two), so every block's product is taken out of
 // tensor memory and added, times its scale, to fp32 registers.  Two
 // accumulators in tensor memory alternate: one is filled while the other is
-// taken out.  A pair, because shared memory bounds these products: a CTA
-// alone (128 x 256) would write and read 96 KB of it for a block, 768 cycles
-// at 128 bytes each for 512 cycles of products; a CTA of a pair holds half of
-// the matrix rows, 64 KB.
+// taken out.  (Four of 128 columns would be free sooner, but products 128
+// columns wide took 1.6 times as long for the same work.)  A pair, because
+// shared memory bounds these products: a CTA alone (128 x 256) would write and
+// read 96 KB of it for a step, 768 cycles at 128 bytes each for 512 cycles of
+// products; a CTA of a pair holds half of the matrix rows, 64 KB.
 //
 // A persistent pair walks (expert, row tile, column tile) triples; each CTA
-// holds 128 of the tile's rows and 128 of its matrix rows.  Warps: warp 0
-// copies boxes of 128 matrix rows (TMA), warp 1 of the first CTA issues the
-// products, warps 4-7 copy the rows, which lie in R segments of any length,
-// with 16-byte asynchronous copies in the swizzle that the products expect,
-// and the scales (warp 2 passes on that they are there); eight warps (two warpgroups, one for each half of the
-// columns) scale, accumulate and store: a thread owns a row.
+// holds 128 of the tile's rows and 128 of its matrix rows.
+// An expert's rows lie in R segments.  Where few segments meet in a tile its
+// rows come in boxes (TMA): two of the largest power of two for each segment,
+// overlapping; a box costs some 80 cycles of the copy unit, whatever its size,
+// so that from kBoxes boxes on threads copy the rows, 16 bytes each, in the
+// swizzle that the products expect.  Warps of a CTA: 0 issues the boxes, 1 (of
+// the first CTA) the products, 2 passes on that the rows and scales copied by
+// warps 4-7 are there, 3 plans the units ahead; eight warps (two warpgroups,
+// one for each half of the columns) scale, accumulate and store: a thread owns
+// a row.
 #include <cstddef>
 
 #include "expert_device.cuh"
@@ -29,53 +34,113 @@ namespace ep {
 
 namespace {
 
-constexpr int kExpertThreads = 512;             // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
-constexpr int kIssueRegs = 24, kCopyRegs = 56, kAccRegs = 216;   // 24 + 56 + 2 * 216 = 4 * 128, the launch's registers
+constexpr int kExpertThreads = 512;             // warpgroup 0: boxes, products, plans; 1: rows; 2, 3: accumulation
+constexpr int kIssueRegs = 56, kCopyRegs = 40, kAccRegs = 208;   // 56 + 40 + 2 * 208 = 4 * 128, the launch's registers
 constexpr int kStages = 6;                      // operand buffers: 192 KB
 constexpr int kPairRows = 2 * kBlock;           // rows of a pair's tile
 constexpr int kCopyWarps = 4;                   // warps that copy rows
+constexpr int kBoxes = 8;                       // most boxes that bring a CTA's rows; else its threads copy them
+constexpr int kPlans = 4;                       // units planned ahead
+constexpr int kPlanUsers = 2 + 1 + kCopyWarps + 8;   // warps that read a plan: 0, 1, 2, copies, accumulation
 // Steps whose scales are kept.  The copies of a step wait until the products
-// kStages steps before are done, which waited for the accumulation two steps
-// before those: its scales may be overwritten from kStages + 2 steps on.
+// kStages steps before are done, which waited for the loads of the accumulation
+// two steps before those, whose scales may still be in use then.
 constexpr int kScaleRing = 16;
-static_assert(kScaleRing > kStages + 2, "scales are still in use when they are overwritten");
+static_assert(kScaleRing > kStages + 3, "scales are still in use when they are overwritten");
+
+struct ExpertMaps {
+    CUtensorMap a[8];     // the rows, in boxes of 2^i rows
+    CUtensorMap w;        // the matrices, in boxes of 128 rows
+};
+
+// A unit of work as its CTA needs it
+struct Plan {
+    int e, nb;            // expert (-1: no more units) and column tile
+    int rows;             // this CTA's rows, at most 128
+    int boxes;            // boxes that bring them, or -1: the threads copy them
+    uint32_t expect;      // bytes of both CTAs' boxes in a step
+};
 
 struct ExpertShared {
     unsigned char buf[kStages][2 * kOperand];              // rows, then matrix rows
     uint64_t rows_full[kStages], full[kStages];            // this CTA's rows and scales; all operands of both CTAs
     uint64_t done[kStages];                                // a step's products: its buffers are free, its sums ready
     uint64_t tempty[2];                                    // accumulators taken out
+    uint64_t plan_full[kPlans], plan_empty[kPlans];
     uint64_t joined;                                       // maxima of a unit are written
     float row_scale[kScaleRing][kBlock], w_scale[kScaleRing][2];
     float amax[2][2][kBlock];                              // [unit parity][warpgroup][row]
+    Plan plan[kPlans];
+    int row[kPlans][kBlock];                               // a unit's receive rows
+    int3 box[kPlans][kBoxes];                              // first row, place, log2 of the height
     WorkList list;
     uint32_t tmem;
     int abort;
 };
 
+__device__ __forceinline__ int clamp_rows(int n) { return min(max(n, 0), kBlock); }
+
+// Lists the boxes that bring rows [m0, m0 + n) of expert e (n <= 128) to a
+// CTA: the part of each segment in up to two boxes of the largest power of
+// two that fits, which may overlap (the same rows to the same places).
+// Returns their number, or more than kBoxes if they are too many.  Called by
+// a whole warp; bytes gets the sum of their sizes (box null: counted only).
+__device__ __forceinline__ int list_boxes(int3 *box, const ExpertArgs &a, int e, int m0, int n, uint32_t &bytes) {
+    const Dims &d = a.d;
+    const int lane = threadIdx.x & 31, R = (int)d.R, Tr = (int)d.Tr;
+    int before = 0, boxes = 0;
+    bytes = 0;
+    for (int r0 = 0; r0 < R; r0 += 32) {
+        const int r = r0 + lane;
+        const int c = r < R ? min(max(a.tokens_per_expert[(int64_t)r * d.E + e], 0), Tr) : 0;
+        int end = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, end, o);
+            if (lane >= o) end += v;
+        }
+        end += before;
+        before = __shfl_sync(kFull, end, 31);
+        const int lo = max(end - c, m0), hi = min(end, m0 + n), len = max(hi - lo, 0);
+        const int lg = 31 - __clz(len | 1), size = 1 << lg;
+        const int mine = len == 0 ? 0 : len == size ? 1 : 2;
+        // boxes of the lanes before, from two ballots
+        const unsigned one = __ballot_sync(kFull, mine >= 1), two = __ballot_sync(kFull, mine == 2);
+        const int at = boxes + __popc(one & lanemask_lt()) + __popc(two & lanemask_lt());
+        boxes += __popc(one) + __popc(two);
+        const int row = (e * R + r) * Tr + lo - (end - c);
+        if (box && mine >= 1 && at < kBoxes) box[at] = make_int3(row, lo - m0, lg);
+        if (box && mine == 2 && at + 1 < kBoxes) box[at + 1] = make_int3(row + len - size, lo - m0 + len - size, lg);
+        bytes += __reduce_add_sync(kFull, (unsigned)(mine * size * kBlock));
+    }
+    __syncwarp();
+    return boxes;
+}
+
 template <bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
-    expert_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ CUtensorMap map_w) {
-    extern __shared__ unsigned char raw[];
-    ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    expert_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ ExpertMaps maps) {
+    extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
+    ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw);
     constexpr int S = kStages, NB = 2;
     static_assert(offsetof(ExpertShared, rows_full) % 8 == 0 && offsetof(ExpertShared, w_scale) % 8 == 0, "");
-    const Dims &d = a.d;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = (int)d.E;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();                           // place in the pair
     const int kb_n = (int)(a.K / kBlock);
     const int n_cols = (int)(SWIGLU ? a.N / 2 : a.N);               // output columns
     const int tile_cols = SWIGLU ? kBlock : NB * kBlock;
-    const int col_tiles = (n_cols + tile_cols - 1) / tile_cols;
-    const int first_unit = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&s.rows_full[i], kCopyWarps * 32);
-            mbar_init(&s.full[i], 3);      // (the first CTA's) the bytes of both boxes, word of both CTAs' rows
+            mbar_init(&s.full[i], 3);      // (the first CTA's) the bytes of both CTAs' boxes, word of both CTAs' rows
             mbar_init(&s.done[i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&s.tempty[i], 16);   // (the first CTA's) the accumulating warps of both
+        for (int i = 0; i < kPlans; ++i) {
+            mbar_init(&s.plan_full[i], 1);
+            mbar_init(&s.plan_empty[i], kPlanUsers);
+        }
         mbar_init(&s.joined, 8);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -87,56 +152,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     cluster_sync();    // the other CTA's barriers are there too
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
-    const int units = s.list.first[E] * col_tiles;   // below 2^31: checked on the host
     volatile int *abort = &s.abort;
+
+    // the next unit's plan, for a whole warp; false after the last one (or an abort)
+    int slot = 0, pph = 0;
+    bool ok = true;
+    const auto next_plan = [&]() {
+        ok = warp_wait(&s.plan_full[slot], pph, abort);
+        return ok && s.plan[slot].e >= 0;
+    };
+    const auto plan_used = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.plan_empty[slot]);
+        if (++slot == kPlans) { slot = 0; pph ^= 1; }
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0) {
-            // ---- matrix rows ----
-            if (lane == 0) {
-                int st = 0, ph = 1, it = 0;
-                bool ok = true;
-                for (int u = first_unit; u < units && ok; u += step) {
-                    const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
-                    const int w_row = SWIGLU ? v.nb * kBlock + rank * n_cols : v.nb * tile_cols + rank * kBlock;
-                    for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                        ok = mbar_wait_or_abort(&s.done[st], ph, abort);
-                        if (!ok) break;
-                        if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kOperand);
-                        tma_load_3d<2>(s.buf[st] + kOperand, &map_w, kb * kBlock, w_row, v.e, cluster_addr(&s.full[st], 0));
-                        if (++st == S) { st = 0; ph ^= 1; }
-                    }
+            // ---- boxes: the matrix rows, and the rows where few boxes bring them ----
+            const uint32_t full = cluster_addr(&s.full[0], 0);
+            int st = 0, ph = 1, it = 0;
+            for (; next_plan(); plan_used()) {
+                const Plan &v = s.plan[slot];
+                const int3 x = s.box[slot][lane & (kBoxes - 1)];
+                const bool mine = lane < v.boxes;
+                const uint32_t expect = v.expect;
+                const int e = v.e, w_row = v.nb * tile_cols + rank * (SWIGLU ? n_cols : kBlock);
+                for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                    ok = warp_wait(&s.done[st], ph, abort);
+                    if (!ok) break;
+                    if (lane == 0 && rank == 0) mbar_expect_tx(&s.full[st], expect);
+                    __syncwarp();
+                    if (mine)
+                        tma_load_2d_pair(s.buf[st] + x.y * kBlock, &maps.a[x.z], kb * kBlock, x.x, full + st * 8);
+                    else if (lane == 31)
+                        tma_load_3d<2>(s.buf[st] + kOperand, &maps.w, kb * kBlock, w_row, e, full + st * 8);
+                    if (++st == S) { st = 0; ph ^= 1; }
                 }
-                // No copy may land after the pair has left.  Only where something gave up is one still in flight
-                // then: the first CTA's barriers count both boxes; the second gives its own a millisecond.
-                if (!ok) {
-                    if (rank == 0) {
-                        for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
-                    } else {
-                        const long long t0 = clock64();
-                        while (clock64() - t0 < (1 << 21)) {}
-                    }
+                if (!ok) break;
+            }
+            // No copy may land after the pair has left.  Only where something gave up is one still in flight then:
+            // the first CTA's barriers count both CTAs' boxes; the second gives its own a millisecond.
+            if (!ok) {
+                if (rank == 0) {
+                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
+                } else {
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < (1 << 21)) {}
                 }
             }
-            __syncwarp();
-        } else if (warp == 1 && rank == 0) {
+        } else if (warp == 1) {
             // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
             constexpr uint32_t idesc = mma_idesc(kPairRows, NB * kBlock);
             const bool issue = elect_one();
             const uint64_t desc = smem_desc(s.buf[0]);
             int st = 0, ph = 0, acc = 0, aph = 1, last = -1;
-            bool ok = true;
-            for (int u = first_unit; u < units && ok; u += step) {
-                for (int kb = 0; kb < kb_n; ++kb) {
-                    ok = mbar_wait_or_abort(&s.tempty[acc], aph, abort) && mbar_wait_or_abort(&s.full[st], ph, abort);
-                    ok = __all_sync(kFull, ok);
+            for (; next_plan(); plan_used()) {
+                for (int kb = 0; kb < (rank == 0 ? kb_n : 0); ++kb) {
+                    ok = warp_wait(&s.full[st], ph, abort) && warp_wait(&s.tempty[acc], aph, abort);
                     if (!ok) break;
                     tmem_fence_after();
                     if (issue) {
                         const uint64_t da = desc + (uint32_t)(st * (2 * kOperand >> 4)), db = da + (kOperand >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)   // 32 channels a step
+                        for (int k = 0; k < 4; ++k)   // 32 channels each
                             mma_f8<2>(tmem + acc * 256, da + k * 2, db + k * 2, idesc, k > 0);
                         mma_commit<2>(&s.done[st]);
                     }
@@ -145,26 +225,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                     acc ^= 1;
                     aph ^= acc == 0;
                 }
+                if (!ok) break;
             }
             if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
-            __syncwarp();
         } else if (warp == 2) {
-            // ---- word of this CTA's rows to the first CTA ----
-            if (lane == 0) {
-                const uint32_t full = cluster_addr(&s.full[0], 0);
-                int st = 0, ph = 0;
-                bool ok = true;
-                for (int u = first_unit; u < units && ok; u += step) {
-                    for (int kb = 0; kb < kb_n; ++kb) {
-                        ok = mbar_wait_or_abort(&s.rows_full[st], ph, abort);
-                        if (!ok) break;
-                        fence_async_shared();
-                        mbar_arrive_cluster(full + st * 8);
-                        if (++st == S) { st = 0; ph ^= 1; }
-                    }
+            // ---- word of this CTA's copied rows and scales to the first CTA ----
+            const uint32_t full = cluster_addr(&s.full[0], 0);
+            int st = 0, ph = 0;
+            for (; next_plan(); plan_used()) {
+                for (int kb = 0; kb < kb_n; ++kb) {
+                    ok = warp_wait(&s.rows_full[st], ph, abort);
+                    if (!ok) break;
+                    fence_async_shared();
+                    if (lane == 0) mbar_arrive_cluster(full + st * 8);
+                    if (++st == S) { st = 0; ph ^= 1; }
                 }
+                if (!ok) break;
             }
-            __syncwarp();
+        } else {
+            // ---- plans ----
+            const int E = (int)a.d.E, col_tiles = (n_cols + tile_cols - 1) / tile_cols;
+            const int units = s.list.first[E] * col_tiles;     // below 2^31: checked on the host
+            int u = blockIdx.x >> 1;
+            while (true) {
+                // (after a round of the plans, the users of the one before have finished with it)
+                ok = warp_wait(&s.plan_empty[slot], pph ^ 1, abort);
+                if (!ok) break;
+                const bool more = u < units;
+                if (more) {
+                    const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
+                    const int m0 = v.m0 + rank * kBlock, n = clamp_rows(v.rows - rank * kBlock);
+                    uint32_t bytes, other;
+                    const int boxes = list_boxes(s.box[slot], a, v.e, m0, n, bytes);
+                    const int most = max(boxes, list_boxes(nullptr, a, v.e, v.m0 + (rank ^ 1) * kBlock,
+                                                           clamp_rows(v.rows - (rank ^ 1) * kBlock), other));
+                    const int m[4] = {m0 + lane, m0 + lane + 32, m0 + lane + 64, m0 + lane + 96};
+                    int row[4];
+                    receive_rows(a, v.e, m, row);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s.row[slot][lane + 32 * i] = row[i];
+                    if (lane == 0)
+                        s.plan[slot] = Plan{v.e, v.nb, n, most <= kBoxes ? boxes : -1,
+                                            2 * kOperand + (most <= kBoxes ? bytes + other : 0)};
+                } else if (lane == 0) {
+                    s.plan[slot].e = -1;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.plan_full[slot]);
+                if (!more) break;
+                if (++slot == kPlans) { slot = 0; pph ^= 1; }
+                u += gridDim.x >> 1;
+            }
         }
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
@@ -173,39 +284,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         static_assert(kMine == 8, "32 rows a warp: one scale a lane");
         const int part = (warp - 4) * 4 + (lane >> 3), piece = lane & 7;
         const int place = (lane >> 2) * kStep + (warp - 4) * 4 + (lane & 3);      // the row whose scale this lane copies
-        const int n_blocks = (int)((a.N + kBlock - 1) / kBlock);
+        const uint32_t K = (uint32_t)a.K;
         int st = 0, ph = 1, ring = 0;
-        bool ok = true;
-        for (int u = first_unit; u < units && ok; u += step) {
-            const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
-            // offsets in blocks of 128 channels, of the rows and so of their scales (below 2^32)
-            int m[kMine + 1], row[kMine + 1];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) m[i] = v.m0 + rank * kBlock + i * kStep + part;
-            m[kMine] = v.m0 + rank * kBlock + place;
-            const int n = v.rows - rank * kBlock;     // this CTA's rows (128 or fewer, or none)
-            receive_rows(a, v.e, m, row);
-#pragma unroll
-            for (int i = 0; i <= kMine; ++i) row[i] *= kb_n;
-            const int blk = SWIGLU ? v.nb : v.nb * NB;
+        for (; next_plan(); plan_used()) {
+            const Plan &v = s.plan[slot];
+            const int n = v.rows, copies = (v.boxes < 0 ? n : 0) - part;
+            const int *rows = s.row[slot];
+            // offsets of the scales, in blocks of 128 channels (below 2^32: 128 bytes of an operand have one)
+            const uint32_t sc = (uint32_t)rows[place] * kb_n;
+            const int n_blocks = (int)((a.N + kBlock - 1) / kBlock), blk = SWIGLU ? v.nb : v.nb * NB;
             uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
             if (lane == 1) ws += SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;   // (zeros beyond N)
             for (int kb = 0; kb < kb_n; ++kb) {
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
+                ok = warp_wait(&s.done[st], ph, abort);
                 if (!ok) break;
                 const uint32_t dst = smem_addr(s.buf[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
                 const uint8_t *src = a.a + kb * kBlock + piece * 16;
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
-                    if (i * kStep < n - part)
-                        cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)row[i] * kBlock);
-                if (place < n)
-                    cp_async4(smem_addr(&s.row_scale[ring][place]), a.a_scales + (uint32_t)(row[kMine] + kb));
+                    if (i * kStep < copies)
+                        cp_async16(dst + i * kStep * kBlock, src + (uint64_t)(uint32_t)rows[i * kStep + part] * K);
+                if (place < n) cp_async4(smem_addr(&s.row_scale[ring][place]), a.a_scales + (sc + kb));
                 if (warp == 4 && lane < 2) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
                 cp_async_arrive(&s.rows_full[st]);
                 if (++st == S) { st = 0; ph ^= 1; }
                 ring = (ring + 1) % kScaleRing;
             }
+            if (!ok) break;
         }
         cp_async_wait_all();
     } else {
@@ -215,24 +320,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         const int r = quarter * 32 + lane;
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + half * 64;
         const uint32_t tempty = cluster_addr(&s.tempty[0], 0);
-        int st = 0, ph = 0, p = 0, ring = 0, unit = 0;
-        bool ok = true;
-        for (int u = first_unit; u < units && ok; u += step, ++unit) {
-            const Unit v = find_unit(s.list, E, kPairRows, col_tiles, u);
-            const bool some = rank * kBlock + quarter * 32 < v.rows;     // rows in this warp's lanes
-            const bool live = rank * kBlock + r < v.rows;
-            const int m[1] = {v.m0 + min(rank * kBlock + r, v.rows - 1)};
-            int rows[1];
-            receive_rows(a, v.e, m, rows);
-            const int row = rows[0];
+        int it = 0, unit = 0;       // (one counter of steps: registers are short here)
+        for (; next_plan(); plan_used(), ++unit) {
+            const bool some = quarter * 32 < s.plan[slot].rows;     // rows in this warp's lanes
             uint64_t acc[NB][32];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) acc[b][c] = 0;
-            for (int kb = 0; kb < kb_n; ++kb) {
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
+            for (int end = it + kb_n; it < end; ++it) {
+                ok = warp_wait(&s.done[it % S], it / S & 1, abort);
                 if (!ok) break;
+                const int p = it & 1, ring = it % kScaleRing;
                 if (some) {
                     tmem_fence_after();
                     const float sr = s.row_scale[ring][r];
@@ -254,11 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 } else if (lane == 0) {
                     mbar_arrive_cluster(tempty + p * 8);
                 }
-                if (++st == S) { st = 0; ph ^= 1; }
-                p ^= 1;
-                ring = (ring + 1) % kScaleRing;
             }
             if (!ok) break;
+            const Plan &v = s.plan[slot];
+            const bool live = r < v.rows;
+            const int64_t row = s.row[slot][r];
             if (SWIGLU) {
                 // gate in acc[0], up in acc[NB - 1]; the cast's maximum over 128 channels joins the two warpgroups
                 float amax = 0.f;
@@ -280,13 +379,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 s.amax[unit & 1][half][r] = amax;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.joined);
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.joined, unit & 1, abort));
+                ok = warp_wait(&s.joined, unit & 1, abort);
                 if (!ok) break;
                 const float other = s.amax[unit & 1][half ^ 1][r];
                 amax = amax != amax || other != other ? __uint_as_float(0x7fffffffu) : fmaxf(amax, other);
                 if (live) {
                     const float inv = amax > 0.f ? fminf(448.f / amax, 3.402823466e38f) : 0.f;
-                    uint8_t *q = a.q + (int64_t)row * n_cols + v.nb * kBlock + half * 64;
+                    uint8_t *q = a.q + row * n_cols + v.nb * kBlock + half * 64;
                     uint32_t o[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
@@ -295,13 +394,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         st_v4(q + 16 * c, make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
-                    if (half == 0) a.q_scales[(int64_t)row * (n_cols / kBlock) + v.nb] = amax / 448.f;
+                    if (half == 0) a.q_scales[row * (n_cols / kBlock) + v.nb] = amax / 448.f;
                 }
             } else if (live) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const int n0 = v.nb * tile_cols + b * kBlock + half * 64;
-                    uint16_t *y = a.y + (int64_t)row * a.N + n0;
+                    uint16_t *y = a.y + row * a.N + n0;
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         if (n0 + 8 * c < n_cols)
@@ -325,8 +424,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
 }
 
 template <bool SWIGLU>
-cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t st) {
-    constexpr int bytes = sizeof(ExpertShared) + 1024;
+cudaError_t launch(const ExpertArgs &a, const ExpertMaps &maps, cudaStream_t st) {
+    constexpr int bytes = sizeof(ExpertShared);
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
@@ -339,16 +438,21 @@ cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t s
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
-    expert_kernel<SWIGLU><<<num_sms() & ~1, kExpertThreads, bytes, st>>>(a, map_w);
+    expert_kernel<SWIGLU><<<num_sms() & ~1, kExpertThreads, bytes, st>>>(a, maps);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_expert_many(const ExpertArgs &a, cudaStream_t st) {
-    CUtensorMap map_w;
-    if (cudaError_t e = matrix_map(a, &map_w)) return e;
-    return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
+    ExpertMaps maps;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.d.E * a.d.T)}, strides[1] = {(cuuint64_t)a.K};
+    for (int i = 0; i < 8; ++i) {
+        const cuuint32_t box[2] = {kBlock, 1u << i};
+        if (cudaError_t e = encode_map(&maps.a[i], 2, a.a, dims, strides, box)) return e;
+    }
+    if (cudaError_t e = matrix_map(a, kBlock, &maps.w)) return e;
+    return a.q ? launch<true>(a, maps, st) : launch<false>(a, maps, st);
 }
 
 }  // namespace ep

@@ -108,11 +108,11 @@ __device__ __forceinline__ void receive_rows(const ExpertArgs &a, int e, const i
     }
 }
 
-// the matrices as a tensor map of bytes: boxes of 128 rows x 128 channels
-inline cudaError_t matrix_map(const ExpertArgs &a, CUtensorMap *map) {
+// the matrices as a tensor map of bytes: boxes of box_rows rows x 128 channels
+inline cudaError_t matrix_map(const ExpertArgs &a, int box_rows, CUtensorMap *map) {
     const cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.d.E};
     const cuuint64_t strides[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.N * a.K)};
-    const cuuint32_t box[3] = {kBlock, kBlock, 1};
+    const cuuint32_t box[3] = {kBlock, (cuuint32_t)box_rows, 1};
     return encode_map(map, 3, a.w, dims, strides, box);
 }
 

@@ -27,7 +27,7 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 512;                   // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
-constexpr int kIssueRegs = 72, kCopyRegs = 88, kAccRegs = 176;   // 72 + 88 + 2 * 176 = 4 * 128, the launch's registers
+constexpr int kIssueRegs = 80, kCopyRegs = 80, kAccRegs = 176;   // 80 + 80 + 2 * 176 = 4 * 128, the launch's registers
 constexpr int kRows = 64;                       // rows of a tile
 constexpr int kCopyThreads = 128;
 constexpr int kAcc = 4;                         // accumulators
@@ -59,8 +59,8 @@ struct FewShared {
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_few_kernel(const __grid_constant__ ExpertArgs a, const __grid_constant__ CUtensorMap map_w) {
-    extern __shared__ unsigned char raw[];
-    FewShared<SWIGLU> &s = *reinterpret_cast<FewShared<SWIGLU> *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
+    FewShared<SWIGLU> &s = *reinterpret_cast<FewShared<SWIGLU> *>(raw);
     constexpr int S = kStages<SWIGLU>, NB = SWIGLU ? 2 : 1;
     static_assert(offsetof(FewShared<SWIGLU>, rows) % 1024 == 0 && offsetof(FewShared<SWIGLU>, rows_full) % 8 == 0, "");
     static_assert(offsetof(FewShared<SWIGLU>, row_scale) % 16 == 0 && offsetof(FewShared<SWIGLU>, amax) % 16 == 0, "");
@@ -127,8 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
                 const uint32_t idesc = mma_idesc(kBlock, (v.rows + 15) & ~15);
                 for (int kb = 0; kb < kb_n; ++kb) {
-                    ok = mbar_wait_or_abort(&s.tempty[acc], aph, abort) && mbar_wait_or_abort(&s.full[st], ph, abort);
-                    ok = __all_sync(kFull, ok);
+                    ok = warp_wait(&s.full[st], ph, abort) && warp_wait(&s.tempty[acc], aph, abort);
                     if (!ok) break;
                     tmem_fence_after();
                     if (issue) {
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 1) ws += n_blocks / 2 * kb_n;             // (SwiGLU: the up block's)
             const bool has_scale = warp < 6 && place < v.rows;
             for (int kb = 0; kb < kb_n; ++kb) {
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
+                ok = warp_wait(&s.done[st], ph, abort);
                 if (!ok) break;
                 const uint32_t dst = smem_addr(s.rows[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
                 const uint8_t *src = a.a + kb * kBlock + piece * 16;
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kMine / 2; ++c) acc[c] = 0;
             for (int kb = 0; kb < kb_n; ++kb) {
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.done[st], ph, abort));
+                ok = warp_wait(&s.done[st], ph, abort);
                 if (!ok) break;
                 tmem_fence_after();
                 uint32_t t[kMine];
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.swapped);
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.swapped, unit & 1, abort));
+                ok = warp_wait(&s.swapped, unit & 1, abort);
                 if (!ok) break;
                 const int n = min(v.rows - half * H, H);   // rows among this warpgroup's columns (may be negative)
                 uint32_t top = 0;                          // lane c: of column c
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < n) s.amax[half * H + lane][quarter] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.joined);
-                ok = __all_sync(kFull, mbar_wait_or_abort(&s.joined, unit & 1, abort));
+                ok = warp_wait(&s.joined, unit & 1, abort);
                 if (!ok) break;
                 float inv = 0.f;                           // lane c: of column c
                 if (lane < n) {
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool SWIGLU>
 cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t st) {
-    constexpr int bytes = sizeof(FewShared<SWIGLU>) + 1024;
+    constexpr int bytes = sizeof(FewShared<SWIGLU>);
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
@@ -349,7 +348,7 @@ cudaError_t launch(const ExpertArgs &a, const CUtensorMap &map_w, cudaStream_t s
 
 cudaError_t launch_expert_few(const ExpertArgs &a, cudaStream_t st) {
     CUtensorMap map_w;
-    if (cudaError_t e = matrix_map(a, &map_w)) return e;
+    if (cudaError_t e = matrix_map(a, kBlock, &map_w)) return e;
     return a.q ? launch<true>(a, map_w, st) : launch<false>(a, map_w, st);
 }
 
