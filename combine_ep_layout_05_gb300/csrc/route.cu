@@ -5,6 +5,14 @@
 // l * V + V - 1 in registers (V a power of two, 32 V >= E), so a row is read
 // once and "lowest index first" is lane order.  Keys are compared as
 // unsigned words in the order of the floats; 0 stands for "not eligible".
+//
+// The memory traffic is small (a row read, k pairs written); what takes the
+// time is instructions: the scores (an exponential and a reciprocal for each
+// expert) and the choice.  The choice sorts each lane's keys once (blocks of
+// eight, a network of minima and maxima without the indices), after which
+// each of the k rounds is one warp maximum over the lanes' heads, a ballot for
+// the lowest lane that has it, and a shift of that lane's list; lane j notes
+// the key and the lane of round j and looks its index up at the end.
 #include "ep_internal.cuh"
 
 namespace ep {
@@ -12,6 +20,7 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWarps = 4;
+constexpr float kMaxFinite = 3.402823466e38f;
 
 // order-preserving word of a float that is neither NaN nor -inf (always > 0)
 __device__ __forceinline__ uint32_t order_word(float f) {
@@ -29,133 +38,252 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
 }
+// maximum of numbers (not NaN) as the maximum of their words
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
+    const uint32_t w = v > -INFINITY ? order_word(v) : 0;
+    const uint32_t m = __reduce_max_sync(kFull, w);
+    return m ? order_float(m) : -INFINITY;
 }
 
-template <typename L>
-__device__ __forceinline__ float load_logit(const L *p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float *p) { return *p; }
-template <>
-__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ void narrow(float v, float &out) { out = v; }
+__device__ __forceinline__ void narrow(float v, uint16_t &out) { out = (uint16_t)pack_bf16x2(v, 0.f); }
 
+// widest vector that V elements of a lane make up
+template <int BYTES> struct Vec { typedef uint4 T; };
+template <> struct Vec<8> { typedef uint2 T; };
+template <> struct Vec<4> { typedef uint32_t T; };
+template <> struct Vec<2> { typedef uint16_t T; };
+
+// A lane's V elements of a row of E; elements beyond E read as -inf.  vec:
+// E = 32 V and every row aligned to the vector.
 template <typename L, int V>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
+__device__ __forceinline__ void load_lane(const L *row, int E, bool vec, float (&x)[V]) {
+    const int lane = threadIdx.x & 31;
+    if (vec) {
+        typedef typename Vec<(sizeof(L) * V > 16 ? 16 : sizeof(L) * V)>::T W;
+        constexpr int N = sizeof(L) * V / sizeof(W);
+        union { W w[N]; L l[V]; } u;
+#pragma unroll
+        for (int i = 0; i < N; ++i) u.w[i] = __ldg(reinterpret_cast<const W *>(row + lane * V) + i);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = widen(u.l[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = lane * V + i < E ? widen(row[lane * V + i]) : -INFINITY;
+    }
+}
+template <typename L, int V>
+__device__ __forceinline__ void store_lane(L *row, int E, bool vec, const float (&x)[V]) {
+    const int lane = threadIdx.x & 31;
+    if (vec) {
+        typedef typename Vec<(sizeof(L) * V > 16 ? 16 : sizeof(L) * V)>::T W;
+        constexpr int N = sizeof(L) * V / sizeof(W);
+        union { W w[N]; L l[V]; } u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) narrow(x[i], u.l[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) reinterpret_cast<W *>(row + lane * V)[i] = u.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane * V + i < E) narrow(x[i], row[lane * V + i]);
+    }
+}
+
+__device__ __forceinline__ void order2(uint32_t &a, uint32_t &b) {
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+// Descending order of 2, 4 or 8 words (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_words(uint32_t *w) {
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+        for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(w[i + j], w[i + j + k]);
+}
+
+// Clears the keys of the groups that are not among the best.  Any split of
+// the experts: groups one after the other, scores kept by lane g % 32.
+template <int V>
+__device__ __forceinline__ void keep_groups(const RouteArgs &a, uint32_t (&key)[V]) {
+    const int lane = threadIdx.x & 31;
+    const int G = a.r.num_groups, per = (int)a.E / G, slots = (G + 31) / 32;
+    uint32_t score[kMaxExperts / 32], kept[kMaxExperts / 32];
+    for (int s = 0; s < slots; ++s) score[s] = kept[s] = 0;
+    for (int g = 0; g < G; ++g) {
+        const int lo = g * per, hi = lo + per;
+        uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            const uint32_t v = e >= lo && e < hi ? key[i] : 0;
+            b2 = max(b2, min(b1, v));
+            b1 = max(b1, v);
+        }
+        const uint32_t top = __reduce_max_sync(kFull, b1);
+        uint32_t w = top;
+        if (a.r.group_best == 2) {
+            const unsigned who = __ballot_sync(kFull, b1 == top);
+            const uint32_t second = __reduce_max_sync(kFull, lane == __ffs(who) - 1 ? b2 : b1);
+            if (top && second) w = order_word(order_float(top) + order_float(second));
+        }
+        if ((g & 31) == lane) score[g >> 5] = w;
+    }
+    for (int n = 0; n < a.r.topk_groups; ++n) {
+        uint32_t b = 0, at = 0x7fffffffu;
+        for (int s = 0; s < slots; ++s)
+            if (score[s] > b) { b = score[s]; at = s * 32 + lane; }
+        const uint32_t top = __reduce_max_sync(kFull, b);
+        if (!top) break;
+        const int g = (int)__reduce_min_sync(kFull, b == top ? at : 0x7fffffffu);
+        for (int s = 0; s < slots; ++s) {
+            if (g == s * 32 + lane) score[s] = 0;
+            if ((g >> 5) == s) kept[s] |= 1u << (g & 31);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int g = (lane * V + i) / per;
+        if (g >= G || !((kept[g >> 5] >> (g & 31)) & 1)) key[i] = 0;
+    }
+}
+
+// The same where a group is 32 / G whole lanes (E = 32 V, G divides 32): the
+// best two of a group meet in a butterfly, and a group is kept if fewer than
+// topk_groups groups are better.
+template <int V>
+__device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, uint32_t (&key)[V]) {
+    const int lane = threadIdx.x & 31;
+    const int G = a.r.num_groups, lanes = 32 / G;
+    uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        b2 = max(b2, min(b1, key[i]));
+        b1 = max(b1, key[i]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+        b2 = max(min(b1, o1), max(b2, o2));
+        b1 = max(b1, o1);
+    }
+    const uint32_t score =
+        a.r.group_best == 2 && b1 && b2 ? order_word(order_float(b1) + order_float(b2)) : b1;
+    int better = 0;
+    for (int l = 0; l < 32; l += lanes) {
+        const uint32_t other = __shfl_sync(kFull, score, l);
+        better += other > score || (other == score && l + lanes <= lane);
+    }
+    if (better >= a.r.topk_groups || !score) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = 0;
+    }
+}
+
+template <typename L, int V, bool SIG>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bool vec) {
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
     const int E = (int)a.E, k = (int)a.k;
-    const bool sig = a.r.scoring == EP_SCORE_SIGMOID;
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
-    float x[V];
+    float x[V], b[V];
     uint32_t key[V];
+    load_lane<L, V>(row, E, vec, x);
     bool nan = false;
 #pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = 0.f;
+    if (a.bias) load_lane<float, V>(a.bias, E, vec && ((uintptr_t)a.bias & 15) == 0, b);
+#pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        x[i] = e < E ? load_logit(row + e) : -INFINITY;
-        const float b = a.bias && e < E ? a.bias[e] : 0.f;
-        const float f = (sig ? sigmoid(x[i]) : x[i]) + b;
-        nan |= x[i] != x[i] || b != b;
-        const bool fit = x[i] > -INFINITY && f > -INFINITY;   // false for NaN
-        key[i] = fit ? order_word(f) : 0;
+        const float f = (SIG ? sigmoid(x[i]) : x[i]) + b[i];
+        nan |= f != f;
+        key[i] = x[i] > -INFINITY && f > -INFINITY ? order_word(f) : 0;   // comparisons are false for NaN
     }
-    if (nan) raise_status(a.dev_status, EP_STATUS_BAD_LOGIT);
+    if (nan) {                // (infinities of opposite signs also add to NaN; they only make an expert ineligible)
+        nan = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) nan |= x[i] != x[i] || b[i] != b[i];
+        if (nan) raise_status(a.dev_status, EP_STATUS_BAD_LOGIT);
+    }
 
     float m = 0.f, z = 1.f;   // softmax over the logits that are numbers
-    if (!sig && !a.r.renormalize) {
+    if (!SIG && !a.r.renormalize) {
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (x[i] > -INFINITY) m = fmaxf(m, fminf(x[i], 3.402823466e38f));
+            if (x[i] > -INFINITY) m = fmaxf(m, fminf(x[i], kMaxFinite));
         m = warp_max(m);
         z = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (x[i] > -INFINITY) z += expf(fminf(x[i], 3.402823466e38f) - m);
+            if (x[i] > -INFINITY) z += expf(fminf(x[i], kMaxFinite) - m);
         z = warp_sum(z);
     }
-
     const int G = a.r.num_groups;
-    if (G > 1 && a.r.topk_groups < G) {
-        // scores of the groups: lane g % 32 keeps group g's word
-        const int per = E / G;
-        uint32_t score[kMaxExperts / 32];
-        for (int s = 0; s < (G + 31) / 32; ++s) score[s] = 0;
-        for (int g = 0; g < G; ++g) {
-            const int lo = g * per, hi = lo + per;
-            uint32_t b1 = 0, b2 = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane * V + i;
-                const uint32_t v = e >= lo && e < hi ? key[i] : 0;
-                if (v > b1) { b2 = b1; b1 = v; }
-                else if (v > b2) b2 = v;
-            }
-            const uint32_t top = __reduce_max_sync(kFull, b1);
-            uint32_t w = top;
-            if (a.r.group_best == 2) {
-                const unsigned who = __ballot_sync(kFull, b1 == top);
-                const bool mine = lane == __ffs(who) - 1;
-                const uint32_t second = __reduce_max_sync(kFull, mine ? b2 : b1);
-                if (top && second) w = order_word(order_float(top) + order_float(second));
-            }
-            if ((g & 31) == lane) score[g >> 5] = w;
-        }
-        // the topk_groups best, lowest group first among equals
-        uint32_t kept[kMaxExperts / 32];
-        for (int s = 0; s < (G + 31) / 32; ++s) kept[s] = 0;
-        for (int n = 0; n < a.r.topk_groups; ++n) {
-            uint32_t b = 0;
-            int at = 0x7fffffff;
-            for (int s = 0; s < (G + 31) / 32; ++s)
-                if (score[s] > b) { b = score[s]; at = s * 32 + lane; }
-            const uint32_t top = __reduce_max_sync(kFull, b);
-            if (!top) break;
-            const int g = (int)__reduce_min_sync(kFull, b == top ? (unsigned)at : 0x7fffffffu);
-            for (int s = 0; s < (G + 31) / 32; ++s) {
-                if (g == s * 32 + lane) score[s] = 0;
-                if ((g >> 5) == s) kept[s] |= 1u << (g & 31);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int g = (lane * V + i) / per;
-            if (g >= G || !((kept[g >> 5] >> (g & 31)) & 1)) key[i] = 0;
-        }
+    if (a.r.topk_groups < G) {
+        if (E == 32 * V && G <= 32 && 32 % G == 0) keep_lane_groups<V>(a, key);
+        else keep_groups<V>(a, key);
     }
 
-    // k times the largest key; lane j keeps entry j
-    int id = -1;
-    float xj = -INFINITY;
+    constexpr int N = V < 8 ? V : 8, B = V / N;   // sorted blocks of a lane
+    uint32_t list[B][N];
+#pragma unroll
+    for (int c = 0; c < B; ++c) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) list[c][i] = key[c * N + i];
+        sort_words<N>(list[c]);
+    }
+    uint32_t mine = 0;        // of round j = lane: the key, and the lane that had it
+    int from = 0;
     for (int j = 0; j < k; ++j) {
-        uint32_t b = 0;
-        int at = 0;
-        float bx = 0.f;
+        uint32_t head = list[0][0];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > b) { b = key[i]; at = i; bx = x[i]; }
-        const uint32_t top = __reduce_max_sync(kFull, b);
+        for (int c = 1; c < B; ++c) head = max(head, list[c][0]);
+        const uint32_t top = __reduce_max_sync(kFull, head);
         if (!top) break;
-        const int win = __ffs(__ballot_sync(kFull, b == top)) - 1;
-        const int e = win * V + __shfl_sync(kFull, at, win);
-        const float ex = __shfl_sync(kFull, bx, win);
-        if (lane == j) { id = e; xj = ex; }
-        if (lane == win) {
+        const int win = __ffs(__ballot_sync(kFull, head == top)) - 1;
+        if (lane == j) { mine = top; from = win; }
+        bool pop = lane == win;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == at) key[i] = 0;
+        for (int c = 0; c < B; ++c) {
+            if (pop && (B == 1 || list[c][0] == top)) {
+#pragma unroll
+                for (int i = 0; i + 1 < N; ++i) list[c][i] = list[c][i + 1];
+                list[c][N - 1] = 0;
+                pop = false;
+            }
         }
     }
+    // The index: the lane's n-th key of that value, n the earlier rounds with the same key and lane.
+    int n = 0;
+    for (int j = 0; j + 1 < k; ++j) {
+        const uint32_t other = __shfl_sync(kFull, mine, j);
+        const int of = __shfl_sync(kFull, from, j);
+        n += j < lane && other == mine && of == from;
+    }
+    int id = -1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t w = __shfl_sync(kFull, key[i], from);
+        if (mine && w == mine && n-- == 0) id = from * V + i;
+    }
+
     float s = 0.f;
-    if (sig) {
+    float xj = id >= 0 ? widen(__ldg(row + id)) : -INFINITY;
+    if (SIG) {
         s = id >= 0 ? sigmoid(xj) : 0.f;
     } else {
-        xj = fminf(xj, 3.402823466e38f);
-        if (a.r.renormalize) m = warp_max(id >= 0 ? xj : -INFINITY);
+        xj = fminf(xj, kMaxFinite);
+        if (a.r.renormalize) m = warp_max(xj);
         s = id >= 0 ? expf(xj - m) : 0.f;
     }
     if (a.r.renormalize) z = warp_sum(s);
@@ -165,15 +293,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     }
 }
 
-template <typename L>
-__device__ __forceinline__ void store_grad(L *p, float v);
-template <>
-__device__ __forceinline__ void store_grad<float>(float *p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void store_grad<uint16_t>(uint16_t *p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.f); }
-
-template <typename L, int V>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a, const int64_t *topk_idx) {
+// DENSE: softmax without renormalisation, where every logit has a gradient and
+// the row is read; otherwise only the chosen logits are.  The row of the
+// gradient is written whole (zeros, or the dense part), then lane j writes the
+// value of entry j over it.
+template <typename L, int V, bool DENSE>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a, const int64_t *topk_idx, bool vec,
+                                                                         bool vec_out) {
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -181,28 +307,27 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     const bool sig = a.r.scoring == EP_SCORE_SIGMOID, norm = a.r.renormalize;
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
     L *out = reinterpret_cast<L *>(a.grad_logits) + t * a.grad_stride;
+    float x[V];
+    if (DENSE) load_lane<L, V>(row, E, vec, x);
     const int64_t id = lane < k ? topk_idx[t * k + lane] : -1;
     float g = lane < k ? a.grad_weights[t * k + lane] * a.r.scale : 0.f;
     const bool in_range = id >= 0 && id < E;
     int st = id != -1 && !in_range ? EP_STATUS_BAD_EXPERT : 0;
-    const unsigned same = __match_any_sync(kFull, in_range ? (long long)id : -2 - lane);
+    const unsigned same = __match_any_sync(kFull, in_range ? (int)id : -2 - lane);
     const bool dup = in_range && (same & lanemask_lt());
     if (dup) st |= EP_STATUS_DUP_EXPERT;
     if (st) raise_status(a.dev_status, st);
-    float xj = in_range && !dup ? load_logit(row + id) : -INFINITY;
+    float xj = in_range && !dup ? widen(__ldg(row + id)) : -INFINITY;
     const bool kept = xj > -INFINITY;
     if (!kept) g = 0.f;
-    float x[V];
     float m = 0.f, inv_z = 1.f;
-    if (!sig) xj = fminf(xj, 3.402823466e38f);
+    if (!sig) xj = fminf(xj, kMaxFinite);
     if (!sig && norm) m = warp_max(kept ? xj : -INFINITY);
-    if (!sig && !norm) {
+    if (DENSE) {
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            x[i] = e < E ? load_logit(row + e) : -INFINITY;
-            x[i] = x[i] > -INFINITY ? fminf(x[i], 3.402823466e38f) : -INFINITY;
+            x[i] = x[i] > -INFINITY ? fminf(x[i], kMaxFinite) : -INFINITY;
             m = fmaxf(m, x[i]);
         }
         m = warp_max(m);
@@ -219,8 +344,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     float ds = g;
     if (norm) {
         const float total = warp_sum(s), inv = total > 0.f ? 1.f / total : 0.f;
-        ds = (g - warp_sum(g * s) * inv) * inv;
-        if (!kept) ds = 0.f;
+        const float mean = warp_sum(g * s) * inv;
+        ds = kept ? (g - mean) * inv : 0.f;
     }
     float mean = 0.f, v;
     if (sig) {
@@ -232,40 +357,60 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
         v = s * (ds - mean);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = !sig && !norm ? -(x[i] * inv_z) * mean : 0.f;
-    for (int j = 0; j < k; ++j) {
-        const int e = __shfl_sync(kFull, kept ? (int)id : -1, j);
-        const float vj = __shfl_sync(kFull, v, j);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e == lane * V + i) x[i] = vj;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (lane * V + i < E) store_grad(out + lane * V + i, x[i]);
+    for (int i = 0; i < V; ++i) x[i] = DENSE ? -(x[i] * inv_z) * mean : 0.f;
+    store_lane<L, V>(out, E, vec_out, x);
+    __syncwarp();
+    if (kept) narrow(v, out[id]);
+}
+
+// rows of a lane's V elements can be moved as vectors
+bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size) {
+    if (E & (E - 1) || E < 32) return false;                    // E = 32 V
+    const int64_t bytes = E / 32 * size, w = bytes > 16 ? 16 : bytes;
+    return (uintptr_t)p % w == 0 && stride * size % w == 0;
 }
 
 }  // namespace
 
-#define EP_ROUTE_CASES(KERNEL, L, ...)                                            \
-    if (a.E <= 32) KERNEL<L, 1><<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__);  \
-    else if (a.E <= 64) KERNEL<L, 2><<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__);   \
-    else if (a.E <= 128) KERNEL<L, 4><<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__);  \
-    else if (a.E <= 256) KERNEL<L, 8><<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__);  \
-    else if (a.E <= 512) KERNEL<L, 16><<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__); \
-    else KERNEL<L, 32><<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__);
+// The kernel for V = 1, 2, 4, .. 32 experts a lane
+#define EP_ROUTE_CASES(KERNEL, L, FLAG, ...)                                                    \
+    do {                                                                                        \
+        const unsigned b = kRouteWarps * 32;                                                    \
+        if (a.E <= 32) KERNEL<L, 1, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);                     \
+        else if (a.E <= 64) KERNEL<L, 2, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);                \
+        else if (a.E <= 128) KERNEL<L, 4, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);               \
+        else if (a.E <= 256) KERNEL<L, 8, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);               \
+        else if (a.E <= 512) KERNEL<L, 16, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);              \
+        else KERNEL<L, 32, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);                              \
+    } while (0)
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    if (a.bf16) { EP_ROUTE_CASES(route_kernel, uint16_t, a) }
-    else { EP_ROUTE_CASES(route_kernel, float, a) }
+    const bool vec = rows_vectorised(a.logits, a.stride, a.E, a.bf16 ? 2 : 4);
+    const bool sig = a.r.scoring == EP_SCORE_SIGMOID;
+    if (a.bf16) {
+        if (sig) EP_ROUTE_CASES(route_kernel, uint16_t, true, a, vec);
+        else EP_ROUTE_CASES(route_kernel, uint16_t, false, a, vec);
+    } else {
+        if (sig) EP_ROUTE_CASES(route_kernel, float, true, a, vec);
+        else EP_ROUTE_CASES(route_kernel, float, false, a, vec);
+    }
     return cudaGetLastError();
 }
 
 cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    if (a.bf16) { EP_ROUTE_CASES(route_backward_kernel, uint16_t, a, topk_idx) }
-    else { EP_ROUTE_CASES(route_backward_kernel, float, a, topk_idx) }
+    const int size = a.bf16 ? 2 : 4;
+    const bool vec = rows_vectorised(a.logits, a.stride, a.E, size);
+    const bool vec_out = rows_vectorised(a.grad_logits, a.grad_stride, a.E, size);
+    const bool dense = a.r.scoring == EP_SCORE_SOFTMAX && !a.r.renormalize;
+    if (a.bf16) {
+        if (dense) EP_ROUTE_CASES(route_backward_kernel, uint16_t, true, a, topk_idx, vec, vec_out);
+        else EP_ROUTE_CASES(route_backward_kernel, uint16_t, false, a, topk_idx, vec, vec_out);
+    } else {
+        if (dense) EP_ROUTE_CASES(route_backward_kernel, float, true, a, topk_idx, vec, vec_out);
+        else EP_ROUTE_CASES(route_backward_kernel, float, false, a, topk_idx, vec, vec_out);
+    }
     return cudaGetLastError();
 }
 
