@@ -5,6 +5,11 @@
 // same chunk of up to 8 rows of y, adds to its part of each row's dot
 // product, and writes the scaled chunk to each row of grad_y.  The parts meet
 // in a fixed order (lanes by halving, then warps in order): no atomics.
+//
+// Bound by memory: each row of y is read once and each row of grad_y written
+// once.  32768 tokens rank-major, hidden 7168: 800 us, 6.8 TB/s, the copy rate;
+// 1024 tokens expert-major: 46 us, 5.4 TB/s (the launch and three dependent
+// loads before the rows are known are 9 us of it).
 #include "combine_device.cuh"
 
 namespace ep {
@@ -12,12 +17,19 @@ namespace ep {
 namespace {
 
 constexpr int kBackRows = 8;   // rows a pass keeps in flight
+// Tokens an SM below which a token gets eight warps.  Measured (hidden 7168,
+// top-8, expert-major): 256 tokens 13.1 us with eight warps and 16.8 with four,
+// 512 tokens 25.0 and 21.5, 1024 tokens 47.4 and 45.9 (seven blocks of four
+// warps fit an SM, so that 1024 tokens are one wave).
+#ifndef EP_COMBINE_BACK_TOKENS
+#define EP_COMBINE_BACK_TOKENS 3
+#endif
 
-template <int LAYOUT>
-__global__ void __launch_bounds__(kWarps * 32) combine_backward_kernel(CombineArgs a, const uint16_t *grad_out,
-                                                                      uint16_t *grad_y, float *grad_weights) {
+template <int LAYOUT, int W>
+__global__ void __launch_bounds__(W * 32) combine_backward_kernel(CombineArgs a, const uint16_t *grad_out,
+                                                                 uint16_t *grad_y, float *grad_weights) {
     __shared__ int64_t s_rows[kMaxTopk];
-    __shared__ float s_wts[kMaxTopk], s_dot[kWarps][kMaxTopk];
+    __shared__ float s_wts[kMaxTopk], s_dot[W][kMaxTopk];
     __shared__ int s_nd, s_entry[kMaxTopk];
     const Dims &d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -35,7 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_backward_kernel(CombineAr
     uint4 *gy = reinterpret_cast<uint4 *>(grad_y);
     for (int g0 = 0; g0 < nd; g0 += kBackRows) {
         float dot[kBackRows] = {};
-        for (int64_t c = threadIdx.x; c < hc; c += kWarps * 32) {
+        for (int64_t c = threadIdx.x; c < hc; c += W * 32) {
             uint4 v[kBackRows];
             if (grad_weights) {
 #pragma unroll
@@ -82,7 +94,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_backward_kernel(CombineAr
         const int i = s_entry[threadIdx.x];
         float v = 0.f;
         if (i >= 0)
-            for (int w = 0; w < kWarps; ++w) v += s_dot[w][i];
+            for (int w = 0; w < W; ++w) v += s_dot[w][i];
         grad_weights[t * d.k + threadIdx.x] = v;
     }
 }
@@ -91,11 +103,15 @@ __global__ void __launch_bounds__(kWarps * 32) combine_backward_kernel(CombineAr
 
 cudaError_t launch_combine_backward(int layout, const CombineArgs &a, const uint16_t *grad_out, uint16_t *grad_y,
                                     float *grad_weights, cudaStream_t st) {
-    const unsigned grid = (unsigned)a.d.T, block = kWarps * 32;
-    if (layout == EP_RANK_MAJOR)
-        combine_backward_kernel<EP_RANK_MAJOR><<<grid, block, 0, st>>>(a, grad_out, grad_y, grad_weights);
-    else
-        combine_backward_kernel<EP_EXPERT_MAJOR><<<grid, block, 0, st>>>(a, grad_out, grad_y, grad_weights);
+    const unsigned grid = (unsigned)a.d.T;
+    const bool few = a.d.T < (int64_t)num_sms() * EP_COMBINE_BACK_TOKENS;
+    if (layout == EP_RANK_MAJOR) {
+        if (few) combine_backward_kernel<EP_RANK_MAJOR, 8><<<grid, 256, 0, st>>>(a, grad_out, grad_y, grad_weights);
+        else combine_backward_kernel<EP_RANK_MAJOR, 4><<<grid, 128, 0, st>>>(a, grad_out, grad_y, grad_weights);
+    } else {
+        if (few) combine_backward_kernel<EP_EXPERT_MAJOR, 8><<<grid, 256, 0, st>>>(a, grad_out, grad_y, grad_weights);
+        else combine_backward_kernel<EP_EXPERT_MAJOR, 4><<<grid, 128, 0, st>>>(a, grad_out, grad_y, grad_weights);
+    }
     return cudaGetLastError();
 }
 

@@ -192,9 +192,17 @@ def _call(name, fn, args):
     _check(name, fn(*args))
 
 
+# handle of a device's current stream; the private call costs a tenth of the stream object's
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _ptr(t, dtype=None, name="tensor", numel=None):
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+            and (numel is None or t.numel() >= numel)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -210,7 +218,7 @@ def _ptr(t, dtype=None, name="tensor", numel=None):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 

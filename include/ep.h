@@ -444,7 +444,7 @@ int ep_route_backward(const ep_problem *p, const ep_router *r, int dtype, const 
  *   grad_y[row] = bf16( fp32( (sum_j topk_weights[t, j], in j order) *
  *   grad_out[t] ) ); rows the handle does not name are not written.
  *   grad_weights[t, j] = sum_h grad_out[t, h] * y[row, h], fp32, summed in an
- *   order that depends on H and k only; 0 for entries that are not kept.
+ *   order that depends on the sizes only; 0 for entries that are not kept.
  * grad_y [rows, H] bf16 or NULL, grad_weights [T, k] fp32 or NULL (y may be
  * NULL then): a NULL output is not computed.  grad_out, y and grad_y 16-byte
  * aligned; grad_y must not overlap y.
