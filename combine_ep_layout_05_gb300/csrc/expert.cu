@@ -29,6 +29,7 @@
 #include <cstddef>
 
 #include "expert_device.cuh"
+#include "vec8.cuh"
 
 namespace ep {
 
@@ -320,6 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         const int r = quarter * 32 + lane;
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + half * 64;
         const uint32_t tempty = cluster_addr(&s.tempty[0], 0);
+        // 32-byte stores where rows start at multiples of 32 bytes (a thread stores along its row, so that a warp's
+        // store touches 32 lines: 16 bytes each took twice as many)
+        const bool wide = SWIGLU ? ((uintptr_t)a.q & 31) == 0 : ((uintptr_t)a.y & 31) == 0 && n_cols % 16 == 0;
         int it = 0, unit = 0;       // (one counter of steps: registers are short here)
         for (; next_plan(); plan_used(), ++unit) {
             const bool some = quarter * 32 < s.plan[slot].rows;     // rows in this warp's lanes
@@ -392,8 +396,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                         o[c] = (uint32_t)pack_e4m3x2(lo2(acc[0][2 * c]) * inv, hi2(acc[0][2 * c]) * inv) |
                                (uint32_t)pack_e4m3x2(lo2(acc[0][2 * c + 1]) * inv, hi2(acc[0][2 * c + 1]) * inv) << 16;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        st_v4(q + 16 * c, make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t *p = o + 8 * c;
+                        if (wide) {
+                            const uint32_t v8[8] = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+                            st_v8(q + 32 * c, v8);
+                        } else {
+                            st_v4(q + 32 * c, make_uint4(p[0], p[1], p[2], p[3]));
+                            st_v4(q + 32 * c + 16, make_uint4(p[4], p[5], p[6], p[7]));
+                        }
+                    }
                     if (half == 0) a.q_scales[row * (n_cols / kBlock) + v.nb] = amax / 448.f;
                 }
             } else if (live) {
@@ -402,13 +414,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                     const int n0 = v.nb * tile_cols + b * kBlock + half * 64;
                     uint16_t *y = a.y + row * a.N + n0;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (n0 + 8 * c < n_cols)
-                            st_v4(y + 8 * c,
-                                  make_uint4(pack_bf16x2(lo2(acc[b][4 * c]), hi2(acc[b][4 * c])),
-                                             pack_bf16x2(lo2(acc[b][4 * c + 1]), hi2(acc[b][4 * c + 1])),
-                                             pack_bf16x2(lo2(acc[b][4 * c + 2]), hi2(acc[b][4 * c + 2])),
-                                             pack_bf16x2(lo2(acc[b][4 * c + 3]), hi2(acc[b][4 * c + 3]))));
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(lo2(acc[b][8 * c + i]), hi2(acc[b][8 * c + i]));
+                        if (wide) {
+                            if (n0 + 16 * c < n_cols) st_v8(y + 16 * c, o);
+                        } else {
+                            if (n0 + 16 * c < n_cols) st_v4(y + 16 * c, make_uint4(o[0], o[1], o[2], o[3]));
+                            if (n0 + 16 * c + 8 < n_cols) st_v4(y + 16 * c + 8, make_uint4(o[4], o[5], o[6], o[7]));
+                        }
+                    }
                 }
             }
         }
