@@ -33,9 +33,17 @@ __device__ __forceinline__ float order_float(uint32_t w) {
 
 __device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.f + expf(-x)); }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// sum, and maximum, over the W lanes of a token
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
     return v;
 }
 // maximum of numbers (not NaN) as the maximum of their words
@@ -57,10 +65,9 @@ template <> struct Vec<4> { typedef uint32_t T; };
 template <> struct Vec<2> { typedef uint16_t T; };
 
 // A lane's V elements of a row of E; elements beyond E read as -inf.  vec:
-// E = 32 V and every row aligned to the vector.
+// the lanes cover E exactly and every row is aligned to the vector.
 template <typename L, int V>
-__device__ __forceinline__ void load_lane(const L *row, int E, bool vec, float (&x)[V]) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void load_lane(const L *row, int E, int lane, bool vec, float (&x)[V]) {
     if (vec) {
         typedef typename Vec<(sizeof(L) * V > 16 ? 16 : sizeof(L) * V)>::T W;
         constexpr int N = sizeof(L) * V / sizeof(W);
@@ -75,8 +82,7 @@ __device__ __forceinline__ void load_lane(const L *row, int E, bool vec, float (
     }
 }
 template <typename L, int V>
-__device__ __forceinline__ void store_lane(L *row, int E, bool vec, const float (&x)[V]) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void store_lane(L *row, int E, int lane, bool vec, const float (&x)[V]) {
     if (vec) {
         typedef typename Vec<(sizeof(L) * V > 16 ? 16 : sizeof(L) * V)>::T W;
         constexpr int N = sizeof(L) * V / sizeof(W);
@@ -158,8 +164,8 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &a, uint32_t (&key)[
 }
 
 // The same where a group is 32 / G whole lanes (E = 32 V, G divides 32): the
-// best two of a group meet in a butterfly, and a group is kept if fewer than
-// topk_groups groups are better.
+// best two of a group meet in a butterfly, then topk_groups rounds take the best
+// score left.
 template <int V>
 __device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, uint32_t (&key)[V]) {
     const int lane = threadIdx.x & 31;
@@ -177,12 +183,18 @@ __device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, uint32_t (&
     }
     const uint32_t score =
         a.r.group_best == 2 && b1 && b2 ? order_word(order_float(b1) + order_float(b2)) : b1;
-    int better = 0;
-    for (int l = 0; l < 32; l += lanes) {
-        const uint32_t other = __shfl_sync(kFull, score, l);
-        better += other > score || (other == score && l + lanes <= lane);
+    uint32_t left = score;
+    bool keep = false;
+    for (int n = 0; n < a.r.topk_groups; ++n) {
+        const uint32_t top = __reduce_max_sync(kFull, left);
+        if (!top) break;
+        const int first = __ffs(__ballot_sync(kFull, left == top)) - 1;     // a group's lowest lane
+        if ((unsigned)(lane - first) < (unsigned)lanes) {
+            keep = true;
+            left = 0;
+        }
     }
-    if (better >= a.r.topk_groups || !score) {
+    if (!keep) {
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = 0;
     }
@@ -197,11 +209,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
     float x[V], b[V];
     uint32_t key[V];
-    load_lane<L, V>(row, E, vec, x);
+    load_lane<L, V>(row, E, lane, vec, x);
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = 0.f;
-    if (a.bias) load_lane<float, V>(a.bias, E, vec && ((uintptr_t)a.bias & 15) == 0, b);
+    if (a.bias) load_lane<float, V>(a.bias, E, lane, vec && ((uintptr_t)a.bias & 15) == 0, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float f = (SIG ? sigmoid(x[i]) : x[i]) + b[i];
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (x[i] > -INFINITY) z += expf(fminf(x[i], kMaxFinite) - m);
-        z = warp_sum(z);
+        z = lanes_sum<32>(z);
     }
     const int G = a.r.num_groups;
     if (a.r.topk_groups < G) {
@@ -263,13 +275,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
             }
         }
     }
-    // The index: the lane's n-th key of that value, n the earlier rounds with the same key and lane.
-    int n = 0;
-    for (int j = 0; j + 1 < k; ++j) {
-        const uint32_t other = __shfl_sync(kFull, mine, j);
-        const int of = __shfl_sync(kFull, from, j);
-        n += j < lane && other == mine && of == from;
-    }
+    // The index: the lane's n-th key of that value, n the earlier rounds with the same key and lane (which come one
+    // after the other).
+    const uint32_t before = __shfl_up_sync(kFull, mine, 1);
+    const int of = __shfl_up_sync(kFull, from, 1);
+    const unsigned fresh = __ballot_sync(kFull, lane == 0 || before != mine || of != from);
+    int n = lane - (31 - __clz(fresh & (lanemask_lt() | 1u << lane)));
     int id = -1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -286,34 +297,39 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
         if (a.r.renormalize) m = warp_max(xj);
         s = id >= 0 ? expf(xj - m) : 0.f;
     }
-    if (a.r.renormalize) z = warp_sum(s);
+    if (a.r.renormalize) z = lanes_sum<32>(s);
     if (lane < k) {
         a.topk_idx[t * k + lane] = id;
         a.topk_weights[t * k + lane] = id >= 0 && z > 0.f ? s / z * a.r.scale : 0.f;
     }
 }
 
+// W lanes own a token: 16 where they can (k <= 16, E <= 512), for two tokens a
+// warp, because the part that entries need (lane j: entry j) takes as many
+// instructions for two tokens as for one.
 // DENSE: softmax without renormalisation, where every logit has a gradient and
 // the row is read; otherwise only the chosen logits are.  The row of the
 // gradient is written whole (zeros, or the dense part), then lane j writes the
 // value of entry j over it.
-template <typename L, int V, bool DENSE>
+template <typename L, int W, int V, bool DENSE>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a, const int64_t *topk_idx, bool vec,
                                                                          bool vec_out) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-    if (t >= a.T) return;
+    const int lane = threadIdx.x & (W - 1);
+    const int64_t own = ((int64_t)blockIdx.x * kRouteWarps * 32 + threadIdx.x) / W;
+    const bool live = own < a.T;                 // (lanes beyond the last token repeat it and write nothing)
+    const int64_t t = live ? own : a.T - 1;
     const int E = (int)a.E, k = (int)a.k;
     const bool sig = a.r.scoring == EP_SCORE_SIGMOID, norm = a.r.renormalize;
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
     L *out = reinterpret_cast<L *>(a.grad_logits) + t * a.grad_stride;
     float x[V];
-    if (DENSE) load_lane<L, V>(row, E, vec, x);
+    if (DENSE) load_lane<L, V>(row, E, lane, vec, x);
     const int64_t id = lane < k ? topk_idx[t * k + lane] : -1;
     float g = lane < k ? a.grad_weights[t * k + lane] * a.r.scale : 0.f;
     const bool in_range = id >= 0 && id < E;
     int st = id != -1 && !in_range ? EP_STATUS_BAD_EXPERT : 0;
-    const unsigned same = __match_any_sync(kFull, in_range ? (int)id : -2 - lane);
+    const int wl = threadIdx.x & 31;
+    const unsigned same = __match_any_sync(kFull, in_range ? (int)id + (wl / W) * kMaxExperts : -2 - wl);
     const bool dup = in_range && (same & lanemask_lt());
     if (dup) st |= EP_STATUS_DUP_EXPERT;
     if (st) raise_status(a.dev_status, st);
@@ -322,29 +338,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     if (!kept) g = 0.f;
     float m = 0.f, inv_z = 1.f;
     if (!sig) xj = fminf(xj, kMaxFinite);
-    if (!sig && norm) m = warp_max(kept ? xj : -INFINITY);
+    if (!sig && norm) m = lanes_max<W>(kept ? xj : -INFINITY);
     if (DENSE) {
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = x[i] > -INFINITY ? fminf(x[i], kMaxFinite) : -INFINITY;
+            x[i] = x[i] > -INFINITY ? fminf(x[i], kMaxFinite) : -INFINITY;    // (NaN: takes no part)
             m = fmaxf(m, x[i]);
         }
-        m = warp_max(m);
+        m = lanes_max<W>(m);
+        const float base = m > -INFINITY ? m : 0.f;
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
+            x[i] = expf(x[i] - base);
             z += x[i];
         }
-        z = warp_sum(z);
+        z = lanes_sum<W>(z);
         inv_z = z > 0.f ? 1.f / z : 0.f;
     }
     const float s = !kept ? 0.f : sig ? sigmoid(xj) : expf(xj - m) * inv_z;
     float ds = g;
     if (norm) {
-        const float total = warp_sum(s), inv = total > 0.f ? 1.f / total : 0.f;
-        const float mean = warp_sum(g * s) * inv;
+        const float total = lanes_sum<W>(s), inv = total > 0.f ? 1.f / total : 0.f;
+        const float mean = lanes_sum<W>(g * s) * inv;
         ds = kept ? (g - mean) * inv : 0.f;
     }
     float mean = 0.f, v;
@@ -353,64 +370,79 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     } else if (norm) {
         v = s * ds;       // sum_j ds_j s_j = 0: the mean is already taken out
     } else {
-        mean = warp_sum(ds * s);
+        mean = lanes_sum<W>(ds * s);
         v = s * (ds - mean);
     }
+    const float f = -inv_z * mean;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = DENSE ? -(x[i] * inv_z) * mean : 0.f;
-    store_lane<L, V>(out, E, vec_out, x);
+    for (int i = 0; i < V; ++i) x[i] = DENSE ? x[i] * f : 0.f;
+    if (live) store_lane<L, V>(out, E, lane, vec_out, x);
     __syncwarp();
-    if (kept) narrow(v, out[id]);
+    if (kept && live) narrow(v, out[id]);
 }
 
 // rows of a lane's V elements can be moved as vectors
-bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size) {
-    if (E & (E - 1) || E < 32) return false;                    // E = 32 V
-    const int64_t bytes = E / 32 * size, w = bytes > 16 ? 16 : bytes;
+bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size, int lanes) {
+    if (E & (E - 1) || E < lanes) return false;                 // E = lanes * V
+    const int64_t bytes = E / lanes * size, w = bytes > 16 ? 16 : bytes;
     return (uintptr_t)p % w == 0 && stride * size % w == 0;
 }
 
 }  // namespace
 
-// The kernel for V = 1, 2, 4, .. 32 experts a lane
-#define EP_ROUTE_CASES(KERNEL, L, FLAG, ...)                                                    \
-    do {                                                                                        \
-        const unsigned b = kRouteWarps * 32;                                                    \
-        if (a.E <= 32) KERNEL<L, 1, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);                     \
-        else if (a.E <= 64) KERNEL<L, 2, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);                \
-        else if (a.E <= 128) KERNEL<L, 4, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);               \
-        else if (a.E <= 256) KERNEL<L, 8, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);               \
-        else if (a.E <= 512) KERNEL<L, 16, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);              \
-        else KERNEL<L, 32, FLAG><<<grid, b, 0, st>>>(__VA_ARGS__);                              \
+// The kernel for V = 1, 2, 4, .. 32 experts a lane, W lanes a token
+#define EP_ROUTE_CASES(W, KERNEL, ...)                                          \
+    do {                                                                        \
+        const int per = ((int)a.E + W - 1) / W;                                 \
+        if (per <= 1) EP_ROUTE_LAUNCH(W, 1, KERNEL, __VA_ARGS__);               \
+        else if (per <= 2) EP_ROUTE_LAUNCH(W, 2, KERNEL, __VA_ARGS__);          \
+        else if (per <= 4) EP_ROUTE_LAUNCH(W, 4, KERNEL, __VA_ARGS__);          \
+        else if (per <= 8) EP_ROUTE_LAUNCH(W, 8, KERNEL, __VA_ARGS__);          \
+        else if (per <= 16) EP_ROUTE_LAUNCH(W, 16, KERNEL, __VA_ARGS__);        \
+        else EP_ROUTE_LAUNCH(W, 32, KERNEL, __VA_ARGS__);                       \
     } while (0)
+#define EP_ROUTE_LAUNCH(W, V, KERNEL, ...) KERNEL(W, V)<<<grid, kRouteWarps * 32, 0, st>>>(__VA_ARGS__)
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    const bool vec = rows_vectorised(a.logits, a.stride, a.E, a.bf16 ? 2 : 4);
-    const bool sig = a.r.scoring == EP_SCORE_SIGMOID;
-    if (a.bf16) {
-        if (sig) EP_ROUTE_CASES(route_kernel, uint16_t, true, a, vec);
-        else EP_ROUTE_CASES(route_kernel, uint16_t, false, a, vec);
+    const bool vec = rows_vectorised(a.logits, a.stride, a.E, a.bf16 ? 2 : 4, 32);
+#define EP_ROUTE_BS(W, V) route_kernel<uint16_t, V, true>
+#define EP_ROUTE_BM(W, V) route_kernel<uint16_t, V, false>
+#define EP_ROUTE_FS(W, V) route_kernel<float, V, true>
+#define EP_ROUTE_FM(W, V) route_kernel<float, V, false>
+    if (a.r.scoring == EP_SCORE_SIGMOID) {
+        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BS, a, vec);
+        else EP_ROUTE_CASES(32, EP_ROUTE_FS, a, vec);
     } else {
-        if (sig) EP_ROUTE_CASES(route_kernel, float, true, a, vec);
-        else EP_ROUTE_CASES(route_kernel, float, false, a, vec);
+        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BM, a, vec);
+        else EP_ROUTE_CASES(32, EP_ROUTE_FM, a, vec);
     }
     return cudaGetLastError();
 }
 
 cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, cudaStream_t st) {
-    const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    const int size = a.bf16 ? 2 : 4;
-    const bool vec = rows_vectorised(a.logits, a.stride, a.E, size);
-    const bool vec_out = rows_vectorised(a.grad_logits, a.grad_stride, a.E, size);
+    const bool half = a.k <= 16 && a.E <= 512;
+    const int W = half ? 16 : 32, size = a.bf16 ? 2 : 4, tokens = kRouteWarps * 32 / W;
+    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
+    const bool vec = rows_vectorised(a.logits, a.stride, a.E, size, W);
+    const bool vec_out = rows_vectorised(a.grad_logits, a.grad_stride, a.E, size, W);
+#define EP_ROUTE_BD(W, V) route_backward_kernel<uint16_t, W, V, true>
+#define EP_ROUTE_BC(W, V) route_backward_kernel<uint16_t, W, V, false>
+#define EP_ROUTE_FD(W, V) route_backward_kernel<float, W, V, true>
+#define EP_ROUTE_FC(W, V) route_backward_kernel<float, W, V, false>
+#define EP_ROUTE_BACK(W)                                                             \
+    do {                                                                             \
+        if (dense) {                                                                 \
+            if (a.bf16) EP_ROUTE_CASES(W, EP_ROUTE_BD, a, topk_idx, vec, vec_out);   \
+            else EP_ROUTE_CASES(W, EP_ROUTE_FD, a, topk_idx, vec, vec_out);          \
+        } else {                                                                     \
+            if (a.bf16) EP_ROUTE_CASES(W, EP_ROUTE_BC, a, topk_idx, vec, vec_out);   \
+            else EP_ROUTE_CASES(W, EP_ROUTE_FC, a, topk_idx, vec, vec_out);          \
+        }                                                                            \
+    } while (0)
     const bool dense = a.r.scoring == EP_SCORE_SOFTMAX && !a.r.renormalize;
-    if (a.bf16) {
-        if (dense) EP_ROUTE_CASES(route_backward_kernel, uint16_t, true, a, topk_idx, vec, vec_out);
-        else EP_ROUTE_CASES(route_backward_kernel, uint16_t, false, a, topk_idx, vec, vec_out);
-    } else {
-        if (dense) EP_ROUTE_CASES(route_backward_kernel, float, true, a, topk_idx, vec, vec_out);
-        else EP_ROUTE_CASES(route_backward_kernel, float, false, a, topk_idx, vec, vec_out);
-    }
+    if (half) EP_ROUTE_BACK(16);
+    else EP_ROUTE_BACK(32);
     return cudaGetLastError();
 }
 
