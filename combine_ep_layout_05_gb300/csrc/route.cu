@@ -81,20 +81,50 @@ __device__ __forceinline__ void load_lane(const L *row, int E, int lane, bool ve
         for (int i = 0; i < V; ++i) x[i] = lane * V + i < E ? widen(row[lane * V + i]) : -INFINITY;
     }
 }
-template <typename L, int V>
-__device__ __forceinline__ void store_lane(L *row, int E, int lane, bool vec, const float (&x)[V]) {
-    if (vec) {
-        typedef typename Vec<(sizeof(L) * V > 16 ? 16 : sizeof(L) * V)>::T W;
-        constexpr int N = sizeof(L) * V / sizeof(W);
-        union { W w[N]; L l[V]; } u;
+
+// The same for work that needs no order (the gradient): W lanes share a row of
+// E elements in turns, of 16 bytes where E is a multiple of them, else of one
+// element.  Only E decides which, so that the order of the sums does not depend
+// on where a row lies; vec: the rows are aligned to 16 bytes.
+template <typename L, int W, int V>
+__device__ __forceinline__ void load_turns(const L *row, int E, int lane, bool vec, float (&x)[V]) {
+    constexpr int C = 16 / sizeof(L);
+    if (V >= C && E % C == 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) narrow(x[i], u.l[i]);
+        for (int i = 0; i < V / C; ++i) {
+            union { uint4 w; L l[C]; } u;
+            const int e = (i * W + lane) * C;
+            if (e < E && vec) u.w = __ldg(reinterpret_cast<const uint4 *>(row + e));
 #pragma unroll
-        for (int i = 0; i < N; ++i) reinterpret_cast<W *>(row + lane * V)[i] = u.w[i];
+            for (int c = 0; c < C; ++c) {
+                if (e < E && !vec) u.l[c] = row[e + c];
+                x[(i * C + c) % V] = e < E ? widen(u.l[c]) : -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i * W + lane < E ? widen(row[i * W + lane]) : -INFINITY;
+    }
+}
+template <typename L, int W, int V>
+__device__ __forceinline__ void store_turns(L *row, int E, int lane, bool vec, const float (&x)[V]) {
+    constexpr int C = 16 / sizeof(L);
+    if (V >= C && E % C == 0) {
+#pragma unroll
+        for (int i = 0; i < V / C; ++i) {
+            union { uint4 w; L l[C]; } u;
+            const int e = (i * W + lane) * C;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                narrow(x[(i * C + c) % V], u.l[c]);
+                if (e < E && !vec) row[e + c] = u.l[c];
+            }
+            if (e < E && vec) *reinterpret_cast<uint4 *>(row + e) = u.w;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane * V + i < E) narrow(x[i], row[lane * V + i]);
+            if (i * W + lane < E) narrow(x[i], row[i * W + lane]);
     }
 }
 
@@ -312,8 +342,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
 // gradient is written whole (zeros, or the dense part), then lane j writes the
 // value of entry j over it.
 template <typename L, int W, int V, bool DENSE>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a, const int64_t *topk_idx, bool vec,
-                                                                         bool vec_out) {
+__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a, const int64_t *topk_idx, bool vec) {
     const int lane = threadIdx.x & (W - 1);
     const int64_t own = ((int64_t)blockIdx.x * kRouteWarps * 32 + threadIdx.x) / W;
     const bool live = own < a.T;                 // (lanes beyond the last token repeat it and write nothing)
@@ -323,7 +352,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
     L *out = reinterpret_cast<L *>(a.grad_logits) + t * a.grad_stride;
     float x[V];
-    if (DENSE) load_lane<L, V>(row, E, lane, vec, x);
+    if (DENSE) load_turns<L, W, V>(row, E, lane, vec, x);
     const int64_t id = lane < k ? topk_idx[t * k + lane] : -1;
     float g = lane < k ? a.grad_weights[t * k + lane] * a.r.scale : 0.f;
     const bool in_range = id >= 0 && id < E;
@@ -376,15 +405,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     const float f = -inv_z * mean;
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = DENSE ? x[i] * f : 0.f;
-    if (live) store_lane<L, V>(out, E, lane, vec_out, x);
+    if (live) store_turns<L, W, V>(out, E, lane, vec, x);
     __syncwarp();
     if (kept && live) narrow(v, out[id]);
 }
 
 // rows of a lane's V elements can be moved as vectors
-bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size, int lanes) {
-    if (E & (E - 1) || E < lanes) return false;                 // E = lanes * V
-    const int64_t bytes = E / lanes * size, w = bytes > 16 ? 16 : bytes;
+bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size) {
+    if (E & (E - 1) || E < 32) return false;                    // E = 32 V
+    const int64_t bytes = E / 32 * size, w = bytes > 16 ? 16 : bytes;
     return (uintptr_t)p % w == 0 && stride * size % w == 0;
 }
 
@@ -405,7 +434,7 @@ bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size, int lan
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    const bool vec = rows_vectorised(a.logits, a.stride, a.E, a.bf16 ? 2 : 4, 32);
+    const bool vec = rows_vectorised(a.logits, a.stride, a.E, a.bf16 ? 2 : 4);
 #define EP_ROUTE_BS(W, V) route_kernel<uint16_t, V, true>
 #define EP_ROUTE_BM(W, V) route_kernel<uint16_t, V, false>
 #define EP_ROUTE_FS(W, V) route_kernel<float, V, true>
@@ -424,8 +453,8 @@ cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, c
     const bool half = a.k <= 16 && a.E <= 512;
     const int W = half ? 16 : 32, size = a.bf16 ? 2 : 4, tokens = kRouteWarps * 32 / W;
     const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
-    const bool vec = rows_vectorised(a.logits, a.stride, a.E, size, W);
-    const bool vec_out = rows_vectorised(a.grad_logits, a.grad_stride, a.E, size, W);
+    const auto in16 = [&](const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride * size % 16 == 0; };
+    const bool vec = in16(a.logits, a.stride) && in16(a.grad_logits, a.grad_stride);
 #define EP_ROUTE_BD(W, V) route_backward_kernel<uint16_t, W, V, true>
 #define EP_ROUTE_BC(W, V) route_backward_kernel<uint16_t, W, V, false>
 #define EP_ROUTE_FD(W, V) route_backward_kernel<float, W, V, true>
@@ -433,11 +462,11 @@ cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, c
 #define EP_ROUTE_BACK(W)                                                             \
     do {                                                                             \
         if (dense) {                                                                 \
-            if (a.bf16) EP_ROUTE_CASES(W, EP_ROUTE_BD, a, topk_idx, vec, vec_out);   \
-            else EP_ROUTE_CASES(W, EP_ROUTE_FD, a, topk_idx, vec, vec_out);          \
+            if (a.bf16) EP_ROUTE_CASES(W, EP_ROUTE_BD, a, topk_idx, vec);   \
+            else EP_ROUTE_CASES(W, EP_ROUTE_FD, a, topk_idx, vec);          \
         } else {                                                                     \
-            if (a.bf16) EP_ROUTE_CASES(W, EP_ROUTE_BC, a, topk_idx, vec, vec_out);   \
-            else EP_ROUTE_CASES(W, EP_ROUTE_FC, a, topk_idx, vec, vec_out);          \
+            if (a.bf16) EP_ROUTE_CASES(W, EP_ROUTE_BC, a, topk_idx, vec);   \
+            else EP_ROUTE_CASES(W, EP_ROUTE_FC, a, topk_idx, vec);          \
         }                                                                            \
     } while (0)
     const bool dense = a.r.scoring == EP_SCORE_SOFTMAX && !a.r.renormalize;
