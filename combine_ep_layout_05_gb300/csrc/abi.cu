@@ -5,7 +5,7 @@
 #include <cstdio>
 #include <cstring>
 
-#include "ep_internal.cuh"
+#include "moe_internal.cuh"
 
 // bf16 dispatch goes through the bulk-copy engine from this many tokens on;
 // below it (decode and low-latency sizes) 16-byte register copies spread
@@ -609,6 +609,7 @@ int prepare_expert(const ep_problem *p, int64_t N, int64_t K, const uint8_t *act
         return fail(EP_ERR_INVALID_ARG, "the product's channels must be a multiple of 128, at most 2^24");
     if (N < 8 || N % 8 || N > (1 << 24))
         return fail(EP_ERR_INVALID_ARG, "out_features must be a multiple of 8, at most 2^24");
+    if (N * K >= (int64_t)1 << 40) return fail(EP_ERR_INVALID_ARG, "out_features * channels must be below 2^40");
     if (d.T > 0 && d.E > INT32_MAX / d.T) return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens exceeds int32");
     // tiles of 128 rows x 128 columns are counted in 32 bits
     if (d.E * d.T / 128 + d.E > INT32_MAX / ((N + 127) / 128))

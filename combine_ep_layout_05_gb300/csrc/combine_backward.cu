@@ -11,6 +11,7 @@
 // 1024 tokens expert-major: 46 us, 5.4 TB/s (the launch and three dependent
 // loads before the rows are known are 9 us of it).
 #include "combine_device.cuh"
+#include "moe_internal.cuh"
 
 namespace ep {
 
@@ -25,6 +26,28 @@ constexpr int kBackRows = 8;   // rows a pass keeps in flight
 #define EP_COMBINE_BACK_TOKENS 3
 #endif
 
+// The row of entry j = lane among the rows that resolve_sources kept, -1 if
+// it has none (called by a whole warp).
+template <int LAYOUT>
+__device__ __forceinline__ int entry_row(const CombineArgs &a, int64_t t, const RouteRegs &g, const int64_t *rows, int nd) {
+    const Dims &d = a.d;
+    const bool in_range = g.e >= 0 && g.e < d.E;
+    const unsigned same = __match_any_sync(kFull, in_range ? (int)g.e : -2 - (int)(threadIdx.x & 31));
+    const bool kept = in_range && !(same & lanemask_lt());       // the first of repeated ids
+    const uint32_t r = kept ? rank_of(d, (uint32_t)g.e) : 0;
+    int64_t slot = g.s0, block = g.e;
+    if (LAYOUT == EP_RANK_MAJOR) {
+        const int32_t g0 = __shfl_sync(kFull, g.s0, r & 31), g1 = __shfl_sync(kFull, g.s1, r & 31);
+        slot = r < 32 ? g0 : g1;
+        block = r;
+    }
+    if (!kept || slot < 0 || slot >= d.Tr) return -1;
+    const int64_t row = (block * d.R + t / d.Tr) * d.Tr + slot;
+    for (int i = 0; i < nd; ++i)
+        if (rows[i] == row) return i;
+    return -1;
+}
+
 template <int LAYOUT, int W>
 __global__ void __launch_bounds__(W * 32) combine_backward_kernel(CombineArgs a, const uint16_t *grad_out,
                                                                  uint16_t *grad_y, float *grad_weights) {
@@ -35,9 +58,9 @@ __global__ void __launch_bounds__(W * 32) combine_backward_kernel(CombineArgs a,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = blockIdx.x, hc = d.H / 8;
     if (warp == 0) {
-        int entry;
-        const int nd = resolve_sources<LAYOUT>(a, t, t / d.Tr, load_route<LAYOUT>(a, t), s_rows, s_wts, &entry);
-        s_entry[lane] = entry;
+        const RouteRegs g = load_route<LAYOUT>(a, t);
+        const int nd = resolve_sources<LAYOUT>(a, t, t / d.Tr, g, s_rows, s_wts);
+        s_entry[lane] = entry_row<LAYOUT>(a, t, g, s_rows, nd);
         if (lane == 0) s_nd = nd;
     }
     __syncthreads();

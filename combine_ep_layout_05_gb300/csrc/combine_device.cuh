@@ -81,11 +81,9 @@ __device__ __forceinline__ RouteRegs load_route(const CombineArgs &a, int64_t t)
 // the first entry of each row.  Ids outside [0, E) and repeats are dropped
 // (and flagged in the status word); in the rank-major layout the entries
 // of one rank share its row, with their weights summed in j order.
-// entry_row (if not null): lane j < k gets the index of entry j's row in
-// rows, -1 for an entry that is not kept.
 template <int LAYOUT>
 __device__ __forceinline__ int resolve_sources(const CombineArgs &a, int64_t t, int64_t src, const RouteRegs &g,
-                                               int64_t *rows, float *wts, int *entry_row = nullptr) {
+                                               int64_t *rows, float *wts) {
     const Dims &d = a.d;
     const int lane = threadIdx.x & 31;
     int st = 0;
@@ -103,12 +101,10 @@ __device__ __forceinline__ int resolve_sources(const CombineArgs &a, int64_t t, 
 
     int64_t row = -1;
     float wsum = w;
-    int lead = lane;   // the lane that holds this entry's row
     if (LAYOUT == EP_RANK_MAJOR) {
         const int r = kept ? (int)rank_of(d, (uint32_t)e) : -1;
         const unsigned grp = __match_any_sync(kFull, kept ? r : -100 - lane);
         const bool leader = kept && !(grp & lanemask_lt());
-        lead = __ffs(grp) - 1;
         // weight of the rank: the group's weights summed in j order
         wsum = 0.f;
         for (int j = 0; j < (int)d.k; ++j) {
@@ -137,7 +133,6 @@ __device__ __forceinline__ int resolve_sources(const CombineArgs &a, int64_t t, 
         rows[i] = row;
         wts[i] = wsum;
     }
-    if (entry_row) *entry_row = kept && ((m >> lead) & 1) ? __popc(m & ((1u << lead) - 1)) : -1;
     __syncwarp();
     return __popc(m);
 }

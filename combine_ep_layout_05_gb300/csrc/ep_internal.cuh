@@ -93,35 +93,6 @@ struct CombineArgs {
     int64_t piece_elems;
 };
 
-struct RouteArgs {
-    int64_t T, E, k;
-    ep_router r;
-    bool bf16;               // logits and their gradient: bf16, else fp32
-    const void *logits;
-    int64_t stride;          // elements between rows of logits
-    const float *bias;
-    int64_t *topk_idx;
-    float *topk_weights;
-    const float *grad_weights;
-    void *grad_logits;
-    int64_t grad_stride;
-    int32_t *dev_status;
-};
-
-struct ExpertArgs {
-    Dims d;
-    int64_t N, K;            // weight rows (2 * I with SwiGLU) and channels
-    const uint8_t *a;
-    const float *a_scales;
-    const uint8_t *w;
-    const float *w_scales;
-    const int32_t *tokens_per_expert;
-    uint16_t *y;             // bf16 output, or
-    uint8_t *q;              // e4m3 codes and scales of the SwiGLU
-    float *q_scales;
-    int32_t *dev_status;
-};
-
 // destination set of the dispatch kernels besides EP_RANK_MAJOR /
 // EP_EXPERT_MAJOR: one row per (token, node) of the node-major staging
 // buffer (the first hop of the two-level dispatch)
@@ -166,13 +137,6 @@ cudaError_t launch_wire_quant(int layout, int fmt, const DispatchArgs &a, const 
                               cudaStream_t st);
 cudaError_t launch_combine_wire(int layout, int fmt, const CombineArgs &a, const uint8_t *wq, const void *ws,
                                 cudaStream_t st);
-cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);
-cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, cudaStream_t st);
-cudaError_t launch_combine_backward(int layout, const CombineArgs &a, const uint16_t *grad_out, uint16_t *grad_y,
-                                    float *grad_weights, cudaStream_t st);
-cudaError_t launch_expert(const ExpertArgs &a, cudaStream_t st);        // chooses between
-cudaError_t launch_expert_many(const ExpertArgs &a, cudaStream_t st);
-cudaError_t launch_expert_few(const ExpertArgs &a, cudaStream_t st);
 
 // Sets the message ep_last_error_string() returns on this thread; returns code.
 int set_last_error(int code, const char *fmt, ...);

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             receive_rows(a, v.e, m, row);
             if (warp < 6) s.row[unit % kScaleRing][place] = row[kMine];   // (announced with the first step's copies)
 #pragma unroll
-            for (int i = 0; i <= kMine; ++i) row[i] *= kb_n;
+            for (int i = 0; i <= kMine; ++i) row[i] = (int)((uint32_t)row[i] * kb_n);
             uint32_t ws = (uint32_t)(v.e * n_blocks + v.nb) * kb_n;
             if (lane == 1) ws += n_blocks / 2 * kb_n;             // (SwiGLU: the up block's)
             const bool has_scale = warp < 6 && place < v.rows;

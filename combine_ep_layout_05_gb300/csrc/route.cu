@@ -13,7 +13,7 @@
 // each of the k rounds is one warp maximum over the lanes' heads, a ballot for
 // the lowest lane that has it, and a shift of that lane's list; lane j notes
 // the key and the lane of round j and looks its index up at the end.
-#include "ep_internal.cuh"
+#include "moe_internal.cuh"
 
 namespace ep {
 

@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "dispatch_device.cuh"
+#include "moe_internal.cuh"
 
 namespace ep {
 

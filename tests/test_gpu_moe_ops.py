@@ -507,6 +507,7 @@ EXPERT = [
     (1, 1, 1, 1, 128, 0.0), (1, 1, 8, 2, 256, 0.0), (4, 8, 16, 4, 1024, 0.0), (3, 5, 12, 3, 384, 0.5),
     (2, 61, 4, 2, 640, 0.1), (8, 33, 8, 4, 512, 0.0), (2, 150, 2, 1, 256, 0.0), (64, 3, 64, 8, 128, 0.2),
     (1, 700, 3, 2, 384, 0.0), (5, 7, 5, 2, 256, 1.0),
+    (64, 3, 64, 32, 256, 0.1), (16, 20, 16, 4, 384, 0.0),     # many rows in many short segments
 ]
 
 
@@ -559,6 +560,24 @@ def check_swiglu(m, p, counts, live, a, s, w, ws, E, I, K):
     step = torch.maximum(2.0 ** -4 * h.abs(), 2.0 ** -10 * scale.repeat_interleave(128, 1))
     tol = step * (1 + 2.0 ** -10) + 1.1 * eh
     assert bool(((dec - h).abs() <= tol).all()), float(((dec - h).abs() / tol).max())
+
+
+@pytest.mark.parametrize("R,Tr,E,k", [(2, 16, 8, 2), (2, 150, 2, 1)])
+def test_expert_outputs_at_sixteen_bytes(m, R, Tr, E, k):
+    """Outputs that start 16 bytes off a 32-byte boundary give the same values (few and many rows an expert)."""
+    K, N, I, rows = 256, 256, 128, E * R * Tr
+    p, counts, live, a, s, w, ws = expert_case(m, R, Tr, E, k, N, K, 4)
+    y = torch.zeros(rows * N, dtype=torch.bfloat16, device=DEV)
+    y16 = torch.zeros(rows * N + 8, dtype=torch.bfloat16, device=DEV)[8:]
+    q, qs = torch.zeros(rows * I, dtype=torch.uint8, device=DEV), torch.zeros(rows, device=DEV)
+    q16 = torch.zeros(rows * I + 16, dtype=torch.uint8, device=DEV)[16:]
+    assert y16.data_ptr() % 32 == 16 and q16.data_ptr() % 32 == 16
+    m.ep_expert_gemm(p, a, s, w, ws, counts, y)
+    m.ep_expert_gemm(p, a, s, w, ws, counts, y16)
+    m.ep_expert_swiglu(p, a, s, w, ws, counts, q, qs)
+    m.ep_expert_swiglu(p, a, s, w, ws, counts, q16, qs)
+    assert torch.equal(y, y16) and torch.equal(q, q16)
+    assert bool((y != 0).any()) and bool((q != 0).any())
 
 
 def test_expert_swiglu_large_and_zero_values(m):
