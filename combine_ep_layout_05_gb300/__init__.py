@@ -1,4 +1,4 @@
-"""MoE expert-parallel dispatch layout, dispatch and combine on one GB300.
+"""MoE expert-parallel routing, dispatch layout, dispatch, FP8 experts and combine on one GB300.
 
 Importing the package loads nothing native; ``combine_ep_layout_05_gb300.ep``
 loads the CUDA library (and raises if it has not been built).

@@ -5,8 +5,8 @@
 // rows are the tensor core's M, the expert's rows its N (16, 32, 48 or 64, as
 // many as there are), so a step costs next to nothing beside the copy of its
 // matrix rows: SwiGLU 32 KB (128 gate and 128 up rows), else 16 KB, for which
-// an SM's share of the memory rate takes some 1400 and 700 cycles.  160 KB (128
-// KB) of operands in flight cover the memory's latency several times.
+// an SM's share of the memory rate takes some 1400 and 700 cycles.  160 KB of
+// operands in flight cover the memory's latency several times.
 //
 // An accumulator in tensor memory has a matrix row in each lane and the
 // expert's rows in its columns; four alternate.  A thread owns a matrix row:
@@ -14,6 +14,11 @@
 // memory.  Warps as in expert.cu; SwiGLU's two warpgroups hold gate and up,
 // swap halves of their columns through shared memory at the end, and each
 // finishes its half.
+//
+// Measured: 32 tokens x top-8 over 256 experts of 7168 x 2048, SwiGLU: 645 us,
+// 7.4 TB/s (reading alone is faster than the copy that the rate is judged by, 6.8);
+// 1024 tokens 1.12 to 1.14 ms, 6.7 TB/s; one token's down product 24.6 us (117 MB;
+// 22 us from a graph, 17 of them memory, the rest launch and first tiles).
 #include <cstddef>
 
 #include "expert_device.cuh"
