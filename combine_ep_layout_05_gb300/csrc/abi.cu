@@ -611,9 +611,9 @@ int prepare_expert(const ep_problem *p, int64_t N, int64_t K, const uint8_t *act
         return fail(EP_ERR_INVALID_ARG, "out_features must be a multiple of 8, at most 2^24");
     if (N * K >= (int64_t)1 << 40) return fail(EP_ERR_INVALID_ARG, "out_features * channels must be below 2^40");
     if (d.T > 0 && d.E > INT32_MAX / d.T) return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens exceeds int32");
-    // tiles of 128 rows x 128 columns are counted in 32 bits
-    if (d.E * d.T / 128 + d.E > INT32_MAX / ((N + 127) / 128))
-        return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens * out_features exceeds 2^45");
+    // tiles of 64 rows x 128 columns are counted in 32 bits, with room for a step of the grid beyond the last
+    if (d.E * d.T / 64 + d.E > (INT32_MAX - 65536) / ((N + 127) / 128))
+        return fail(EP_ERR_INVALID_ARG, "num_experts * num_tokens * out_features too large (about 2^44)");
     if (d.T > 0) {
         if (!act || !aligned(act, 16) || !w || !aligned(w, 16))
             return fail(EP_ERR_INVALID_ARG, "a / w NULL or not 16-byte aligned");

@@ -478,7 +478,8 @@ int ep_combine_backward(const ep_problem *p, int layout, const uint16_t *grad_ou
  *   per row and 128 channels q = e4m3(h * inv), scale = amax / 448, ready to
  *   be the a of ep_expert_gemm.  q [rows, I] e4m3, q_scales [rows, I / 128].
  *   H % 128 == 0, I % 128 == 0.
- * a, w, y and q 16-byte aligned; E * T < 2^31.
+ * a, w, y and q 16-byte aligned; E * T < 2^31, and tiles of 64 rows x 128
+ * columns, at most (E * T / 64 + E) * ceil(N / 128), below 2^31 - 2^16.
  */
 int ep_expert_gemm(const ep_problem *p, int64_t out_features, int64_t in_features, const uint8_t *a,
                    const float *a_scales, const uint8_t *w, const float *w_scales,

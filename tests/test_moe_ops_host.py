@@ -95,6 +95,10 @@ def test_expert_arguments_rejected(ep):
     g[0] = ctypes.byref(huge)
     assert lib.ep_expert_gemm(*g) == ep.EP_ERR_INVALID_ARG
     assert "int32" in ep.ep_last_error_string()
+    wide = ep.problem(1 << 22, 256, 8, 256, 4)                 # 2^24 tiles of rows, 2^17 of columns
+    g[0], g[1] = ctypes.byref(wide), 1 << 24
+    assert lib.ep_expert_gemm(*g) == ep.EP_ERR_INVALID_ARG
+    assert "too large" in ep.ep_last_error_string()
 
 
 def test_python_binding_refuses(ep):
