@@ -1,10 +1,11 @@
 // Routing: a token's logits -> its k experts and their weights, and the
 // gradient of the weights with respect to the logits.
 //
-// A warp owns one token.  Lane l holds the V consecutive experts l * V ..
-// l * V + V - 1 in registers (V a power of two, 32 V >= E), so a row is read
-// once and "lowest index first" is lane order.  Keys are compared as
-// unsigned words in the order of the floats; 0 stands for "not eligible".
+// A warp owns one token.  Lanes hold consecutive experts in registers, up to V
+// each (V a power of two), so a row is read once and "lowest index first" is
+// lane order; where experts form groups, a group has lanes of its own.  Keys
+// are compared as unsigned words in the order of the floats; 0 stands for
+// "not eligible".
 //
 // The memory traffic is small (a row read, k pairs written); what takes the
 // time is instructions: the scores (an exponential and a reciprocal for each
@@ -14,7 +15,7 @@
 // the lowest lane that has it, and a shift of that lane's list; lane j notes
 // the key and the lane of round j and looks its index up at the end.
 //
-// Measured (256 experts, top-8, grouped sigmoid with a bias): 65536 tokens 61 us,
+// Measured (256 experts, top-8, grouped sigmoid with a bias): 65536 tokens 60 us,
 // 990 instructions a token at 89% of the issue slots, of which some 200 are the
 // exponentials and reciprocals of the scores, correctly rounded because a key
 // decides; the memory alone would take 11 us.  32 tokens: 3.3 us from a graph.
@@ -69,21 +70,32 @@ template <> struct Vec<8> { typedef uint2 T; };
 template <> struct Vec<4> { typedef uint32_t T; };
 template <> struct Vec<2> { typedef uint16_t T; };
 
-// A lane's V elements of a row of E; elements beyond E read as -inf.  vec:
-// the lanes cover E exactly and every row is aligned to the vector.
+// Which experts a lane holds: 1 << log lanes share each of the groups of `per`
+// experts, `each` a lane.
+struct LaneMap {
+    int groups, per, log, each;
+    __device__ __forceinline__ int in(int lane) const { return (lane & ((1 << log) - 1)) * each; }
+    __device__ __forceinline__ int first(int lane) const { return (lane >> log) * per + in(lane); }
+    __device__ __forceinline__ int count(int lane) const {
+        return lane >> log < groups ? max(0, min(each, per - in(lane))) : 0;
+    }
+};
+
+// A lane's n <= V elements of a row, from element lo on; the rest read as -inf.
+// vec: every lane has V, and rows are aligned to the vector.
 template <typename L, int V>
-__device__ __forceinline__ void load_lane(const L *row, int E, int lane, bool vec, float (&x)[V]) {
+__device__ __forceinline__ void load_lane(const L *row, int lo, int n, bool vec, float (&x)[V]) {
     if (vec) {
         typedef typename Vec<(sizeof(L) * V > 16 ? 16 : sizeof(L) * V)>::T W;
         constexpr int N = sizeof(L) * V / sizeof(W);
         union { W w[N]; L l[V]; } u;
 #pragma unroll
-        for (int i = 0; i < N; ++i) u.w[i] = __ldg(reinterpret_cast<const W *>(row + lane * V) + i);
+        for (int i = 0; i < N; ++i) u.w[i] = __ldg(reinterpret_cast<const W *>(row + lo) + i);
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = widen(u.l[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = lane * V + i < E ? widen(row[lane * V + i]) : -INFINITY;
+        for (int i = 0; i < V; ++i) x[i] = i < n ? widen(row[lo + i]) : -INFINITY;
     }
 }
 
@@ -152,10 +164,11 @@ __device__ __forceinline__ void sort_words(uint32_t *w) {
                     if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(w[i + j], w[i + j + k]);
 }
 
-// Clears the keys of the groups that are not among the best.  Any split of
-// the experts: groups one after the other, scores kept by lane g % 32.
+// Clears the keys of the groups that are not among the best.  Any split of the
+// experts (more than 32 groups, or groups too large for lanes of their own):
+// groups one after the other, scores kept by lane g % 32.
 template <int V>
-__device__ __forceinline__ void keep_groups(const RouteArgs &a, uint32_t (&key)[V]) {
+__device__ __forceinline__ void keep_groups(const RouteArgs &a, int first, uint32_t (&key)[V]) {
     const int lane = threadIdx.x & 31;
     const int G = a.r.num_groups, per = (int)a.E / G, slots = (G + 31) / 32;
     uint32_t score[kMaxExperts / 32], kept[kMaxExperts / 32];
@@ -165,7 +178,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &a, uint32_t (&key)[
         uint32_t b1 = 0, b2 = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
+            const int e = first + i;
             const uint32_t v = e >= lo && e < hi ? key[i] : 0;
             b2 = max(b2, min(b1, v));
             b1 = max(b1, v);
@@ -193,18 +206,16 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &a, uint32_t (&key)[
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int g = (lane * V + i) / per;
+        const int g = (first + i) / per;
         if (g >= G || !((kept[g >> 5] >> (g & 31)) & 1)) key[i] = 0;
     }
 }
 
-// The same where a group is 32 / G whole lanes (E = 32 V, G divides 32): the
-// best two of a group meet in a butterfly, then topk_groups rounds take the best
-// score left.
+// The same where every group has `lanes` lanes of its own: the best two of a
+// group meet in a butterfly, then topk_groups rounds take the best score left.
 template <int V>
-__device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, uint32_t (&key)[V]) {
+__device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, int lanes, uint32_t (&key)[V]) {
     const int lane = threadIdx.x & 31;
-    const int G = a.r.num_groups, lanes = 32 / G;
     uint32_t b1 = 0, b2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -236,19 +247,19 @@ __device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, uint32_t (&
 }
 
 template <typename L, int V, bool SIG>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bool vec) {
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, LaneMap map, bool vec) {
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
-    const int E = (int)a.E, k = (int)a.k;
+    const int k = (int)a.k, lo = map.first(lane), held = map.count(lane);
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
     float x[V], b[V];
     uint32_t key[V];
-    load_lane<L, V>(row, E, lane, vec, x);
+    load_lane<L, V>(row, lo, held, vec, x);
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = 0.f;
-    if (a.bias) load_lane<float, V>(a.bias, E, lane, vec && ((uintptr_t)a.bias & 15) == 0, b);
+    if (a.bias) load_lane<float, V>(a.bias, lo, held, vec && ((uintptr_t)a.bias & 15) == 0, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float f = (SIG ? sigmoid(x[i]) : x[i]) + b[i];
@@ -275,10 +286,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
             if (x[i] > -INFINITY) z += expf(fminf(x[i], kMaxFinite) - m);
         z = lanes_sum<32>(z);
     }
-    const int G = a.r.num_groups;
-    if (a.r.topk_groups < G) {
-        if (E == 32 * V && G <= 32 && 32 % G == 0) keep_lane_groups<V>(a, key);
-        else keep_groups<V>(a, key);
+    if (a.r.topk_groups < a.r.num_groups) {
+        if (map.groups == a.r.num_groups) keep_lane_groups<V>(a, 1 << map.log, key);
+        else keep_groups<V>(a, lo, key);
     }
 
     constexpr int N = V < 8 ? V : 8, B = V / N;   // sorted blocks of a lane
@@ -320,7 +330,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, bo
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t w = __shfl_sync(kFull, key[i], from);
-        if (mine && w == mine && n-- == 0) id = from * V + i;
+        if (mine && w == mine && n-- == 0) id = map.first(from) + i;
     }
 
     float s = 0.f;
@@ -417,19 +427,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     if (kept && live) narrow(v, out[id]);
 }
 
-// rows of a lane's V elements can be moved as vectors
-bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size) {
-    if (E & (E - 1) || E < 32) return false;                    // E = 32 V
-    const int64_t bytes = E / 32 * size, w = bytes > 16 ? 16 : bytes;
-    return (uintptr_t)p % w == 0 && stride * size % w == 0;
-}
-
 }  // namespace
 
-// The kernel for V = 1, 2, 4, .. 32 experts a lane, W lanes a token
+// The kernel for V = 1, 2, 4, .. 32 (at least `per`) experts a lane, W lanes a token
 #define EP_ROUTE_CASES(W, KERNEL, ...)                                          \
     do {                                                                        \
-        const int per = ((int)a.E + W - 1) / W;                                 \
         if (per <= 1) EP_ROUTE_LAUNCH(W, 1, KERNEL, __VA_ARGS__);               \
         else if (per <= 2) EP_ROUTE_LAUNCH(W, 2, KERNEL, __VA_ARGS__);          \
         else if (per <= 4) EP_ROUTE_LAUNCH(W, 4, KERNEL, __VA_ARGS__);          \
@@ -441,24 +443,37 @@ bool rows_vectorised(const void *p, int64_t stride, int64_t E, int size) {
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    const bool vec = rows_vectorised(a.logits, a.stride, a.E, a.bf16 ? 2 : 4);
+    const int E = (int)a.E, G = a.r.num_groups, size = a.bf16 ? 2 : 4;
+    // A group to lanes of its own, if 32 lanes of up to 32 experts can hold them so.  65536 tokens, 160 experts in 8
+    // groups: 61 us, against 140 us with the groups taken one after the other; 384 in 12: 127 against 302.
+    LaneMap map{1, E, 5, (E + 31) / 32};
+    if (a.r.topk_groups < G && G <= 32) {
+        int log = 5;
+        while (G << log > 32) --log;
+        const int each = (E / G + (1 << log) - 1) >> log;
+        if (each <= 32) map = LaneMap{G, E / G, log, each};
+    }
+    const int per = map.each;
+    const bool full = (per & (per - 1)) == 0 && per * 32 == E;       // every lane has V experts, one after the other
+    const int64_t bytes = (int64_t)per * size, width = bytes > 16 ? 16 : bytes;
+    const bool vec = full && (uintptr_t)a.logits % width == 0 && a.stride * size % width == 0;
 #define EP_ROUTE_BS(W, V) route_kernel<uint16_t, V, true>
 #define EP_ROUTE_BM(W, V) route_kernel<uint16_t, V, false>
 #define EP_ROUTE_FS(W, V) route_kernel<float, V, true>
 #define EP_ROUTE_FM(W, V) route_kernel<float, V, false>
     if (a.r.scoring == EP_SCORE_SIGMOID) {
-        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BS, a, vec);
-        else EP_ROUTE_CASES(32, EP_ROUTE_FS, a, vec);
+        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BS, a, map, vec);
+        else EP_ROUTE_CASES(32, EP_ROUTE_FS, a, map, vec);
     } else {
-        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BM, a, vec);
-        else EP_ROUTE_CASES(32, EP_ROUTE_FM, a, vec);
+        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BM, a, map, vec);
+        else EP_ROUTE_CASES(32, EP_ROUTE_FM, a, map, vec);
     }
     return cudaGetLastError();
 }
 
 cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, cudaStream_t st) {
     const bool half = a.k <= 16 && a.E <= 512;
-    const int W = half ? 16 : 32, size = a.bf16 ? 2 : 4, tokens = kRouteWarps * 32 / W;
+    const int W = half ? 16 : 32, per = ((int)a.E + W - 1) / W, size = a.bf16 ? 2 : 4, tokens = kRouteWarps * 32 / W;
     const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
     const auto in16 = [&](const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride * size % 16 == 0; };
     const bool vec = in16(a.logits, a.stride) && in16(a.grad_logits, a.grad_stride);

@@ -129,6 +129,10 @@ ROUTE = [
     (17, 36, 5, "fp32", "softmax", True, 36, 9, 2, True, 1.0, 1.0, 0.0),       # groups of one expert
     (300, 128, 8, "bf16", "softmax", False, 1, 1, 1, True, 1.0, 8.0, 0.0),
     (16, 512, 8, "bf16", "sigmoid", True, 16, 4, 2, True, 1.0, 0.5, 0.98),     # rows left with nothing
+    (45, 120, 8, "fp32", "sigmoid", True, 24, 7, 2, True, 1.0, 1.0, 0.1),      # groups that leave lanes over
+    (31, 352, 9, "bf16", "sigmoid", False, 11, 5, 1, True, 1.0, 1.0, 0.2),
+    (23, 999, 9, "fp32", "softmax", False, 3, 2, 2, True, 1.0, 1.0, 0.0),      # groups too large for lanes of their own
+    (30, 66, 3, "fp32", "softmax", True, 2, 1, 2, False, 1.0, 1.0, 0.4),       # a group's last lanes empty
 ]
 
 
