@@ -228,7 +228,7 @@ __device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, int lanes, 
         b1 = max(b1, o1);
     }
     const uint32_t score =
-        a.r.group_best == 2 && b1 && b2 ? order_word(order_float(b1) + order_float(b2)) : b1;
+        a.r.group_best == 2 && b1 && b2 ? order_word(order_float(b1) + order_float(b2)) : b1;   // (never -0: no key is)
     uint32_t left = score;
     bool keep = false;
     for (int n = 0; n < a.r.topk_groups; ++n) {
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, La
     if (a.bias) load_lane<float, V>(a.bias, lo, held, vec && ((uintptr_t)a.bias & 15) == 0, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float f = (SIG ? sigmoid(x[i]) : x[i]) + b[i];
+        const float f = (SIG ? sigmoid(x[i]) : x[i]) + b[i] + 0.f;        // (-0 + 0 = +0: equal keys, equal words)
         nan |= f != f;
         key[i] = x[i] > -INFINITY && f > -INFINITY ? order_word(f) : 0;   // comparisons are false for NaN
     }
