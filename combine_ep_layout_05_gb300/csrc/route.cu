@@ -404,21 +404,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
         inv_z = z > 0.f ? 1.f / z : 0.f;
     }
     const float s = !kept ? 0.f : sig ? sigmoid(xj) : expf(xj - m) * inv_z;
-    float ds = g;
+    // sigmoid: s' = sigmoid(x) sigmoid(-x); 1 - s has no digits left where s rounds to 1.  Renormalised weights: the
+    // quotients s_j / S, not 1 / S, which is infinite for scores that are not yet 0.
+    float p = s, d = g, mean = 0.f;
     if (norm) {
-        const float total = lanes_sum<W>(s), inv = total > 0.f ? 1.f / total : 0.f;
-        const float mean = lanes_sum<W>(g * s) * inv;
-        ds = kept ? (g - mean) * inv : 0.f;
+        const float total = lanes_sum<W>(s);
+        p = total > 0.f ? s / total : 0.f;
+        d = g - lanes_sum<W>(g * p);
+    } else if (DENSE) {
+        mean = lanes_sum<W>(g * s);
+        d = g - mean;
     }
-    float mean = 0.f, v;
-    if (sig) {
-        v = ds * s * (1.f - s);
-    } else if (norm) {
-        v = s * ds;       // sum_j ds_j s_j = 0: the mean is already taken out
-    } else {
-        mean = lanes_sum<W>(ds * s);
-        v = s * (ds - mean);
-    }
+    const float v = sig ? d * p * sigmoid(-xj) : d * p;   // (softmax, renormalised: the mean is already taken out)
     const float f = -inv_z * mean;
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = DENSE ? x[i] * f : 0.f;
