@@ -583,6 +583,8 @@ int prepare_route(const ep_problem *p, const ep_router *r, int dtype, const void
         return fail(EP_ERR_INVALID_ARG, "topk_groups must be in 1..num_groups");
     if (r->group_best != 1 && r->group_best != 2) return fail(EP_ERR_INVALID_ARG, "group_best must be 1 or 2");
     if (!std::isfinite(r->scale)) return fail(EP_ERR_INVALID_ARG, "scale must be finite");
+    if (r->softmax_key != EP_KEY_LOGIT && r->softmax_key != EP_KEY_SCORE)
+        return fail(EP_ERR_INVALID_ARG, "unknown softmax_key %d", r->softmax_key);
     if (dtype != EP_BF16 && dtype != EP_FP32) return fail(EP_ERR_INVALID_ARG, "logits must be EP_BF16 or EP_FP32");
     if (stride < d.E) return fail(EP_ERR_INVALID_ARG, "logits_row_stride smaller than num_experts");
     if (!aligned(dev_status, 4)) return fail(EP_ERR_INVALID_ARG, "dev_status misaligned");

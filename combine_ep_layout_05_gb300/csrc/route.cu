@@ -246,8 +246,13 @@ __device__ __forceinline__ void keep_lane_groups(const RouteArgs &a, int lanes, 
     }
 }
 
-template <typename L, int V, bool SIG>
+// What the keys are, as a template argument: as a run-time branch the softmax scores cost the other softmax key 2 us
+// of 37 (65536 tokens x 256 experts, fp32, renormalised; by score 55 us: an exponential and a quotient for each expert)
+enum { kSoftmaxLogit, kSoftmaxScore, kSigmoid };
+
+template <typename L, int V, int KEY>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, LaneMap map, bool vec) {
+    constexpr bool SIG = KEY == kSigmoid, by_score = KEY == kSoftmaxScore;
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -260,21 +265,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, La
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = 0.f;
     if (a.bias) load_lane<float, V>(a.bias, lo, held, vec && ((uintptr_t)a.bias & 15) == 0, b);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float f = (SIG ? sigmoid(x[i]) : x[i]) + b[i] + 0.f;        // (-0 + 0 = +0: equal keys, equal words)
-        nan |= f != f;
-        key[i] = x[i] > -INFINITY && f > -INFINITY ? order_word(f) : 0;   // comparisons are false for NaN
-    }
-    if (nan) {                // (infinities of opposite signs also add to NaN; they only make an expert ineligible)
-        nan = false;
-#pragma unroll
-        for (int i = 0; i < V; ++i) nan |= x[i] != x[i] || b[i] != b[i];
-        if (nan) raise_status(a.dev_status, EP_STATUS_BAD_LOGIT);
-    }
-
-    float m = 0.f, z = 1.f;   // softmax over the logits that are numbers
-    if (!SIG && !a.r.renormalize) {
+    // softmax over the logits that are numbers, where a weight or a key needs it
+    float m = 0.f, z = 1.f;
+    if (!SIG && (by_score || !a.r.renormalize)) {
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -285,6 +278,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, La
         for (int i = 0; i < V; ++i)
             if (x[i] > -INFINITY) z += expf(fminf(x[i], kMaxFinite) - m);
         z = lanes_sum<32>(z);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float c = SIG ? sigmoid(x[i]) : x[i];
+        if (by_score && x[i] > -INFINITY) c = expf(fminf(x[i], kMaxFinite) - m) / z;
+        const float f = c + b[i] + 0.f;        // (-0 + 0 = +0: equal keys, equal words)
+        nan |= f != f;
+        key[i] = x[i] > -INFINITY && f > -INFINITY ? order_word(f) : 0;   // comparisons are false for NaN
+    }
+    if (nan) {                // (infinities of opposite signs also add to NaN; they only make an expert ineligible)
+        nan = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) nan |= x[i] != x[i] || b[i] != b[i];
+        if (nan) raise_status(a.dev_status, EP_STATUS_BAD_LOGIT);
     }
     if (a.r.topk_groups < a.r.num_groups) {
         if (map.groups == a.r.num_groups) keep_lane_groups<V>(a, 1 << map.log, key);
@@ -454,16 +461,21 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
     const bool full = (per & (per - 1)) == 0 && per * 32 == E;       // every lane has V experts, one after the other
     const int64_t bytes = (int64_t)per * size, width = bytes > 16 ? 16 : bytes;
     const bool vec = full && (uintptr_t)a.logits % width == 0 && a.stride * size % width == 0;
-#define EP_ROUTE_BS(W, V) route_kernel<uint16_t, V, true>
-#define EP_ROUTE_BM(W, V) route_kernel<uint16_t, V, false>
-#define EP_ROUTE_FS(W, V) route_kernel<float, V, true>
-#define EP_ROUTE_FM(W, V) route_kernel<float, V, false>
+#define EP_ROUTE_BG(W, V) route_kernel<uint16_t, V, kSigmoid>
+#define EP_ROUTE_BL(W, V) route_kernel<uint16_t, V, kSoftmaxLogit>
+#define EP_ROUTE_BS(W, V) route_kernel<uint16_t, V, kSoftmaxScore>
+#define EP_ROUTE_FG(W, V) route_kernel<float, V, kSigmoid>
+#define EP_ROUTE_FL(W, V) route_kernel<float, V, kSoftmaxLogit>
+#define EP_ROUTE_FS(W, V) route_kernel<float, V, kSoftmaxScore>
     if (a.r.scoring == EP_SCORE_SIGMOID) {
+        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BG, a, map, vec);
+        else EP_ROUTE_CASES(32, EP_ROUTE_FG, a, map, vec);
+    } else if (a.r.softmax_key == EP_KEY_LOGIT) {
+        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BL, a, map, vec);
+        else EP_ROUTE_CASES(32, EP_ROUTE_FL, a, map, vec);
+    } else {
         if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BS, a, map, vec);
         else EP_ROUTE_CASES(32, EP_ROUTE_FS, a, map, vec);
-    } else {
-        if (a.bf16) EP_ROUTE_CASES(32, EP_ROUTE_BM, a, map, vec);
-        else EP_ROUTE_CASES(32, EP_ROUTE_FM, a, map, vec);
     }
     return cudaGetLastError();
 }

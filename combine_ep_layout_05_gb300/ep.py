@@ -25,11 +25,13 @@ EP_STATUS_BAD_LOGIT = 16
 EP_RANK_MAJOR, EP_EXPERT_MAJOR = 0, 1
 EP_BF16, EP_FP8_E4M3, EP_FP32 = 0, 1, 2
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_KEY_LOGIT, EP_KEY_SCORE = 0, 1
 EP_WIRE_MXFP8, EP_WIRE_NVFP4 = 1, 2
 WIRES = {"mxfp8": EP_WIRE_MXFP8, "nvfp4": EP_WIRE_NVFP4}
 
 LAYOUTS = {"rank_major": EP_RANK_MAJOR, "expert_major": EP_EXPERT_MAJOR}
 SCORINGS = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+SOFTMAX_KEYS = {"logit": EP_KEY_LOGIT, "score": EP_KEY_SCORE}
 DTYPES = {"bf16": EP_BF16, "fp8_e4m3": EP_FP8_E4M3}
 
 # every symbol include/ep.h declares
@@ -63,15 +65,19 @@ class ep_problem(ctypes.Structure):
 
 class ep_router(ctypes.Structure):
     _fields_ = [("scoring", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
-                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softmax_key", ctypes.c_int32)]
 
 
 def router(scoring: str = "softmax", num_groups: int = 1, topk_groups: int = 1, group_best: int = 1,
-           renormalize: bool = True, scale: float = 1.0) -> ep_router:
+           renormalize: bool = True, scale: float = 1.0, softmax_key: str = "logit") -> ep_router:
     """How ep_route scores and chooses: "softmax" or "sigmoid" scores; the best `topk_groups` of `num_groups`
     groups, each scored by the sum of its best `group_best` keys; weights divided by their sum or not, times
-    `scale`."""
-    return ep_router(SCORINGS[scoring], num_groups, topk_groups, group_best, int(renormalize), scale)
+    `scale`.  A key is the sigmoid score plus the bias; with softmax, the "logit" plus the bias or the "score" plus
+    the bias.  A softmax router that was trained with a bias on its scores, or with group_best=2 on scores, needs
+    softmax_key="score": with a bias or group_best=2 the two choose other experts."""
+    return ep_router(SCORINGS[scoring], num_groups, topk_groups, group_best, int(renormalize), scale,
+                     SOFTMAX_KEYS[softmax_key])
 
 
 def problem(T: int, H: int, k: int, E: int, R: int, G: int | None = None) -> ep_problem:

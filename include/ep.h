@@ -64,8 +64,13 @@ enum { EP_BF16 = 0, EP_FP8_E4M3 = 1 };
 enum { EP_FP32 = 2 };   /* routing logits only: EP_BF16 or EP_FP32 */
 enum { EP_WIRE_MXFP8 = 1, EP_WIRE_NVFP4 = 2 };
 enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
+enum { EP_KEY_LOGIT = 0, EP_KEY_SCORE = 1 };
 
-/* How ep_route turns a token's logits into experts and weights. */
+/* How ep_route turns a token's logits into experts and weights.  A router
+ * trained with a bias on its softmax scores, or with groups scored by sums of
+ * them, needs EP_KEY_SCORE: with EP_KEY_LOGIT a bias, and sums of two keys,
+ * choose other experts (without either both choose the same, but for scores
+ * that round to the same number). */
 typedef struct ep_router {
     int32_t scoring;      /* EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID               */
     int32_t num_groups;   /* g: experts are g equal consecutive groups; E % g == 0 */
@@ -73,6 +78,9 @@ typedef struct ep_router {
     int32_t group_best;   /* a group's score: sum of its best 1 or 2 keys       */
     int32_t renormalize;  /* nonzero: divide the weights by their sum           */
     float scale;          /* factor on the weights, finite                      */
+    int32_t softmax_key;  /* EP_SCORE_SOFTMAX: what the bias is added to and groups
+                             are scored by: EP_KEY_LOGIT or EP_KEY_SCORE (sigmoid
+                             scores: always the score)                          */
 } ep_router;
 
 /* Text for the last failing call on this thread ("" if none). */
@@ -394,8 +402,9 @@ int ep_selftest_wait_timeout(uint32_t *words, uint32_t polls, int32_t *dev_statu
  *
  * x = logits[t, :] (fp32 or bf16, widened exactly), b = bias (fp32 [E], or
  * NULL for zero).  All arithmetic is fp32.
- *   key_e   = x_e + b_e (EP_SCORE_SOFTMAX) or 1 / (1 + exp(-x_e)) + b_e
- *             (EP_SCORE_SIGMOID).  The bias moves the choice, never a weight.
+ *   key_e   = x_e + b_e (EP_SCORE_SOFTMAX with EP_KEY_LOGIT) or s_e + b_e
+ *             (EP_SCORE_SIGMOID, and EP_SCORE_SOFTMAX with EP_KEY_SCORE), s_e as
+ *             below.  The bias moves the choice, never a weight.
  *   Expert e is eligible if x_e and key_e are neither NaN nor -inf.  (A logit
  *   of -inf takes an expert out; a row of them is a padding token.)  A NaN
  *   logit or bias raises EP_STATUS_BAD_LOGIT.  A logit of +inf counts as the
