@@ -52,7 +52,8 @@ struct FewShared {
     unsigned char w[kStages<SWIGLU>][(SWIGLU ? 2 : 1) * kOperand];
     unsigned char rows[kStages<SWIGLU>][kRows * kBlock];
     uint64_t rows_full[kStages<SWIGLU>], full[kStages<SWIGLU>];   // rows and scales; all operands
-    uint64_t done[kStages<SWIGLU>];                               // a step's products: buffers free, sums ready
+    uint64_t done[kStages<SWIGLU>];                               // a step's products: buffers free, sums, scales and
+                                                                  // rows ready
     uint64_t tempty[kAcc];                                        // accumulators taken out
     uint64_t swapped, joined;                                     // the ends of a SwiGLU unit
     alignas(16) float row_scale[kScaleRing][kRows];               // (read 16 bytes at a time, as are the maxima)
@@ -82,9 +83,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&s.rows_full[i], kCopyThreads);
+            mbar_init(&s.rows_full[i], kCopyThreads + 2);   // the copies' own arrivals; two warps for what they stored
             mbar_init(&s.full[i], 2);          // the boxes' bytes, word of the rows
-            mbar_init(&s.done[i], 1);
+            mbar_init(&s.done[i], 2);          // the products' commit, word of the rows
         }
         for (int i = 0; i < kAcc; ++i) mbar_init(&s.tempty[i], 8);
         mbar_init(&s.swapped, 8);
@@ -159,7 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
             __syncwarp();
         } else if (warp == 2) {
-            // ---- word of the rows ----
+            // ---- word of the rows: to the products, and to the accumulation, which reads the scales and the rows'
+            // numbers with ordinary loads and has no other release of them to wait for (the commit's arrival tells of
+            // the products) ----
             if (lane == 0) {
                 int st = 0, ph = 0;
                 bool ok = true;
@@ -168,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = mbar_wait_or_abort(&s.rows_full[st], ph, abort);
                         if (!ok) break;
                         fence_async_shared();
+                        mbar_arrive(&s.done[st]);
                         mbar_arrive(&s.full[st]);
                         if (++st == S) { st = 0; ph ^= 1; }
                     }
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kMine; ++i) m[i] = v.m0 + i * kStep + part;
             m[kMine] = v.m0 + place;
             receive_rows(a, v.e, m, row);
-            if (warp < 6) s.row[unit % kScaleRing][place] = row[kMine];   // (announced with the first step's copies)
+            if (warp < 6) s.row[unit % kScaleRing][place] = row[kMine];
 #pragma unroll
             for (int i = 0; i <= kMine; ++i) row[i] = (int)((uint32_t)row[i] * kb_n);
             uint32_t ws = (uint32_t)(v.e * n_blocks + v.nb) * kb_n;
@@ -210,6 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (has_scale) cp_async4(smem_addr(&s.row_scale[ring][place]), a.a_scales + (uint32_t)(row[kMine] + kb));
                 if (warp == 7 && lane < NB) cp_async4(smem_addr(&s.w_scale[ring][lane]), a.w_scales + (ws + kb));
                 cp_async_arrive(&s.rows_full[st]);
+                // the copies' arrival speaks for the copies only: an ordinary one releases the stores to s.row (every
+                // step, since the barrier's count is)
+                __syncwarp();
+                if (warp < 6 && lane == 0) mbar_arrive(&s.rows_full[st]);
                 if (++st == S) { st = 0; ph ^= 1; }
                 ring = (ring + 1) % kScaleRing;
             }
