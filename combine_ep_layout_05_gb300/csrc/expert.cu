@@ -72,7 +72,8 @@ struct Plan {
 struct ExpertShared {
     unsigned char buf[kStages][2 * kOperand];              // rows, then matrix rows
     uint64_t rows_full[kStages], full[kStages];            // this CTA's rows and scales; all operands of both CTAs
-    uint64_t done[kStages];                                // a step's products: its buffers are free, its sums ready
+    uint64_t done[kStages];                                // a step's products: its buffers are free, its sums and
+                                                           // this CTA's scales ready
     uint64_t tempty[2];                                    // accumulators taken out
     uint64_t plan_full[kPlans], plan_empty[kPlans];
     uint64_t joined;                                       // maxima of a unit are written
@@ -142,7 +143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         for (int i = 0; i < S; ++i) {
             mbar_init(&s.rows_full[i], kCopyWarps * 32);
             mbar_init(&s.full[i], 3);      // (the first CTA's) the bytes of both CTAs' boxes, word of both CTAs' rows
-            mbar_init(&s.done[i], 1);
+            mbar_init(&s.done[i], 2);      // the products' commit, word of this CTA's rows and scales
         }
         for (int i = 0; i < 2; ++i) mbar_init(&s.tempty[i], 16);   // (the first CTA's) the accumulating warps of both
         for (int i = 0; i < kPlans; ++i) {
@@ -218,8 +219,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             int st = 0, ph = 0, acc = 0, aph = 1, last = -1;
             for (; next_plan(); plan_used()) {
                 for (int kb = 0; kb < (rank == 0 ? kb_n : 0); ++kb) {
-                    ok = warp_wait(&s.full[st], ph, abort) && warp_wait(&s.tempty[acc], aph, abort);
+                    ok = warp_wait<true>(&s.full[st], ph, abort) && warp_wait<true>(&s.tempty[acc], aph, abort);
                     if (!ok) break;
+                    acquire_shared_of_cluster();
                     tmem_fence_after();
                     if (issue) {
                         const uint64_t da = desc + (uint32_t)(st * (2 * kOperand >> 4)), db = da + (kOperand >> 4);
@@ -237,7 +239,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             }
             if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
         } else if (warp == 2) {
-            // ---- word of this CTA's copied rows and scales to the first CTA ----
+            // ---- word of this CTA's copied rows and scales: to this CTA's accumulation, which reads the scales with
+            // ordinary loads (the commit's arrival tells of the products), and to the first CTA's products ----
             const uint32_t full = cluster_addr(&s.full[0], 0);
             int st = 0, ph = 0;
             for (; next_plan(); plan_used()) {
@@ -245,7 +248,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                     ok = warp_wait(&s.rows_full[st], ph, abort);
                     if (!ok) break;
                     fence_async_shared();
-                    if (lane == 0) mbar_arrive_cluster(full + st * 8);
+                    if (lane == 0) {
+                        mbar_arrive(&s.done[st]);
+                        release_shared_to_cluster();
+                        mbar_arrive_relaxed_cluster(full + st * 8);
+                    }
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
@@ -331,6 +338,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         // 32-byte stores where rows start at multiples of 32 bytes (a thread stores along its row, so that a warp's
         // store touches 32 lines: 16 bytes each took twice as many)
         const bool wide = SWIGLU ? ((uintptr_t)a.q & 31) == 0 : ((uintptr_t)a.y & 31) == 0 && n_cols % 16 == 0;
+        // Arrivals on tempty order no memory and need not: they say that this warp's loads from tensor memory are
+        // complete, and the fences of tcgen05 before them and after the products' wait order tensor memory.  (Releases
+        // at cluster scope here, by 16 warps a step, took 4.6 ms in place of 1.75.)  The scales
+        // of a step, which the copies of a later one overwrite, were read into registers eight steps before the release
+        // that those copies wait for (kScaleRing - kStages - 2).
         int it = 0, unit = 0;       // (one counter of steps: registers are short here)
         for (; next_plan(); plan_used(), ++unit) {
             const bool some = quarter * 32 < s.plan[slot].rows;     // rows in this warp's lanes
@@ -356,13 +368,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                         if (b == NB - 1) {
                             tmem_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(tempty + p * 8);
+                            if (lane == 0) mbar_arrive_relaxed_cluster(tempty + p * 8);
                         }
 #pragma unroll
                         for (int c = 0; c < 32; ++c) fma2(acc[b][c], pair2(t[2 * c], t[2 * c + 1]), sc[b]);
                     }
                 } else if (lane == 0) {
-                    mbar_arrive_cluster(tempty + p * 8);
+                    mbar_arrive_relaxed_cluster(tempty + p * 8);
                 }
             }
             if (!ok) break;

@@ -11,13 +11,26 @@ namespace ep {
 
 namespace {
 
+// The test for arrivals of the other CTA's threads; orders no memory by itself.
+__device__ __forceinline__ bool mbar_try_wait_relaxed_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits for a phase of an mbarrier.  Gives up after about two seconds of
 // clocks, or as soon as another thread of the CTA has given up; the caller
 // then drains what it has in flight and leaves.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+    const auto over = [&]() { return CLUSTER ? mbar_try_wait_relaxed_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (over()) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!over()) {
         if (*abort) return false;
         if (clock64() - t0 > (1ll << 32)) {
             *abort = 1;
@@ -29,8 +42,9 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parit
 
 // The same for a whole warp; every lane polls (one lane's poll and a shuffle
 // of its result took 1.1 to 1.2 times as long in the expert products).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(kFull, mbar_wait_or_abort(bar, parity, abort));
+    return __all_sync(kFull, mbar_wait_or_abort<CLUSTER>(bar, parity, abort));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -43,8 +57,23 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Shared memory of a CTA, handed to a thread of the other CTA of its pair: the
+// release, of what this thread has written and seen in its own CTA's shared
+// memory, before a relaxed arrival, and the acquire after a relaxed wait.
+// Restricted to shared memory, the only kind that crosses: a release of all
+// memory at cluster scope takes 1900 to 2700 cycles (8192 tokens' SwiGLU over
+// 32 experts 3.4 ms with one for each step, 1.75 so).
+__device__ __forceinline__ void release_shared_to_cluster() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void acquire_shared_of_cluster() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+// Arrival on a barrier of either CTA that orders no memory by itself: after
+// the release above, or for word of tensor memory's accumulators, which tcgen05's
+// own fences on both sides order.
+__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // one lane of a converged warp, always the same
 __device__ __forceinline__ bool elect_one() {

@@ -205,3 +205,36 @@ def bad_operands(m, R, Tr, E, k, N, K, rows):
 
 def test_few_rows_nan_and_infinities(m):
     bad_operands(m, 2, 30, 8, 4, 768, 384, 20)
+
+
+# Many rows an expert: 16 experts of about 300 rows and 32 or 16 column tiles are 7 to 13 units for each of 76 pairs, so
+# that the ring of 4 plans goes around two or three times.  One or two long segments come in boxes, 16 short ones by threads.
+MANY = [(2, 600, 16, 4, 8192, 128, 300), (16, 80, 16, 4, 8192, 128, 320), (2, 600, 16, 4, 4096, 1024, 300),
+        (16, 80, 16, 4, 4096, 1024, 320), (4, 160, 16, 2, 8192, 256, 90), (1, 1200, 16, 4, 8192, 384, 600)]
+
+
+@pytest.mark.parametrize("R,Tr,E,k,N,K,rows", MANY)
+def test_many_rows_many_units(m, R, Tr, E, k, N, K, rows):
+    assert R * Tr * k > 48 * E
+    c = case(m, R, Tr, E, k, N, K, spread(R, Tr, E, rows, N + K + rows))
+    check_gemm(m, *c)
+    check_swiglu(m, *c)
+
+
+@pytest.mark.parametrize("K", [128, 640])
+def test_many_rows_rule_with_uneven_experts(m, K):
+    """One expert of 8 takes every token, the others none to three: tiles of one row, in the kernel for many rows."""
+    R, Tr, E, k, N = 4, 256, 8, 2, 4096
+    counts = np.zeros((R, E), np.int32)
+    counts[:, 6] = Tr
+    counts[0, 0] = counts[3, 7] = 1
+    counts[:3, 3] = 1
+    assert R * Tr * k > 48 * E
+    c = case(m, R, Tr, E, k, N, K, counts)
+    check_gemm(m, *c)
+    check_swiglu(m, *c)
+
+
+@pytest.mark.parametrize("R,Tr,E", [(2, 200, 4), (8, 50, 8)])
+def test_many_rows_nan_and_infinities(m, R, Tr, E):
+    bad_operands(m, R, Tr, E, 4, 768, 384, 180)
