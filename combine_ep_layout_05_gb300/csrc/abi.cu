@@ -633,6 +633,7 @@ int prepare_expert(const ep_problem *p, int64_t N, int64_t K, const uint8_t *act
     a.w_scales = w_scales;
     a.tokens_per_expert = tokens_per_expert;
     a.dev_status = dev_status;
+    a.wait_clocks = ep::kWaitClocks;
     return EP_OK;
 }
 
@@ -739,6 +740,30 @@ int ep_expert_swiglu(const ep_problem *p, int64_t intermediate, const uint8_t *a
     a.q_scales = q_scales;
     cudaError_t e = ep::launch_expert(a, (cudaStream_t)stream);
     return e ? cuda_fail(e, "ep_expert_swiglu launch") : EP_OK;
+}
+
+int ep_selftest_expert_timeout(const ep_problem *p, int kernel, int64_t out_features, int64_t in_features,
+                               const uint8_t *act, const float *a_scales, const uint8_t *w, const float *w_scales,
+                               const int32_t *tokens_per_expert, uint16_t *y, uint8_t *q, float *q_scales,
+                               int64_t clocks, int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    if (kernel != EP_EXPERT_FEW_ROWS && kernel != EP_EXPERT_MANY_ROWS)
+        return fail(EP_ERR_INVALID_ARG, "unknown kernel %d", kernel);
+    if (clocks < 1 || clocks > ep::kWaitClocks) return fail(EP_ERR_INVALID_ARG, "clocks must be in 1..2^32");
+    if (!dev_status) return fail(EP_ERR_INVALID_ARG, "dev_status is NULL");
+    ep::ExpertArgs a{};
+    const int rc = prepare_expert(p, out_features, in_features, act, a_scales, w, w_scales, tokens_per_expert,
+                                  dev_status, a);
+    if (rc != EP_OK || a.d.T == 0) return rc;
+    if (y ? !aligned(y, 16) : !q || !aligned(q, 16) || !q_scales || !aligned(q_scales, 4) || out_features % 256)
+        return fail(EP_ERR_INVALID_ARG, "y, or q and q_scales (out_features a multiple of 256), NULL or misaligned");
+    a.y = y;
+    a.q = y ? nullptr : q;
+    a.q_scales = q_scales;
+    a.wait_clocks = clocks;
+    cudaError_t e = kernel == EP_EXPERT_FEW_ROWS ? ep::launch_expert_few(a, (cudaStream_t)stream)
+                                                 : ep::launch_expert_many(a, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_selftest_expert_timeout launch") : EP_OK;
 }
 
 }  // extern "C"

@@ -22,8 +22,8 @@
 // overlapping; a box costs some 80 cycles of the copy unit, whatever its size,
 // so that from kBoxes boxes on threads copy the rows, 16 bytes each, in the
 // swizzle that the products expect.  Warps of a CTA: 0 issues the boxes, 1 (of
-// the first CTA) the products, 2 passes on that the rows and scales copied by
-// warps 4-7 are there, 3 plans the units ahead; eight warps (two warpgroups,
+// the first CTA) the products, 2 passes on that the boxes and the rows and scales
+// copied by warps 4-7 are there, 3 plans the units ahead; eight warps (two warpgroups,
 // one for each half of the columns) scale, accumulate and store: a thread owns
 // a row.
 //
@@ -66,12 +66,13 @@ struct Plan {
     int e, nb;            // expert (-1: no more units) and column tile
     int rows;             // this CTA's rows, at most 128
     int boxes;            // boxes that bring them, or -1: the threads copy them
-    uint32_t expect;      // bytes of both CTAs' boxes in a step
+    uint32_t expect;      // bytes of this CTA's boxes in a step
 };
 
 struct ExpertShared {
     unsigned char buf[kStages][2 * kOperand];              // rows, then matrix rows
-    uint64_t rows_full[kStages], full[kStages];            // this CTA's rows and scales; all operands of both CTAs
+    uint64_t boxes[kStages], rows_full[kStages];           // this CTA's boxes; its copied rows and scales
+    uint64_t full[kStages];                                // (the first CTA's) all operands of both CTAs
     uint64_t done[kStages];                                // a step's products: its buffers are free, its sums and
                                                            // this CTA's scales ready
     uint64_t tempty[2];                                    // accumulators taken out
@@ -84,7 +85,8 @@ struct ExpertShared {
     int3 box[kPlans][kBoxes];                              // first row, place, log2 of the height
     WorkList list;
     uint32_t tmem;
-    int abort;
+    int issued;                                            // steps whose products the first CTA has issued
+    int gave_up;
 };
 
 __device__ __forceinline__ int clamp_rows(int n) { return min(max(n, 0), kBlock); }
@@ -132,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
     ExpertShared &s = *reinterpret_cast<ExpertShared *>(raw);
     constexpr int S = kStages, NB = 2;
-    static_assert(offsetof(ExpertShared, rows_full) % 8 == 0 && offsetof(ExpertShared, w_scale) % 8 == 0, "");
+    static_assert(offsetof(ExpertShared, boxes) % 8 == 0 && offsetof(ExpertShared, w_scale) % 8 == 0, "");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();                           // place in the pair
     const int kb_n = (int)(a.K / kBlock);
@@ -141,9 +143,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
+            mbar_init(&s.boxes[i], 1);
             mbar_init(&s.rows_full[i], kCopyWarps * 32);
-            mbar_init(&s.full[i], 3);      // (the first CTA's) the bytes of both CTAs' boxes, word of both CTAs' rows
-            mbar_init(&s.done[i], 2);      // the products' commit, word of this CTA's rows and scales
+            mbar_init(&s.full[i], 2);      // word of both CTAs
+            mbar_init(&s.done[i], 2);      // the products' commit, word of this CTA's operands
         }
         for (int i = 0; i < 2; ++i) mbar_init(&s.tempty[i], 16);   // (the first CTA's) the accumulating warps of both
         for (int i = 0; i < kPlans; ++i) {
@@ -151,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             mbar_init(&s.plan_empty[i], kPlanUsers);
         }
         mbar_init(&s.joined, 8);
-        s.abort = 0;
+        s.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<2>(&s.tmem);
@@ -161,13 +164,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     cluster_sync();    // the other CTA's barriers are there too
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
-    volatile int *abort = &s.abort;
+    const Patience patience{&s.gave_up, a.wait_clocks};
 
-    // the next unit's plan, for a whole warp; false after the last one (or an abort)
+    // the next unit's plan, for a whole warp; false after the last one (or where patience ran out)
     int slot = 0, pph = 0;
     bool ok = true;
     const auto next_plan = [&]() {
-        ok = warp_wait(&s.plan_full[slot], pph, abort);
+        ok = warp_wait(&s.plan_full[slot], pph, patience);
         return ok && s.plan[slot].e >= 0;
     };
     const auto plan_used = [&]() {
@@ -180,7 +183,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0) {
             // ---- boxes: the matrix rows, and the rows where few boxes bring them ----
-            const uint32_t full = cluster_addr(&s.full[0], 0);
             int st = 0, ph = 1, it = 0;
             for (; next_plan(); plan_used()) {
                 const Plan &v = s.plan[slot];
@@ -189,37 +191,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 const uint32_t expect = v.expect;
                 const int e = v.e, w_row = v.nb * tile_cols + rank * (SWIGLU ? n_cols : kBlock);
                 for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                    ok = warp_wait(&s.done[st], ph, abort);
+                    ok = warp_wait(&s.done[st], ph, patience);
                     if (!ok) break;
-                    if (lane == 0 && rank == 0) mbar_expect_tx(&s.full[st], expect);
+                    if (lane == 0) mbar_expect_tx(&s.boxes[st], expect);
                     __syncwarp();
                     if (mine)
-                        tma_load_2d_pair(s.buf[st] + x.y * kBlock, &maps.a[x.z], kb * kBlock, x.x, full + st * 8);
+                        tma_load_2d(s.buf[st] + x.y * kBlock, &maps.a[x.z], kb * kBlock, x.x, &s.boxes[st]);
                     else if (lane == 31)
-                        tma_load_3d<2>(s.buf[st] + kOperand, &maps.w, kb * kBlock, w_row, e, full + st * 8);
+                        tma_load_3d(s.buf[st] + kOperand, &maps.w, kb * kBlock, w_row, e, &s.boxes[st]);
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
             }
-            // No copy may land after the pair has left.  Only where something gave up is one still in flight then:
-            // the first CTA's barriers count both CTAs' boxes; the second gives its own a millisecond.
-            if (!ok) {
-                if (rank == 0) {
-                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
-                } else {
-                    const long long t0 = clock64();
-                    while (clock64() - t0 < (1 << 21)) {}
-                }
-            }
+            drain<S>(s.boxes, it);
+            __syncwarp();
         } else if (warp == 1) {
             // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
             constexpr uint32_t idesc = mma_idesc(kPairRows, NB * kBlock);
             const bool issue = elect_one();
             const uint64_t desc = smem_desc(s.buf[0]);
-            int st = 0, ph = 0, acc = 0, aph = 1, last = -1;
+            int st = 0, ph = 0, acc = 0, aph = 1, it = 0;
             for (; next_plan(); plan_used()) {
-                for (int kb = 0; kb < (rank == 0 ? kb_n : 0); ++kb) {
-                    ok = warp_wait<true>(&s.full[st], ph, abort) && warp_wait<true>(&s.tempty[acc], aph, abort);
+                for (int kb = 0; kb < (rank == 0 ? kb_n : 0); ++kb, ++it) {
+                    ok = warp_wait<true>(&s.full[st], ph, patience) && warp_wait<true>(&s.tempty[acc], aph, patience);
                     if (!ok) break;
                     acquire_shared_of_cluster();
                     tmem_fence_after();
@@ -230,22 +224,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                             mma_f8<2>(tmem + acc * 256, da + k * 2, db + k * 2, idesc, k > 0);
                         mma_commit<2>(&s.done[st]);
                     }
-                    last = st | ph << 8;
                     if (++st == S) { st = 0; ph ^= 1; }
                     acc ^= 1;
                     aph ^= acc == 0;
                 }
                 if (!ok) break;
             }
-            if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
+            if (rank == 0 && lane < 2) store_cluster(cluster_addr(&s.issued, lane), it);
+            __syncwarp();
         } else if (warp == 2) {
-            // ---- word of this CTA's copied rows and scales: to this CTA's accumulation, which reads the scales with
-            // ordinary loads (the commit's arrival tells of the products), and to the first CTA's products ----
+            // ---- word of this CTA's boxes, copied rows and scales: to this CTA's accumulation, which reads the scales
+            // with ordinary loads (the commit's arrival tells of the products), and to the first CTA's products ----
             const uint32_t full = cluster_addr(&s.full[0], 0);
             int st = 0, ph = 0;
             for (; next_plan(); plan_used()) {
                 for (int kb = 0; kb < kb_n; ++kb) {
-                    ok = warp_wait(&s.rows_full[st], ph, abort);
+                    ok = warp_wait(&s.rows_full[st], ph, patience) && warp_wait(&s.boxes[st], ph, patience);
                     if (!ok) break;
                     fence_async_shared();
                     if (lane == 0) {
@@ -264,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             int u = blockIdx.x >> 1;
             while (true) {
                 // (after a round of the plans, the users of the one before have finished with it)
-                ok = warp_wait(&s.plan_empty[slot], pph ^ 1, abort);
+                ok = warp_wait(&s.plan_empty[slot], pph ^ 1, patience);
                 if (!ok) break;
                 const bool more = u < units;
                 if (more) {
@@ -281,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                     for (int i = 0; i < 4; ++i) s.row[slot][lane + 32 * i] = row[i];
                     if (lane == 0)
                         s.plan[slot] = Plan{v.e, v.nb, n, most <= kBoxes ? boxes : -1,
-                                            2 * kOperand + (most <= kBoxes ? bytes + other : 0)};
+                                            kOperand + (most <= kBoxes ? bytes : 0)};
                 } else if (lane == 0) {
                     s.plan[slot].e = -1;
                 }
@@ -311,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
             uint32_t ws = (uint32_t)(v.e * n_blocks + blk) * kb_n;
             if (lane == 1) ws += SWIGLU ? n_blocks / 2 * kb_n : blk + 1 < n_blocks ? kb_n : 0;   // (zeros beyond N)
             for (int kb = 0; kb < kb_n; ++kb) {
-                ok = warp_wait(&s.done[st], ph, abort);
+                ok = warp_wait(&s.done[st], ph, patience);
                 if (!ok) break;
                 const uint32_t dst = smem_addr(s.buf[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
                 const uint8_t *src = a.a + kb * kBlock + piece * 16;
@@ -352,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) acc[b][c] = 0;
             for (int end = it + kb_n; it < end; ++it) {
-                ok = warp_wait(&s.done[it % S], it / S & 1, abort);
+                ok = warp_wait(&s.done[it % S], it / S & 1, patience);
                 if (!ok) break;
                 const int p = it & 1, ring = it % kScaleRing;
                 if (some) {
@@ -402,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 s.amax[unit & 1][half][r] = amax;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.joined);
-                ok = warp_wait(&s.joined, unit & 1, abort);
+                ok = warp_wait(&s.joined, unit & 1, patience);
                 if (!ok) break;
                 const float other = s.amax[unit & 1][half ^ 1][r];
                 amax = amax != amax || other != other ? __uint_as_float(0x7fffffffu) : fmaxf(amax, other);
@@ -450,12 +444,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();    // nothing of the other CTA arrives here, or reads from here, any more
+    cluster_sync();    // the other CTA's threads arrive here no more, and its boxes have landed
     if (warp == 1) {
+        drain<S>(s.done, s.issued);      // products read both CTAs' shared memory and arrive in both
+        __syncwarp();
         tmem_fence_after();
         tmem_free<2>(tmem);
     }
-    if (threadIdx.x == 0 && s.abort) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+    if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
 }
 
 template <bool SWIGLU>

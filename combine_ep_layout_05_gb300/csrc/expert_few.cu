@@ -51,6 +51,7 @@ template <bool SWIGLU>
 struct FewShared {
     unsigned char w[kStages<SWIGLU>][(SWIGLU ? 2 : 1) * kOperand];
     unsigned char rows[kStages<SWIGLU>][kRows * kBlock];
+    uint64_t boxes[kStages<SWIGLU>];                              // matrix rows
     uint64_t rows_full[kStages<SWIGLU>], full[kStages<SWIGLU>];   // rows and scales; all operands
     uint64_t done[kStages<SWIGLU>];                               // a step's products: buffers free, sums, scales and
                                                                   // rows ready
@@ -63,7 +64,7 @@ struct FewShared {
     int row[kScaleRing][kRows];                                   // a unit's receive rows (kept like the scales)
     WorkList list;
     uint32_t tmem;
-    int abort;
+    int gave_up;
 };
 
 template <bool SWIGLU>
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
     FewShared<SWIGLU> &s = *reinterpret_cast<FewShared<SWIGLU> *>(raw);
     constexpr int S = kStages<SWIGLU>, NB = SWIGLU ? 2 : 1;
-    static_assert(offsetof(FewShared<SWIGLU>, rows) % 1024 == 0 && offsetof(FewShared<SWIGLU>, rows_full) % 8 == 0, "");
+    static_assert(offsetof(FewShared<SWIGLU>, rows) % 1024 == 0 && offsetof(FewShared<SWIGLU>, boxes) % 8 == 0, "");
     static_assert(offsetof(FewShared<SWIGLU>, row_scale) % 16 == 0 && offsetof(FewShared<SWIGLU>, amax) % 16 == 0, "");
     static_assert(kScaleRing > S + kAcc + 1, "scales are still in use when they are overwritten");
     const Dims &d = a.d;
@@ -84,13 +85,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&s.rows_full[i], kCopyThreads + 2);   // the copies' own arrivals; two warps for what they stored
-            mbar_init(&s.full[i], 2);          // the boxes' bytes, word of the rows
-            mbar_init(&s.done[i], 2);          // the products' commit, word of the rows
+            mbar_init(&s.boxes[i], 1);
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.done[i], 2);          // the products' commit, word of the operands
         }
         for (int i = 0; i < kAcc; ++i) mbar_init(&s.tempty[i], 8);
         mbar_init(&s.swapped, 8);
         mbar_init(&s.joined, 8);
-        s.abort = 0;
+        s.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<1>(&s.tmem);
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
     const int units = s.list.first[E] * col_tiles;   // below 2^31: checked on the host
-    volatile int *abort = &s.abort;
+    const Patience patience{&s.gave_up, a.wait_clocks};
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -112,32 +114,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                     const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
                     for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                        ok = mbar_wait_or_abort(&s.done[st], ph, abort);
+                        ok = mbar_wait(&s.done[st], ph, patience);
                         if (!ok) break;
-                        mbar_expect_tx(&s.full[st], NB * kOperand);
+                        mbar_expect_tx(&s.boxes[st], NB * kOperand);
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
-                            tma_load_3d<1>(s.w[st] + b * kOperand, &map_w, kb * kBlock, v.nb * kBlock + b * n_cols, v.e,
-                                           smem_addr(&s.full[st]));
+                            tma_load_3d(s.w[st] + b * kOperand, &map_w, kb * kBlock, v.nb * kBlock + b * n_cols, v.e,
+                                        &s.boxes[st]);
                         if (++st == S) { st = 0; ph ^= 1; }
                     }
                 }
-                // no copy may land after the CTA has left (only where something gave up is one still in flight)
-                if (!ok)
-                    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&s.full[i % S], (i / S) & 1);
+                drain<S>(s.boxes, it);
             }
             __syncwarp();
         } else if (warp == 1) {
             // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
             const bool issue = elect_one();
             const uint64_t dw = smem_desc(s.w[0]), dr = smem_desc(s.rows[0]);
-            int st = 0, ph = 0, acc = 0, aph = 1, last = -1;
+            int st = 0, ph = 0, acc = 0, aph = 1, it = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const Unit v = find_unit(s.list, E, kRows, col_tiles, u);
                 const uint32_t idesc = mma_idesc(kBlock, (v.rows + 15) & ~15);
-                for (int kb = 0; kb < kb_n; ++kb) {
-                    ok = warp_wait(&s.full[st], ph, abort) && warp_wait(&s.tempty[acc], aph, abort);
+                for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                    ok = warp_wait(&s.full[st], ph, patience) && warp_wait(&s.tempty[acc], aph, patience);
                     if (!ok) break;
                     tmem_fence_after();
                     if (issue) {
@@ -151,16 +151,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           k > 0);
                         mma_commit<1>(&s.done[st]);
                     }
-                    last = st | ph << 8;
                     if (++st == S) { st = 0; ph ^= 1; }
                     acc = (acc + 1) % kAcc;
                     aph ^= acc == 0;
                 }
             }
-            if (!ok && last >= 0) mbar_wait_bounded(&s.done[last & 255], last >> 8);
+            drain<S>(s.done, it);
             __syncwarp();
         } else if (warp == 2) {
-            // ---- word of the rows: to the products, and to the accumulation, which reads the scales and the rows'
+            // ---- word of the operands: to the products, and to the accumulation, which reads the scales and the rows'
             // numbers with ordinary loads and has no other release of them to wait for (the commit's arrival tells of
             // the products) ----
             if (lane == 0) {
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                     for (int kb = 0; kb < kb_n; ++kb) {
-                        ok = mbar_wait_or_abort(&s.rows_full[st], ph, abort);
+                        ok = mbar_wait(&s.rows_full[st], ph, patience) && mbar_wait(&s.boxes[st], ph, patience);
                         if (!ok) break;
                         fence_async_shared();
                         mbar_arrive(&s.done[st]);
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 1) ws += n_blocks / 2 * kb_n;             // (SwiGLU: the up block's)
             const bool has_scale = warp < 6 && place < v.rows;
             for (int kb = 0; kb < kb_n; ++kb) {
-                ok = warp_wait(&s.done[st], ph, abort);
+                ok = warp_wait(&s.done[st], ph, patience);
                 if (!ok) break;
                 const uint32_t dst = smem_addr(s.rows[st]) + part * kBlock + ((piece ^ (part & 7)) << 4);
                 const uint8_t *src = a.a + kb * kBlock + piece * 16;
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kMine / 2; ++c) acc[c] = 0;
             for (int kb = 0; kb < kb_n; ++kb) {
-                ok = warp_wait(&s.done[st], ph, abort);
+                ok = warp_wait(&s.done[st], ph, patience);
                 if (!ok) break;
                 tmem_fence_after();
                 uint32_t t[kMine];
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.swapped);
-                ok = warp_wait(&s.swapped, unit & 1, abort);
+                ok = warp_wait(&s.swapped, unit & 1, patience);
                 if (!ok) break;
                 const int n = min(v.rows - half * H, H);   // rows among this warpgroup's columns (may be negative)
                 uint32_t top = 0;                          // lane c: of column c
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < n) s.amax[half * H + lane][quarter] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.joined);
-                ok = warp_wait(&s.joined, unit & 1, abort);
+                ok = warp_wait(&s.joined, unit & 1, patience);
                 if (!ok) break;
                 float inv = 0.f;                           // lane c: of column c
                 if (lane < n) {
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_after();
         tmem_free<1>(tmem);
     }
-    if (threadIdx.x == 0 && s.abort) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+    if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
 }
 
 template <bool SWIGLU>

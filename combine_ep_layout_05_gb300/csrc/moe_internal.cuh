@@ -21,6 +21,8 @@ struct RouteArgs {
     int32_t *dev_status;
 };
 
+constexpr int64_t kWaitClocks = (int64_t)1 << 32;   // after which the expert products' waits give up: some two seconds
+
 struct ExpertArgs {
     Dims d;
     int64_t N, K;            // matrix rows (2 * I with SwiGLU) and channels
@@ -33,6 +35,7 @@ struct ExpertArgs {
     uint8_t *q;              // e4m3 codes and scales of the SwiGLU
     float *q_scales;
     int32_t *dev_status;
+    int64_t wait_clocks;
 };
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);

@@ -11,40 +11,65 @@ namespace ep {
 
 namespace {
 
-// The test for arrivals of the other CTA's threads; orders no memory by itself.
-__device__ __forceinline__ bool mbar_try_wait_relaxed_cluster(uint64_t *bar, uint32_t parity) {
+// Whether a phase is over: asked at once (SLEEP false), or after sleeping until
+// it is, or for as long as the hardware lets a thread sleep.  CLUSTER: for
+// arrivals of the other CTA's threads; orders no memory by itself.
+template <bool SLEEP, bool CLUSTER>
+__device__ __forceinline__ bool mbar_over(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+#define EP_MBAR_OVER(WAIT)                                                                                        \
+    asm volatile("{ .reg .pred p; mbarrier." WAIT ".shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"          \
+                 : "=r"(ok)                                                                                       \
+                 : "r"(smem_addr(bar)), "r"(parity)                                                               \
+                 : "memory")
+    if (SLEEP && CLUSTER) EP_MBAR_OVER("try_wait.parity.relaxed.cluster");
+    else if (SLEEP) EP_MBAR_OVER("try_wait.parity");
+    else if (CLUSTER) EP_MBAR_OVER("test_wait.parity.relaxed.cluster");
+    else EP_MBAR_OVER("test_wait.parity");
+#undef EP_MBAR_OVER
     return ok != 0;
 }
 
-// Waits for a phase of an mbarrier.  Gives up after about two seconds of
-// clocks, or as soon as another thread of the CTA has given up; the caller
-// then drains what it has in flight and leaves.
+// How long a thread waits: until `clocks` cycles have passed, or another
+// thread of the CTA has set the flag because they had.
+struct Patience {
+    volatile int *gave_up;
+    long long clocks;
+};
+
+// Waits for a phase of an mbarrier; false if patience ran out.  The caller then
+// leaves, and what it has in flight is drained at the end.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    const auto over = [&]() { return CLUSTER ? mbar_try_wait_relaxed_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (over()) return true;
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const Patience &p) {
+    if (mbar_over<false, CLUSTER>(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!over()) {
-        if (*abort) return false;
-        if (clock64() - t0 > (1ll << 32)) {
-            *abort = 1;
+    do {
+        if (clock64() - t0 > p.clocks) {
+            *p.gave_up = 1;
             return false;
         }
-    }
-    return true;
+        if (mbar_over<true, CLUSTER>(bar, parity)) return true;
+    } while (!*p.gave_up);
+    return false;
 }
 
 // The same for a whole warp; every lane polls (one lane's poll and a shuffle
 // of its result took 1.1 to 1.2 times as long in the expert products).
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(kFull, mbar_wait_or_abort<CLUSTER>(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Patience &p) {
+    return __all_sync(kFull, mbar_wait<CLUSTER>(bar, parity, p));
+}
+
+// Waits for the phases of steps [max(0, n - S), n) of a ring of S barriers:
+// of copies and products that have been issued and so end by themselves.
+// Every CTA does, so that nothing is in flight when it leaves, whether it gave
+// up or not.  All steps together get a second (2^31 cycles).
+template <int S>
+__device__ __forceinline__ void drain(uint64_t *bars, int n) {
+    const long long t0 = clock64();
+    for (int i = n > S ? n - S : 0; i < n; ++i)
+        while (!mbar_try_wait(&bars[i % S], i / S & 1))
+            if (clock64() - t0 > (1ll << 31)) return;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -81,6 +106,10 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
     return r != 0;
 }
+// a word of the shared memory of either CTA
+__device__ __forceinline__ void store_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -90,30 +119,19 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One box of a 3-d tensor map -> this CTA's shared memory; its bytes are
-// counted on bar (a cluster address: of a pair, CG = 2, either CTA's).
-template <int CG>
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-    if (CG == 2)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-            "{%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-            "%4}], [%5];" ::"r"(smem_addr(dst)),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-            : "memory");
-}
-
-// the same from a 2-d tensor map, counted in the first CTA of a pair
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+// One box of a tensor map -> this CTA's shared memory; its bytes are counted on bar.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
 

@@ -26,6 +26,7 @@ EP_RANK_MAJOR, EP_EXPERT_MAJOR = 0, 1
 EP_BF16, EP_FP8_E4M3, EP_FP32 = 0, 1, 2
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_KEY_LOGIT, EP_KEY_SCORE = 0, 1
+EP_EXPERT_FEW_ROWS, EP_EXPERT_MANY_ROWS = 0, 1
 EP_WIRE_MXFP8, EP_WIRE_NVFP4 = 1, 2
 WIRES = {"mxfp8": EP_WIRE_MXFP8, "nvfp4": EP_WIRE_NVFP4}
 
@@ -40,7 +41,7 @@ EXPORTS = ("ep_last_error_string", "ep_get_status", "ep_recv_rows", "ep_layout_w
            "ep_dequant_fp8", "ep_layout_noalloc", "ep_layout_dispatch_workspace_bytes", "ep_layout_dispatch",
            "ep_selftest_wait_timeout", "ep_combine_quantize", "ep_combine_wire", "ep_stage_rows",
            "ep_dispatch_two_level", "ep_combine_two_level", "ep_route", "ep_route_backward",
-           "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu")
+           "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu", "ep_selftest_expert_timeout")
 
 
 class EpError(RuntimeError):
@@ -139,6 +140,8 @@ def _load():
     lib.ep_expert_gemm.restype = i
     lib.ep_expert_swiglu.argtypes = [pp, i64, P, P, P, P, P, P, P, P, P]
     lib.ep_expert_swiglu.restype = i
+    lib.ep_selftest_expert_timeout.argtypes = [pp, i, i64, i64, P, P, P, P, P, P, P, P, i64, P, P]
+    lib.ep_selftest_expert_timeout.restype = i
     return lib
 
 
@@ -504,6 +507,22 @@ def ep_expert_swiglu(p: ep_problem, a, a_scales, w, w_scales, tokens_per_expert,
         _ptr(tokens_per_expert, torch.int32, "tokens_per_expert", p.num_ranks * E), _ptr(q, u8, "q", rows * I),
         _ptr(q_scales, f32, "q_scales", rows * (I // 128)), _ptr(dev_status, torch.int32, "dev_status", 1),
         _stream(stream)))
+
+
+def ep_selftest_expert_timeout(p: ep_problem, kernel: int, a, a_scales, w, w_scales, tokens_per_expert, y, q, q_scales,
+                               clocks: int, dev_status, stream=None) -> None:
+    """ep_expert_gemm (y) or ep_expert_swiglu (y None: q, q_scales) by the kernel for few or many rows an expert
+    (EP_EXPERT_*), with waits that give up after `clocks` cycles and raise EP_STATUS_TIMEOUT."""
+    N, K = _expert_shape(p, w, "w")
+    E, rows, u8, f32 = p.num_experts, p.num_experts * p.num_tokens, torch.uint8, torch.float32
+    return _call("ep_selftest_expert_timeout", _lib.ep_selftest_expert_timeout, (
+        ctypes.byref(p), int(kernel), N, K, _ptr(a, u8, "a", rows * K),
+        _ptr(a_scales, f32, "a_scales", rows * (K // 128)), _ptr(w, u8, "w"),
+        _ptr(w_scales, f32, "w_scales", E * ((N + 127) // 128) * (K // 128)),
+        _ptr(tokens_per_expert, torch.int32, "tokens_per_expert", p.num_ranks * E),
+        _ptr(y, torch.bfloat16, "y", rows * N), _ptr(q, u8, "q", rows * (N // 2)),
+        _ptr(q_scales, f32, "q_scales", rows * (N // 256)), int(clocks),
+        _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
 
 
 def ep_selftest_wait_timeout(words, polls: int, dev_status, stream=None) -> None:

@@ -65,6 +65,7 @@ enum { EP_FP32 = 2 };   /* routing logits only: EP_BF16 or EP_FP32 */
 enum { EP_WIRE_MXFP8 = 1, EP_WIRE_NVFP4 = 2 };
 enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
 enum { EP_KEY_LOGIT = 0, EP_KEY_SCORE = 1 };
+enum { EP_EXPERT_FEW_ROWS = 0, EP_EXPERT_MANY_ROWS = 1 };   /* ep_selftest_expert_timeout only */
 
 /* How ep_route turns a token's logits into experts and weights.  A router
  * trained with a bias on its softmax scores, or with groups scored by sums of
@@ -496,6 +497,21 @@ int ep_expert_gemm(const ep_problem *p, int64_t out_features, int64_t in_feature
 int ep_expert_swiglu(const ep_problem *p, int64_t intermediate, const uint8_t *a, const float *a_scales,
                      const uint8_t *w, const float *w_scales, const int32_t *tokens_per_expert, uint8_t *q,
                      float *q_scales, int32_t *dev_status, ep_stream_t stream);
+
+/*
+ * ep_selftest_expert_timeout - failure-detection self-test: the expert products
+ * with waits that give up after `clocks` cycles (1 .. 2^32, the products' own
+ * limit), by the kernel for few or for many rows an expert.
+ *
+ * y not NULL: ep_expert_gemm; else ep_expert_swiglu of in_features channels and
+ * out_features = 2 I matrix rows.  A launch whose waits give up raises
+ * EP_STATUS_TIMEOUT in *dev_status (not NULL), leaves any part of its output
+ * unwritten and returns with nothing in flight.
+ */
+int ep_selftest_expert_timeout(const ep_problem *p, int kernel, int64_t out_features, int64_t in_features,
+                               const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales,
+                               const int32_t *tokens_per_expert, uint16_t *y, uint8_t *q, float *q_scales,
+                               int64_t clocks, int32_t *dev_status, ep_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -238,3 +238,36 @@ def test_many_rows_rule_with_uneven_experts(m, K):
 @pytest.mark.parametrize("R,Tr,E", [(2, 200, 4), (8, 50, 8)])
 def test_many_rows_nan_and_infinities(m, R, Tr, E):
     bad_operands(m, R, Tr, E, 4, 768, 384, 180)
+
+
+@pytest.mark.parametrize("R,Tr", [(2, 320), (16, 40)])       # rows in boxes, and copied by threads
+@pytest.mark.parametrize("kernel", ["EP_EXPERT_FEW_ROWS", "EP_EXPERT_MANY_ROWS"])
+def test_waits_that_give_up(m, kernel, R, Tr):
+    """A launch whose waits run out says so, comes back with nothing in flight, and the next one is right."""
+    E, N, K = 16, 2048, 1024
+    p, counts, live, a, s, w, ws = case(m, R, Tr, E, 4, N, K, spread(R, Tr, E, 200, 5))
+    rows = a.shape[0]
+
+    def run(clocks, gemm):
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        y = torch.full((rows, N), -5.0, dtype=torch.bfloat16, device=DEV) if gemm else None
+        q = None if gemm else torch.full((rows, N // 2), 0x55, dtype=torch.uint8, device=DEV)
+        qs = None if gemm else torch.full((rows, N // 256), -5.0, device=DEV)
+        m.ep_selftest_expert_timeout(p, getattr(m, kernel), a, s, w, ws, counts, y, q, qs, clocks, st)
+        return int(st.item()), (y,) if gemm else (q, qs)
+
+    for gemm in (True, False):
+        code, want = run(1 << 32, gemm)
+        assert code == 0
+        # the first wait that is not over at once gives up; longer limits run out further in, or not at all
+        assert run(1, gemm)[0] == m.EP_STATUS_TIMEOUT
+        for clocks in (200, 1000, 1800, 2500, 3500, 5000, 8000, 20000, 10 ** 9):
+            code, out = run(clocks, gemm)
+            assert code in (0, m.EP_STATUS_TIMEOUT) and (code == 0 or clocks < 10 ** 9)
+            for o, right in zip(out, want):
+                assert bool((o[~live] == right[~live]).all())          # never a row that does not count
+                assert code != 0 or torch.equal(o, right)
+            code, out = run(1 << 32, gemm)
+            assert code == 0 and all(torch.equal(o, right) for o, right in zip(out, want))
+    check_gemm(m, p, counts, live, a, s, w, ws)
+    check_swiglu(m, p, counts, live, a, s, w, ws)
