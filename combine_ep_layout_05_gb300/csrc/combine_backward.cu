@@ -8,7 +8,7 @@
 //
 // Bound by memory: each row of y is read once and each row of grad_y written
 // once.  32768 tokens rank-major, hidden 7168: 800 us, 6.8 TB/s, the copy rate;
-// 1024 tokens expert-major: 46 us, 5.4 TB/s (the launch and three dependent
+// 1024 tokens expert-major: 47 us, 5.3 TB/s (the launch and three dependent
 // loads before the rows are known are 9 us of it).
 #include "combine_device.cuh"
 #include "moe_internal.cuh"

@@ -28,8 +28,8 @@
 // a row.
 //
 // Measured: 8192 tokens x top-8 over 32 experts of 7168 x 2048 (2048 rows each):
-// SwiGLU 1.65 ms, 2.3 PFLOP/s; down product 0.94 ms, 2.05 PFLOP/s; the tensor pipe
-// is active 54% and 45% of the cycles.  A step takes some 950 cycles, bound by the
+// SwiGLU 1.74 to 1.79 ms, 2.2 PFLOP/s; down product 0.98 to 1.0 ms, 1.95 PFLOP/s;
+// the tensor pipe is active 53% and 45% of the cycles.  A step takes some 950 cycles, bound by the
 // way around an accumulator: 512 of products, 580 from the first load to its
 // release, and 800 of signals between the two CTAs' warps, over two accumulators.
 // Without the accumulation the same loop takes 730.

@@ -15,18 +15,25 @@
 // swap halves of their columns through shared memory at the end, and each
 // finishes its half.
 //
-// Measured: 32 tokens x top-8 over 256 experts of 7168 x 2048, SwiGLU: 645 us,
-// 7.4 TB/s (reading alone is faster than the copy that the rate is judged by, 6.8);
-// 1024 tokens 1.12 to 1.14 ms, 6.7 TB/s; one token's down product 24.6 us (117 MB;
-// 22 us from a graph, 17 of them memory, the rest launch and first tiles).
+// Measured: 32 tokens x top-8 over 256 experts of 7168 x 2048, SwiGLU: 680 to 720 us,
+// 6.7 to 7.1 TB/s (reading alone is faster than the copy that the rate is judged by,
+// 6.8); 1024 tokens 1.14 ms, 6.6 TB/s; one token's down product 25.0 us (117 MB; 22.9
+// from a graph, 17 of them memory, the rest launch and first tiles).
 #include <cstddef>
 
 #include "expert_device.cuh"
 
 // Most rows an expert, on average (tokens x top-k / experts, what the host
 // knows), for this kernel: a tile of 64 rows has to hold nearly every expert.
-// Measured against the other kernel, hidden 7168 x 2048, 32 experts: SwiGLU 190
-// and 205 us at 48 rows, 228 and 207 at 64; down product 87 and 108, 123 and 111.
+// Measured, this kernel / the other, hidden 7168 x 2048, SwiGLU in us:
+//                      32 rows        48 rows        64 rows
+//   256 experts, uniform    1141 / 1493    1200 / 1516    1755 / 1534
+//   256, popularity 1/rank  1373 / 1581    1564 / 1613    1835 / 1675
+//   32, uniform                             186 / 207      267 / 208
+// (down product of 256 experts at 48 rows: 634 / 819 uniform, 853 / 829 by 1/rank;
+// at 64: 987 / 819).  The counts are on the device, so the average is what the rule
+// has; where a few experts take every token it is the slower choice (all on 8 of
+// 256 experts: 303 / 124 at an average of 16 rows, 893 / 317 at 48).
 #ifndef EP_EXPERT_FEW_ROWS
 #define EP_EXPERT_FEW_ROWS 48
 #endif

@@ -15,8 +15,8 @@
 // the lowest lane that has it, and a shift of that lane's list; lane j notes
 // the key and the lane of round j and looks its index up at the end.
 //
-// Measured (256 experts, top-8, grouped sigmoid with a bias): 65536 tokens 60 us,
-// 990 instructions a token at 89% of the issue slots, of which some 200 are the
+// Measured (256 experts, top-8, grouped sigmoid with a bias): 65536 tokens 59.5 us,
+// 980 instructions a token at 90% of the issue slots, of which some 200 are the
 // exponentials and reciprocals of the scores, correctly rounded because a key
 // decides; the memory alone would take 11 us.  32 tokens: 3.3 us from a graph.
 #include "moe_internal.cuh"
@@ -358,9 +358,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, La
 
 // W lanes own a token: 16 where they can (k <= 16, E <= 512), for two tokens a
 // warp, because the part that entries need (lane j: entry j) takes as many
-// instructions for two tokens as for one.  Measured with 16 and 32 lanes: 32768
-// tokens x 256 experts, softmax, bf16: 12.0 and 17.9 us (the memory alone 5.4);
-// 4120 x 160, sigmoid, fp32: 2.5 and 3.0 us.
+// instructions for two tokens as for one.  Measured with 16 and 32 lanes, from a
+// graph: 32768 tokens x 256 experts, softmax, bf16: 10.9 and 13.9 us (the memory alone
+// 5.4; 65% of the issue slots are used: a token's loads and reductions wait for one
+// another); 4120 x 160, sigmoid, fp32: 2.7 and 3.3 us.
 // DENSE: softmax without renormalisation, where every logit has a gradient and
 // the row is read; otherwise only the chosen logits are.  The row of the
 // gradient is written whole (zeros, or the dense part), then lane j writes the

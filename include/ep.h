@@ -486,7 +486,7 @@ int ep_combine_backward(const ep_problem *p, int layout, const uint16_t *grad_ou
  *   w_scales [E, 2 I / 128, K / 128], K = p->hidden;
  *   h = gate / (1 + exp(-gate)) * up in fp32, then cast as ep_dispatch casts:
  *   per row and 128 channels q = e4m3(h * inv), scale = amax / 448, ready to
- *   be the a of ep_expert_gemm.  q [rows, I] e4m3, q_scales [rows, I / 128].
+ *   be the a of ep_expert_gemm.  A NaN among the 128 makes their scale NaN.  q [rows, I] e4m3, q_scales [rows, I / 128].
  *   H % 128 == 0, I % 128 == 0.
  * a, w, y and q 16-byte aligned; E * T < 2^31, and tiles of 64 rows x 128
  * columns, at most (E * T / 64 + E) * ceil(N / 128), below 2^31 - 2^16.
