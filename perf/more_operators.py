@@ -271,12 +271,15 @@ def _route(c, logits, bias):
 
 
 def _cast(x):
-    """x rounded to e4m3 with a scale for each 128 channels: the values the codes stand for."""
+    """x rounded to e4m3 with a scale for each 128 channels: the values the codes stand for.  (Quotients of two
+    tensors are rounded once; with a number on one side a reciprocal is taken, and many bf16 inputs lie on the border
+    of two codes.)"""
     b = x.view(*x.shape[:-1], -1, BLOCK)
     amax = b.abs().amax(-1, keepdim=True)
-    inv = torch.where(amax > 0, (E4M3_MAX / amax).clamp_max(3.4028234663852886e38), 0.0)
+    most = torch.full_like(amax, E4M3_MAX)
+    inv = torch.where(amax > 0, (most / amax).clamp_max(3.4028234663852886e38), 0.0)
     q = (b * inv).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).to(x.dtype)
-    return (q * (amax / E4M3_MAX)).view(x.shape)
+    return (q * (amax / most)).view(x.shape)
 
 
 def _widen(q, s):
@@ -375,9 +378,11 @@ def _exact_route(c, logits, bias):
 
 
 def _exact_cast(v):
+    """The cast's values.  Its factor 448 / amax and the product with it are 32-bit numbers by definition, which
+    decides the inputs that lie between two codes: bf16 ones often do."""
     top = v.reshape(v.shape[0], -1, BLOCK).abs().amax(2).repeat_interleave(BLOCK, 1)
-    unit = torch.where(top > 0, top, 1.0) / E4M3_MAX
-    return (v / unit).to(torch.float8_e4m3fn).double() * unit
+    inv = (torch.full_like(top, E4M3_MAX) / torch.where(top > 0, top, 1.0)).float()
+    return (v * inv.double()).float().to(torch.float8_e4m3fn).double() * top / E4M3_MAX
 
 
 def exact(case, seed):
