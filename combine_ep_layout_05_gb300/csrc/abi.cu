@@ -767,3 +767,199 @@ int ep_selftest_expert_timeout(const ep_problem *p, int kernel, int64_t out_feat
 }
 
 }  // extern "C"
+
+namespace {
+
+// A dense product's sizes
+struct LinearSizes {
+    int64_t M, K, N, wide;      // wide: rows of w
+};
+
+bool linear_sizes(int64_t rows, int64_t in_features, int64_t out_features, int activation, LinearSizes &d) {
+    if (activation < EP_ACT_NONE || activation > EP_ACT_SWIGLU)
+        return fail(EP_ERR_INVALID_ARG, "unknown activation %d", activation), false;
+    if (rows < 0 || rows > ((int64_t)1 << 30)) return fail(EP_ERR_INVALID_ARG, "rows must be in 0..2^30"), false;
+    if (in_features < 8 || in_features % 8 || in_features > (1 << 24))
+        return fail(EP_ERR_INVALID_ARG, "in_features must be a multiple of 8, at most 2^24"), false;
+    if (out_features < 1 || out_features > (1 << 24))
+        return fail(EP_ERR_INVALID_ARG, "out_features must be in 1..2^24"), false;
+    d = LinearSizes{rows, in_features, out_features, activation == EP_ACT_SWIGLU ? 2 * out_features : out_features};
+    // tiles of 256 x 128 of each product, and the splits of those that are few, are counted in 32 bits
+    const auto tiles = [](int64_t a, int64_t b) { return ((a + 255) / 256) * ((b + 127) / 128); };
+    if (tiles(d.M, d.wide) > (1 << 26) || tiles(d.M, d.K) > (1 << 26) || tiles(d.wide, d.K) > (1 << 26))
+        return fail(EP_ERR_INVALID_ARG, "product too large (over 2^26 tiles of 256 x 128)"), false;
+    return true;
+}
+
+size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// The parts of ep_linear_backward's workspace: G [M, wide up to a multiple of 8], sums of its columns by block, and
+// the parts of the two products (one after the other)
+struct BackwardParts {
+    int64_t g_stride;
+    int blocks, splits_x, splits_w;
+    size_t g, sums, parts, total;
+};
+BackwardParts backward_parts(const LinearSizes &d) {
+    BackwardParts b;
+    b.g_stride = (d.wide + 7) / 8 * 8;
+    b.blocks = ep::act_grad_blocks(d.M, d.N);
+    b.splits_x = ep::linear_splits(d.M, d.K, d.wide);
+    b.splits_w = ep::linear_splits(d.wide, d.K, d.M);
+    b.g = round16((size_t)d.M * b.g_stride * 2);
+    b.sums = round16((size_t)b.blocks * d.wide * 4);
+    const size_t px = b.splits_x > 1 ? (size_t)b.splits_x * d.M * d.K * 4 : 0;
+    const size_t pw = b.splits_w > 1 ? (size_t)b.splits_w * d.wide * d.K * 4 : 0;
+    b.parts = px > pw ? px : pw;
+    b.total = b.g + b.sums + b.parts;
+    return b;
+}
+
+// One product of the backward pass: straight into its output, or in parts that are summed
+cudaError_t backward_product(int form, int64_t R, int64_t C, int64_t L, int splits, const ep::LinearOperand &A,
+                             const ep::LinearOperand &B, bool out32, void *out, int64_t out_stride, float *parts,
+                             int32_t *dev_status, cudaStream_t st) {
+    ep::LinearArgs a{};
+    a.R = R;
+    a.C = C;
+    a.L = L;
+    a.splits = splits;
+    a.dev_status = dev_status;
+    a.wait_clocks = ep::kWaitClocks;
+    const bool split = splits > 1;
+    a.out32 = split || out32;
+    a.out = split ? parts : out;
+    a.out_stride = split ? C : out_stride;
+    a.split_stride = R * C;
+    a.out_align = ep::row_align(a.out, a.out_stride * (a.out32 ? 4 : 2));
+    if (cudaError_t e = ep::launch_linear(form, a, A, B, st)) return e;
+    if (!split) return cudaSuccess;
+    return ep::launch_sum_parts(ep::SumPartsArgs{parts, splits, R, C, out32, out, out_stride, false}, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ep_linear(int64_t rows, int64_t in_features, int64_t out_features, int activation, const uint16_t *x,
+              int64_t x_stride, const uint16_t *w, const float *bias, const uint16_t *residual,
+              int64_t residual_stride, int out_dtype, void *out, int64_t out_stride, uint16_t *pre,
+              int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    LinearSizes d;
+    if (!linear_sizes(rows, in_features, out_features, activation, d)) return EP_ERR_INVALID_ARG;
+    if (out_dtype != EP_BF16 && out_dtype != EP_FP32) return fail(EP_ERR_INVALID_ARG, "out must be EP_BF16 or EP_FP32");
+    if (x_stride < d.K || x_stride % 8 || x_stride >= (int64_t)1 << 38)
+        return fail(EP_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least in_features");
+    if (out_stride < d.N || (residual && residual_stride < d.N))
+        return fail(EP_ERR_INVALID_ARG, "out_stride / residual_stride smaller than out_features");
+    if (!aligned(dev_status, 4)) return fail(EP_ERR_INVALID_ARG, "dev_status misaligned");
+    if (d.M == 0) return EP_OK;
+    if (!x || !aligned(x, 16) || !w || !aligned(w, 16))
+        return fail(EP_ERR_INVALID_ARG, "x / w NULL or not 16-byte aligned");
+    if (!out || !aligned(out, out_dtype == EP_FP32 ? 4 : 2)) return fail(EP_ERR_INVALID_ARG, "out NULL or misaligned");
+    if (!aligned(bias, 4) || !aligned(residual, 2) || !aligned(pre, 2))
+        return fail(EP_ERR_INVALID_ARG, "bias / residual / pre misaligned");
+    ep::LinearArgs a{};
+    a.R = d.M;
+    a.C = d.N;
+    a.L = d.K;
+    a.act = activation;
+    a.bias = bias;
+    a.residual = residual;
+    a.residual_stride = residual_stride;
+    a.out32 = out_dtype == EP_FP32;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.pre = pre;
+    a.pre_stride = d.wide;
+    a.out_align = ep::row_align(out, out_stride * (a.out32 ? 4 : 2));
+    a.residual_align = ep::row_align(residual, residual_stride * 2);
+    // (the up half of a SwiGLU's pre-activations starts at column N)
+    a.pre_align = ep::row_align(pre, (activation == EP_ACT_SWIGLU ? d.N : d.wide) * 2);
+    a.splits = 1;
+    a.dev_status = dev_status;
+    a.wait_clocks = ep::kWaitClocks;
+    cudaError_t e = ep::launch_linear(ep::kFormForward, a, ep::LinearOperand{x, d.M, d.K, x_stride},
+                                      ep::LinearOperand{w, d.wide, d.K, d.K}, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_linear launch") : EP_OK;
+}
+
+size_t ep_linear_backward_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features, int activation) {
+    g_err[0] = 0;
+    LinearSizes d;
+    return linear_sizes(rows, in_features, out_features, activation, d) ? backward_parts(d).total : 0;
+}
+
+int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, int activation, int grad_dtype,
+                       const void *grad_out, int64_t grad_stride, const uint16_t *x, int64_t x_stride,
+                       const uint16_t *w, const uint16_t *pre, uint16_t *grad_x, int64_t grad_x_stride,
+                       int grad_w_dtype, void *grad_w, float *grad_bias, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    LinearSizes d;
+    if (!linear_sizes(rows, in_features, out_features, activation, d)) return EP_ERR_INVALID_ARG;
+    const bool grad32 = grad_dtype == EP_FP32, w32 = grad_w_dtype == EP_FP32;
+    if (!grad32 && grad_dtype != EP_BF16) return fail(EP_ERR_INVALID_ARG, "grad_out must be EP_BF16 or EP_FP32");
+    if (grad_w && !w32 && grad_w_dtype != EP_BF16) return fail(EP_ERR_INVALID_ARG, "grad_w must be EP_BF16 or EP_FP32");
+    if (grad_stride < d.N) return fail(EP_ERR_INVALID_ARG, "grad_stride smaller than out_features");
+    if (grad_x && grad_x_stride < d.K) return fail(EP_ERR_INVALID_ARG, "grad_x_stride smaller than in_features");
+    if (grad_w && (x_stride < d.K || x_stride % 8 || x_stride >= (int64_t)1 << 38))
+        return fail(EP_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least in_features");
+    if (!aligned(dev_status, 4)) return fail(EP_ERR_INVALID_ARG, "dev_status misaligned");
+    if (!aligned(grad_w, 16)) return fail(EP_ERR_INVALID_ARG, "grad_w not 16-byte aligned");
+    if (!aligned(grad_bias, 4) || !aligned(grad_x, 2)) return fail(EP_ERR_INVALID_ARG, "grad_bias / grad_x misaligned");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (d.M == 0) {
+        cudaError_t e = cudaSuccess;
+        if (grad_w) e = cudaMemsetAsync(grad_w, 0, (size_t)d.wide * d.K * (w32 ? 4 : 2), st);
+        if (!e && grad_bias) e = cudaMemsetAsync(grad_bias, 0, (size_t)d.wide * 4, st);
+        return e ? cuda_fail(e, "ep_linear_backward") : EP_OK;
+    }
+    if (!grad_x && !grad_w && !grad_bias) return EP_OK;
+    if (!grad_out || !aligned(grad_out, grad32 ? 4 : 2))
+        return fail(EP_ERR_INVALID_ARG, "grad_out NULL or misaligned");
+    if (activation != EP_ACT_NONE && (!pre || !aligned(pre, 2)))
+        return fail(EP_ERR_INVALID_ARG, "pre NULL or misaligned");
+    if (grad_w && (!x || !aligned(x, 16))) return fail(EP_ERR_INVALID_ARG, "x NULL or not 16-byte aligned");
+    if (grad_x && (!w || !aligned(w, 16))) return fail(EP_ERR_INVALID_ARG, "w NULL or not 16-byte aligned");
+    const BackwardParts b = backward_parts(d);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < b.total)
+        return fail(EP_ERR_INVALID_ARG, "workspace NULL, not 16-byte aligned or too small (%zu bytes, needs %zu)",
+                    workspace_bytes, b.total);
+    char *ws = (char *)workspace;
+    float *sums = (float *)(ws + b.g), *parts = (float *)(ws + b.g + b.sums);
+    // the tensor core reads a bf16 gradient where it lies, if rows start where its copies may
+    const bool direct = activation == EP_ACT_NONE && !grad32 && grad_stride % 8 == 0 &&
+                        grad_stride < (int64_t)1 << 38 && aligned(grad_out, 16);
+    const bool products = grad_x || grad_w;
+    cudaError_t e = cudaSuccess;
+    if (grad_bias || (products && !direct)) {
+        ep::ActGradArgs a{};
+        a.M = d.M;
+        a.N = d.N;
+        a.act = activation;
+        a.grad32 = grad32;
+        a.grad = grad_out;
+        a.grad_stride = grad_stride;
+        a.pre = pre;
+        a.G = products && !direct ? (uint16_t *)ws : nullptr;
+        a.G_stride = b.g_stride;
+        a.sums = grad_bias ? sums : nullptr;
+        a.blocks = b.blocks;
+        a.bias = grad_bias;
+        e = ep::launch_act_grad(a, st);
+        if (e) return cuda_fail(e, "ep_linear_backward launch");
+    }
+    const ep::LinearOperand G{direct ? (const uint16_t *)grad_out : (const uint16_t *)ws, d.M, d.wide,
+                              direct ? grad_stride : b.g_stride};
+    if (grad_x)
+        e = backward_product(ep::kFormGradX, d.M, d.K, d.wide, b.splits_x, G, ep::LinearOperand{w, d.wide, d.K, d.K},
+                             false, grad_x, grad_x_stride, parts, dev_status, st);
+    if (!e && grad_w)
+        e = backward_product(ep::kFormGradW, d.wide, d.K, d.M, b.splits_w, G, ep::LinearOperand{x, d.M, d.K, x_stride},
+                             w32, grad_w, d.K, parts, dev_status, st);
+    return e ? cuda_fail(e, "ep_linear_backward launch") : EP_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,305 @@
+// Dense products with an epilogue (ep_linear) and the products of their
+// gradients, for any number of rows.
+//
+//   out[r, c] = act(sum_l A(r, l) B(c, l) + bias[c]) + residual[r, c]
+//
+// bf16 operands, fp32 sums in tensor memory over the whole contraction, one
+// rounding at the end.  Three forms of the same loop, which differ in the way
+// the operands lie in memory:
+//   forward  A = x [M, K], B = w [N, K]: both along the contraction
+//   grad_x   A = G [M, N], B = w [N, K]: B along its rows (columns of w)
+//   grad_w   A = G [M, N], B = x [M, K]: both along their rows
+// Nothing is transposed in memory: the tensor core reads either form from
+// shared memory, with boxes of 128 rows x 64 contraction or of 64 x 64.
+//
+// A CTA pair computes 256 x 256 outputs (SwiGLU: 256 x 128, the gate's rows in
+// the first CTA's B, the up rows in the second's): each CTA holds 128 rows of A
+// and 128 of B, 32 KB a step of 64, and its rows' accumulators.  A CTA alone
+// (128 x 256) would write and read 96 KB of shared memory for each 512 cycles of
+// products, a CTA of the pair 64.  Two accumulators of 256 columns alternate, so
+// that one is stored while the other is summed.  Warps: 0 issues the boxes (whose
+// bytes are counted on the first CTA's barrier, wherever they land), 1 the
+// products (first CTA), 4 to 11 the epilogue: a thread owns a row of a half of
+// the columns.
+#include <algorithm>
+#include <cstddef>
+
+#include "linear_device.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kStages = 6;                      // 192 KB of operands
+constexpr int kTile = 2 * kPart;                // rows and columns of a pair's tile
+constexpr int kGroup = 8;                       // row tiles that are walked together, for L2
+
+struct LinearShared {
+    unsigned char buf[kStages][2 * kPartBytes];  // A, then B
+    uint64_t full[kStages];                     // (the first CTA's) both CTAs' operands
+    uint64_t empty[kStages];                    // a step's products are done
+    uint64_t tfull[2];                          // an accumulator is complete
+    uint64_t tempty[2];                         // (the first CTA's) taken out by both CTAs
+    uint32_t tmem;
+    int gave_up;
+};
+
+struct LinearMaps {
+    CUtensorMap a, b;
+};
+
+// A unit of work: a tile and a part of the contraction
+struct LinearUnit {
+    int row, col, split, first, last;           // tile, part, steps [first, last)
+};
+__device__ __forceinline__ LinearUnit linear_unit(const LinearArgs &a, int u) {
+    const int tiles = a.row_tiles * a.col_tiles;
+    LinearUnit v;
+    v.split = u / tiles;
+    const int t = u - v.split * tiles, per = kGroup * a.col_tiles, g = t / per;
+    const int in = t - g * per, n = min(kGroup, a.row_tiles - g * kGroup);
+    v.row = g * kGroup + in % n;
+    v.col = in / n;
+    v.first = v.split * a.split_steps;
+    v.last = min(v.first + a.split_steps, a.steps);
+    return v;
+}
+
+template <bool SWIGLU, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ LinearMaps maps) {
+    extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
+    LinearShared &s = *reinterpret_cast<LinearShared *>(raw);
+    constexpr int S = kStages;
+    static_assert(offsetof(LinearShared, full) % 8 == 0, "");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int units = a.row_tiles * a.col_tiles * a.splits, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], 16);
+        }
+        s.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<2>(&s.tmem);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();    // the other CTA's barriers are there too
+    tmem_fence_after();
+    const uint32_t tmem = s.tmem;
+    const Patience patience{&s.gave_up, a.wait_clocks};
+
+    if (warp == 0) {
+        // ---- boxes ----
+        if (lane == 0) {
+            const uint32_t full = cluster_addr(&s.full[0], 0);
+            int st = 0, ph = 1, it = 0;
+            bool ok = true;
+            for (int u = blockIdx.x >> 1; u < units && ok; u += pairs) {
+                const LinearUnit v = linear_unit(a, u);
+                const int r0 = v.row * kTile + rank * kPart;
+                const int c0 = SWIGLU ? rank * (int)a.C + v.col * kPart : v.col * kTile + rank * kPart;
+                for (int k = v.first; k < v.last; ++k, ++it) {
+                    ok = mbar_wait(&s.empty[st], ph, patience);
+                    if (!ok) break;
+                    if (rank == 0) mbar_expect_tx(&s.full[st], 4 * kPartBytes);
+                    unsigned char *pa = s.buf[st], *pb = pa + kPartBytes;
+                    const uint32_t bar = full + st * 8;
+                    if (A_MN) {
+                        tma_load_2d_pair(pa, &maps.a, r0 * 2, k * kStep, bar);
+                        tma_load_2d_pair(pa + kPartBytes / 2, &maps.a, r0 * 2 + 128, k * kStep, bar);
+                    } else {
+                        tma_load_2d_pair(pa, &maps.a, k * kStep * 2, r0, bar);
+                    }
+                    if (B_MN) {
+                        tma_load_2d_pair(pb, &maps.b, c0 * 2, k * kStep, bar);
+                        tma_load_2d_pair(pb + kPartBytes / 2, &maps.b, c0 * 2 + 128, k * kStep, bar);
+                    } else {
+                        tma_load_2d_pair(pb, &maps.b, k * kStep * 2, c0, bar);
+                    }
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+            }
+            drain<S>(s.empty, it);     // the products of a step follow its boxes
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
+        if (rank == 0) {
+            constexpr uint32_t idesc = mma_idesc_bf16(kTile, kTile, A_MN, B_MN);
+            const bool issue = elect_one();
+            const uint64_t da0 = A_MN ? smem_desc_mn(s.buf[0], kPartBytes / 2) : smem_desc(s.buf[0]);
+            const uint64_t db0 = B_MN ? smem_desc_mn(s.buf[0] + kPartBytes, kPartBytes / 2)
+                                      : smem_desc(s.buf[0] + kPartBytes);
+            // 16 of the contraction: 32 bytes along a row, or 16 lines of 128 bytes
+            constexpr uint32_t ka = A_MN ? 2048 >> 4 : 32 >> 4, kb = B_MN ? 2048 >> 4 : 32 >> 4;
+            int st = 0, ph = 0, acc = 0, aph = 1;
+            bool ok = true;
+            for (int u = blockIdx.x >> 1; u < units && ok; u += pairs) {
+                const LinearUnit v = linear_unit(a, u);
+                ok = warp_wait<true>(&s.tempty[acc], aph, patience);
+                if (!ok) break;
+                tmem_fence_after();
+                for (int k = v.first; k < v.last; ++k) {
+                    ok = warp_wait<true>(&s.full[st], ph, patience);
+                    if (!ok) break;
+                    acquire_shared_of_cluster();
+                    tmem_fence_after();
+                    if (issue) {
+                        const uint32_t at = (uint32_t)(st * (2 * kPartBytes >> 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16<2>(tmem + acc * kTile, da0 + at + i * ka, db0 + at + i * kb, idesc,
+                                        k > v.first || i > 0);
+                        mma_commit<2>(&s.empty[st]);
+                    }
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                if (issue) mma_commit<2>(&s.tfull[acc]);
+                acc ^= 1;
+                aph ^= acc == 0;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- epilogue ----
+        const int half = (warp - 4) >> 2, quarter = warp & 3;
+        const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536;
+        const uint32_t tempty = cluster_addr(&s.tempty[0], 0);
+        int acc = 0, ph = 0;
+        bool ok = true;
+        for (int u = blockIdx.x >> 1; u < units && ok; u += pairs) {
+            const LinearUnit v = linear_unit(a, u);
+            ok = warp_wait(&s.tfull[acc], ph, patience);
+            if (!ok) break;
+            tmem_fence_after();
+            const int64_t r = (int64_t)v.row * kTile + rank * kPart + quarter * 32 + lane;
+            const bool live = r < a.R;
+            constexpr int kCols = SWIGLU ? kPart / 2 : kPart;      // output columns of a thread
+            const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
+#pragma unroll 1
+            for (int q = 0; q < kCols / 32; ++q) {
+                __syncwarp();                  // (lanes whose rows do not exist come back early)
+                uint32_t t[SWIGLU ? 64 : 32];
+                const uint32_t at = tm + acc * kTile + half * kCols + q * 32;
+                tmem_ld16(at, t);
+                tmem_ld16(at + 16, t + 16);
+                if (SWIGLU) {
+                    tmem_ld16(at + kPart, t + 32);
+                    tmem_ld16(at + kPart + 16, t + 48);
+                }
+                tmem_wait_ld<(SWIGLU ? 64 : 32)>(t);
+                if (q == kCols / 32 - 1) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed_cluster(tempty + acc * 8);
+                }
+                const int64_t c = c0 + q * 32;
+                const int n = (int)min(a.C - c, (int64_t)32);
+                if (!live || n <= 0) continue;
+                float z[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(t[i]);
+                if (a.bias) add_vector(a.bias + c, z, n);
+                if (a.pre) store_bf16(a.pre + r * a.pre_stride + c, z, n, a.pre_align);
+                if (SWIGLU) {
+                    float up[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(t[(SWIGLU ? 32 : 0) + i]);
+                    if (a.bias) add_vector(a.bias + a.C + c, up, n);
+                    if (a.pre) store_bf16(a.pre + r * a.pre_stride + a.C + c, up, n, a.pre_align);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] = swiglu(z[i], up[i]);
+                } else if (a.act != EP_ACT_NONE) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] = activate(z[i], a.act);
+                }
+                if (a.residual) add_bf16(a.residual + r * a.residual_stride + c, z, n, a.residual_align);
+                if (a.out32)
+                    store_fp32(reinterpret_cast<float *>(a.out) + v.split * a.split_stride + r * a.out_stride + c, z, n,
+                               a.out_align);
+                else
+                    store_bf16(reinterpret_cast<uint16_t *>(a.out) + r * a.out_stride + c, z, n, a.out_align);
+            }
+            acc ^= 1;
+            ph ^= acc == 0;
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();    // nothing arrives here any more, and what reads this CTA's shared memory is done
+    if (warp == 1) {
+        tmem_fence_after();
+        tmem_free<2>(tmem);
+    }
+    if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+}
+
+// The operand as a tensor map of bytes.  Along the contraction: boxes of 128
+// rows x 128 bytes; along its rows: boxes of 64 of the contraction x 128 bytes.
+cudaError_t operand_map(const LinearOperand &o, bool mn, CUtensorMap *map) {
+    const cuuint64_t dims[2] = {(cuuint64_t)o.cols * 2, (cuuint64_t)o.rows}, strides[1] = {(cuuint64_t)o.stride * 2};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(mn ? kStep : kPart)};
+    return encode_map(map, 2, o.p, dims, strides, box);
+}
+
+template <bool SWIGLU, bool A_MN, bool B_MN>
+cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st) {
+    constexpr int bytes = sizeof(LinearShared);
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    static std::atomic<int> ready[kCacheDevices];
+    cudaError_t e = cudaSuccess;
+    cached_per_device(ready, [&](int) {
+        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        return e == cudaSuccess ? 1 : 0;
+    });
+    if (e) return e;
+    const int64_t units = (int64_t)a.row_tiles * a.col_tiles * a.splits;
+    const int grid = (int)std::min<int64_t>(num_sms() & ~1, 2 * units);
+    linear_kernel<SWIGLU, A_MN, B_MN><<<grid, kThreads, bytes, st>>>(a, maps);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// By the time that the pairs' turns take, in us: a step of 64 some 0.3, a unit's start and end 1.5, the parts' sum their
+// bytes at 5 TB/s and a launch.
+int linear_splits(int64_t R, int64_t C, int64_t L) {
+    const int64_t tiles = ((R + kTile - 1) / kTile) * ((C + kTile - 1) / kTile), steps = (L + kStep - 1) / kStep;
+    int best = 1;
+    double least = 1e30;
+    for (int64_t s = 1; s <= std::min<int64_t>(steps, 16); ++s) {
+        const int64_t per = (steps + s - 1) / s;
+        if ((steps + per - 1) / per != s) continue;          // every part has steps
+        const double turns = (double)((tiles * s + 75) / 76);
+        const double t = turns * (0.3 * per + 1.5) + (s > 1 ? 3.0 + 4e-6 * R * C * (s + 1) / 5.0 : 0.0);
+        if (t < least) { least = t; best = (int)s; }
+    }
+    return best;
+}
+
+cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st) {
+    const bool swiglu = form == kFormForward && a.act == EP_ACT_SWIGLU;
+    LinearMaps maps;
+    if (cudaError_t e = operand_map(A, form == kFormGradW, &maps.a)) return e;
+    if (cudaError_t e = operand_map(B, form != kFormForward, &maps.b)) return e;
+    const int cols = swiglu ? kPart : kTile;
+    a.row_tiles = (int)((a.R + kTile - 1) / kTile);
+    a.col_tiles = (int)((a.C + cols - 1) / cols);
+    a.steps = (int)((a.L + kStep - 1) / kStep);
+    a.split_steps = (a.steps + a.splits - 1) / a.splits;
+    if (form == kFormGradX) return launch<false, false, true>(a, maps, st);
+    if (form == kFormGradW) return launch<false, true, true>(a, maps, st);
+    return swiglu ? launch<true, false, false>(a, maps, st) : launch<false, false, false>(a, maps, st);
+}
+
+}  // namespace ep

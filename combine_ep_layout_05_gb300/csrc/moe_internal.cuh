@@ -38,6 +38,70 @@ struct ExpertArgs {
     int64_t wait_clocks;
 };
 
+// A dense product out[r, c] = sum over l of A(r, l) B(c, l), R x C x L, with its
+// epilogue: ep_linear, and the two products of its gradient.
+struct LinearArgs {
+    int64_t R, C, L;         // (SwiGLU: C output columns, 2 C rows of B)
+    int act;
+    const float *bias;
+    const uint16_t *residual;
+    int64_t residual_stride; // elements between rows, as below
+    bool out32;              // fp32 output, else bf16
+    void *out;
+    int64_t out_stride;
+    uint16_t *pre;           // or null: bf16 pre-activations [R, C or 2 C]
+    int64_t pre_stride;
+    int out_align, pre_align, residual_align;   // see row_align
+    int splits;              // parts of the contraction (at least 1; every part has steps)
+    int row_tiles, col_tiles, split_steps, steps;           // by the launcher
+    int64_t split_stride;    // elements between the partial sums of two splits
+    int32_t *dev_status;
+    int64_t wait_clocks;
+};
+
+// alignment, in bytes, of every 16th column of rows that start `stride` bytes apart
+inline int row_align(const void *p, int64_t stride) {
+    const uintptr_t a = (uintptr_t)p | (uintptr_t)stride;
+    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 1;
+}
+
+enum { kFormForward, kFormGradX, kFormGradW };   // what the operands are: see launch_linear
+struct LinearOperand {
+    const uint16_t *p;
+    int64_t rows, cols, stride;   // as they lie in memory: elements of a row side by side
+};
+
+struct ActGradArgs {         // G = grad_out * act'(pre), bf16, and its column sums
+    int64_t M, N;            // (SwiGLU: N columns of grad_out, 2 N of pre and G)
+    int act;
+    bool grad32;
+    const void *grad;
+    int64_t grad_stride;
+    const uint16_t *pre;
+    uint16_t *G;             // or null: only the sums
+    int64_t G_stride;
+    float *sums;             // or null: [blocks, columns of G] partial sums
+    int blocks;
+    float *bias;             // the sums' sum
+};
+
+struct SumPartsArgs {        // out = sum of parts [rows, cols], cols a multiple of 8, one after the other
+    const float *p;
+    int parts;
+    int64_t rows, cols;
+    bool out32;
+    void *out;
+    int64_t stride;          // elements between rows of out
+    bool vec;                // by the launcher
+};
+
+// Parts into which the contraction L of an R x C product is split
+int linear_splits(int64_t R, int64_t C, int64_t L);
+cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st);
+cudaError_t launch_act_grad(const ActGradArgs &a, cudaStream_t st);
+int act_grad_blocks(int64_t M, int64_t N);
+cudaError_t launch_sum_parts(SumPartsArgs a, cudaStream_t st);
+
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);
 cudaError_t launch_route_backward(const RouteArgs &a, const int64_t *topk_idx, cudaStream_t st);
 cudaError_t launch_combine_backward(int layout, const CombineArgs &a, const uint16_t *grad_out, uint16_t *grad_y,

@@ -26,12 +26,15 @@ EP_RANK_MAJOR, EP_EXPERT_MAJOR = 0, 1
 EP_BF16, EP_FP8_E4M3, EP_FP32 = 0, 1, 2
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_KEY_LOGIT, EP_KEY_SCORE = 0, 1
+EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_SWIGLU = 0, 1, 2, 3, 4
 EP_EXPERT_FEW_ROWS, EP_EXPERT_MANY_ROWS = 0, 1
 EP_WIRE_MXFP8, EP_WIRE_NVFP4 = 1, 2
 WIRES = {"mxfp8": EP_WIRE_MXFP8, "nvfp4": EP_WIRE_NVFP4}
 
 LAYOUTS = {"rank_major": EP_RANK_MAJOR, "expert_major": EP_EXPERT_MAJOR}
 SCORINGS = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+ACTIVATIONS = {"none": EP_ACT_NONE, "relu": EP_ACT_RELU, "silu": EP_ACT_SILU, "gelu": EP_ACT_GELU,
+               "swiglu": EP_ACT_SWIGLU}
 SOFTMAX_KEYS = {"logit": EP_KEY_LOGIT, "score": EP_KEY_SCORE}
 DTYPES = {"bf16": EP_BF16, "fp8_e4m3": EP_FP8_E4M3}
 
@@ -41,7 +44,8 @@ EXPORTS = ("ep_last_error_string", "ep_get_status", "ep_recv_rows", "ep_layout_w
            "ep_dequant_fp8", "ep_layout_noalloc", "ep_layout_dispatch_workspace_bytes", "ep_layout_dispatch",
            "ep_selftest_wait_timeout", "ep_combine_quantize", "ep_combine_wire", "ep_stage_rows",
            "ep_dispatch_two_level", "ep_combine_two_level", "ep_route", "ep_route_backward",
-           "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu", "ep_selftest_expert_timeout")
+           "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu", "ep_selftest_expert_timeout", "ep_linear",
+           "ep_linear_backward_workspace_bytes", "ep_linear_backward")
 
 
 class EpError(RuntimeError):
@@ -142,6 +146,12 @@ def _load():
     lib.ep_expert_swiglu.restype = i
     lib.ep_selftest_expert_timeout.argtypes = [pp, i, i64, i64, P, P, P, P, P, P, P, P, i64, P, P]
     lib.ep_selftest_expert_timeout.restype = i
+    lib.ep_linear.argtypes = [i64, i64, i64, i, P, i64, P, P, P, i64, i, P, i64, P, P, P]
+    lib.ep_linear.restype = i
+    lib.ep_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, i]
+    lib.ep_linear_backward_workspace_bytes.restype = sz
+    lib.ep_linear_backward.argtypes = [i64, i64, i64, i, i, P, i64, P, i64, P, P, P, i64, i, P, P, P, sz, P, P]
+    lib.ep_linear_backward.restype = i
     return lib
 
 
@@ -523,6 +533,101 @@ def ep_selftest_expert_timeout(p: ep_problem, kernel: int, a, a_scales, w, w_sca
         _ptr(y, torch.bfloat16, "y", rows * N), _ptr(q, u8, "q", rows * (N // 2)),
         _ptr(q_scales, f32, "q_scales", rows * (N // 256)), int(clocks),
         _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+def _rows(t, name, rows, cols, dtypes=(torch.bfloat16,)):
+    """(pointer, row stride) of a [rows, cols] tensor whose rows are contiguous (any row stride); None: (None, 0)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    stride = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), stride
+
+
+def _shaped(t, name, shape, dtypes):
+    """Pointer of a contiguous tensor of this shape (None: None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a tensor {list(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    return _ptr(t, None, name)
+
+
+def _one_device(*tensors):
+    """The library launches on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _linear_sizes(x, w, activation):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [rows, in_features]")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != x.shape[1]:
+        raise ValueError(f"w must be a tensor [rows, {x.shape[1]}]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    wide = w.shape[0]
+    if activation == "swiglu" and wide % 2:
+        raise ValueError("w must have an even number of rows with swiglu")
+    return x.shape[0], x.shape[1], wide // 2 if activation == "swiglu" else wide, wide
+
+
+_F16, _F32 = (torch.bfloat16,), (torch.float32,)
+
+
+def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "none", dev_status=None,
+              stream=None) -> None:
+    """out [M, N] (bf16 or fp32) = act(x [M, K] @ w.T + bias) + residual; w [N, K], with "swiglu" [2 N, K] (gate rows
+    first), bias fp32, residual [M, N] bf16 (may be out itself), pre [M, w's rows] bf16 receives the pre-activations."""
+    M, K, N, wide = _linear_sizes(x, w, activation)
+    xp, xs = _rows(x, "x", M, K)
+    op, os_ = _rows(out, "out", M, N, _F16 + _F32)
+    rp, rs = _rows(residual, "residual", M, N)
+    if out is None:
+        raise ValueError("out must be a tensor")
+    args = (M, K, N, ACTIVATIONS[activation], xp, xs, _shaped(w, "w", (wide, K), _F16),
+            _shaped(bias, "bias", (wide,), _F32), rp, rs, EP_FP32 if out.dtype == torch.float32 else EP_BF16, op, os_,
+            _shaped(pre, "pre", (M, wide), _F16), _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
+    _one_device(x, w, out, bias, residual, pre, dev_status)
+    return _call("ep_linear", _lib.ep_linear, args)
+
+
+def ep_linear_backward_workspace_bytes(rows: int, in_features: int, out_features: int, activation: str = "none") -> int:
+    return _lib.ep_linear_backward_workspace_bytes(rows, in_features, out_features, ACTIVATIONS[activation])
+
+
+def ep_linear_backward(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None, pre=None, activation: str = "none",
+                       workspace=None, dev_status=None, stream=None) -> None:
+    """Gradients of ep_linear from grad_out [M, N] (bf16 or fp32): grad_x [M, K] bf16, grad_w (w's shape, bf16 or fp32)
+    and grad_bias fp32, each left out if None; pre as ep_linear wrote it (not needed for "none"); workspace uint8 of
+    ep_linear_backward_workspace_bytes()."""
+    M, K, N, wide = _linear_sizes(x, w, activation)
+    xp, xs = _rows(x, "x", M, K)
+    gp, gs = _rows(grad_out, "grad_out", M, N, _F16 + _F32)
+    gxp, gxs = _rows(grad_x, "grad_x", M, K)
+    if grad_out is None:
+        raise ValueError("grad_out must be a tensor")
+    code = lambda t: EP_FP32 if t is not None and t.dtype == torch.float32 else EP_BF16
+    args = (M, K, N, ACTIVATIONS[activation], code(grad_out), gp, gs, xp, xs, _shaped(w, "w", (wide, K), _F16),
+            _shaped(pre, "pre", (M, wide), _F16), gxp, gxs, code(grad_w),
+            _shaped(grad_w, "grad_w", (wide, K), _F16 + _F32), _shaped(grad_bias, "grad_bias", (wide,), _F32),
+            _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
+            _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
+    _one_device(grad_out, x, w, grad_x, grad_w, grad_bias, pre, workspace, dev_status)
+    return _call("ep_linear_backward", _lib.ep_linear_backward, args)
 
 
 def ep_selftest_wait_timeout(words, polls: int, dev_status, stream=None) -> None:

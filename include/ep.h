@@ -65,6 +65,7 @@ enum { EP_FP32 = 2 };   /* routing logits only: EP_BF16 or EP_FP32 */
 enum { EP_WIRE_MXFP8 = 1, EP_WIRE_NVFP4 = 2 };
 enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
 enum { EP_KEY_LOGIT = 0, EP_KEY_SCORE = 1 };
+enum { EP_ACT_NONE = 0, EP_ACT_RELU = 1, EP_ACT_SILU = 2, EP_ACT_GELU = 3, EP_ACT_SWIGLU = 4 };
 enum { EP_EXPERT_FEW_ROWS = 0, EP_EXPERT_MANY_ROWS = 1 };   /* ep_selftest_expert_timeout only */
 
 /* How ep_route turns a token's logits into experts and weights.  A router
@@ -512,6 +513,63 @@ int ep_selftest_expert_timeout(const ep_problem *p, int kernel, int64_t out_feat
                                const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales,
                                const int32_t *tokens_per_expert, uint16_t *y, uint8_t *q, float *q_scales,
                                int64_t clocks, int32_t *dev_status, ep_stream_t stream);
+
+/*
+ * ep_linear - a dense product with bias, activation and residual: the gate that
+ * makes ep_route's logits, and the matrices of a shared expert, which every
+ * token goes through.  (No counterpart on the pages: an addition of this
+ * library, as are its gradient and ep_moe_few.)
+ *
+ * z[m, n] = sum_i x[m, i] * w[n, i] + bias[n], bf16 operands, fp32 sums;
+ * out[m, n] = act(z[m, n]) + residual[m, n], rounded once:
+ *   EP_ACT_NONE z, EP_ACT_RELU max(z, 0), EP_ACT_SILU z / (1 + exp(-z)),
+ *   EP_ACT_GELU z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3) (the
+ *   tanh form), EP_ACT_SWIGLU: w and bias have 2 N rows, gate rows first, and
+ *   out[m, n] = silu(z[m, n]) * z[m, N + n].
+ * pre (NULL: not written): bf16(z), what ep_linear_backward needs of an
+ * activation.
+ *
+ * x [rows, in_features] bf16, row m at x + m * x_stride; w [out_features (x 2),
+ * in_features] bf16, contiguous; bias fp32 or NULL; residual bf16 or NULL, with
+ * its own row stride; out bf16 (EP_BF16) or fp32 (EP_FP32), with its own; pre
+ * [rows, out_features (x 2)] bf16, contiguous.  Strides are in elements and not
+ * smaller than a row.  in_features % 8 == 0, x_stride % 8 == 0, x and w 16-byte
+ * aligned; any out_features (rows of out that start at multiples of 32 bytes are
+ * written fastest).  rows <= 2^30, in_features and out_features <= 2^24.  out may
+ * be the bf16 residual itself; other overlaps of outputs and inputs are not
+ * allowed.  Identical outputs on every run.
+ */
+int ep_linear(int64_t rows, int64_t in_features, int64_t out_features, int activation, const uint16_t *x,
+              int64_t x_stride, const uint16_t *w, const float *bias, const uint16_t *residual,
+              int64_t residual_stride, int out_dtype, void *out, int64_t out_stride, uint16_t *pre,
+              int32_t *dev_status, ep_stream_t stream);
+
+/* Bytes of device workspace ep_linear_backward needs (0 for invalid sizes).  Host-only. */
+size_t ep_linear_backward_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features, int activation);
+
+/*
+ * ep_linear_backward - gradients of ep_linear (the residual's is grad_out itself).
+ *
+ * G[m, n] = grad_out[m, n] * act'(pre[m, n]) in fp32 (EP_ACT_SWIGLU: 2 N columns,
+ * gate and up), from the bf16 pre-activations that ep_linear wrote;
+ *   grad_bias[n] = sum_m G[m, n];
+ *   grad_x[m, i] = sum_n bf16(G[m, n]) * w[n, i], rounded once to bf16;
+ *   grad_w[n, i] = sum_m bf16(G[m, n]) * x[m, i], rounded once if bf16.
+ * G is rounded to bf16 as an operand of the tensor core; a bf16 grad_out
+ * without an activation goes in exactly.  Sums are fp32.  An output that is NULL is not
+ * computed.  grad_out [rows, out_features] bf16 or fp32 (grad_dtype); pre NULL
+ * without an activation; grad_x bf16, row stride grad_x_stride; grad_w
+ * [out_features (x 2), in_features] bf16 or fp32 (grad_w_dtype), contiguous, 16-byte
+ * aligned; grad_bias fp32.  x (for grad_w) and w (for grad_x) as in ep_linear.
+ * rows = 0 makes grad_w and grad_bias zero.  workspace: 16-byte aligned, at least
+ * ep_linear_backward_workspace_bytes() bytes, overwritten.  Outputs, inputs and
+ * workspace must not overlap.  Identical outputs on every run.
+ */
+int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, int activation, int grad_dtype,
+                       const void *grad_out, int64_t grad_stride, const uint16_t *x, int64_t x_stride,
+                       const uint16_t *w, const uint16_t *pre, uint16_t *grad_x, int64_t grad_x_stride,
+                       int grad_w_dtype, void *grad_w, float *grad_bias, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, ep_stream_t stream);
 
 #ifdef __cplusplus
 }
