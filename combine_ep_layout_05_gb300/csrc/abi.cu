@@ -963,3 +963,85 @@ int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, 
 }
 
 }  // extern "C"
+
+namespace {
+
+// The parts of ep_moe_few's workspace, each from a multiple of 256 bytes on
+struct MoeFewParts {
+    size_t h, h_scales, y, arrived, total;
+};
+bool moe_few_parts(const ep::Dims &d, int64_t I, MoeFewParts &b) {
+    if (d.T > ep::kMoeFewTokens)
+        return fail(EP_ERR_INVALID_ARG, "ep_moe_few takes at most %d tokens", ep::kMoeFewTokens), false;
+    if (d.H % 128 || d.H > (1 << 24)) return fail(EP_ERR_INVALID_ARG, "hidden must be a multiple of 128, at most 2^24"), false;
+    if (I < 128 || I % 128 || I > (1 << 23))
+        return fail(EP_ERR_INVALID_ARG, "intermediate must be a multiple of 128, at most 2^23"), false;
+    if (d.H * I >= (int64_t)1 << 39) return fail(EP_ERR_INVALID_ARG, "hidden * intermediate must be below 2^39"), false;
+    const auto round = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    const size_t rows = (size_t)d.T * d.k;
+    b.h = round(rows * I);
+    b.h_scales = round(rows * (I / 128) * 4);
+    b.y = round(rows * d.H * 4);
+    b.arrived = round(d.H / 128 * 4);
+    b.total = b.h + b.h_scales + b.y + b.arrived;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ep_moe_few_workspace_bytes(const ep_problem *p, int64_t intermediate) {
+    g_err[0] = 0;
+    ep::Dims d;
+    MoeFewParts b;
+    return make_dims(p, d) && moe_few_parts(d, intermediate, b) ? b.total : 0;
+}
+
+int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, const uint16_t *x, int logits_dtype,
+               const void *logits, int64_t logits_row_stride, const float *bias, const uint8_t *gate_up,
+               const float *gate_up_scales, const uint8_t *down, const float *down_scales, const uint16_t *residual,
+               uint16_t *out, int64_t *topk_idx, float *topk_weights, void *workspace, size_t workspace_bytes,
+               int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    ep::Dims d;
+    MoeFewParts b;
+    if (!make_dims(p, d) || !moe_few_parts(d, intermediate, b)) return EP_ERR_INVALID_ARG;
+    ep::MoeFewArgs a{};
+    const int rc = prepare_route(p, r, logits_dtype, logits, logits_row_stride, dev_status, a.route);
+    if (rc != EP_OK || d.T == 0) return rc;
+    if (!aligned(bias, 4)) return fail(EP_ERR_INVALID_ARG, "bias misaligned");
+    if (!topk_idx || !aligned(topk_idx, 8) || !topk_weights || !aligned(topk_weights, 4))
+        return fail(EP_ERR_INVALID_ARG, "topk_idx / topk_weights NULL or misaligned");
+    if (!x || !aligned(x, 16) || !gate_up || !aligned(gate_up, 16) || !down || !aligned(down, 16))
+        return fail(EP_ERR_INVALID_ARG, "x / gate_up / down NULL or not 16-byte aligned");
+    if (!gate_up_scales || !aligned(gate_up_scales, 4) || !down_scales || !aligned(down_scales, 4))
+        return fail(EP_ERR_INVALID_ARG, "gate_up_scales / down_scales NULL or misaligned");
+    if (!out || !aligned(out, 8) || !aligned(residual, 8))
+        return fail(EP_ERR_INVALID_ARG, "out NULL, or out / residual not 8-byte aligned");
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < b.total)
+        return fail(EP_ERR_INVALID_ARG, "workspace NULL, not 256-byte aligned or too small (%zu bytes, needs %zu)",
+                    workspace_bytes, b.total);
+    char *ws = (char *)workspace;
+    a.route.bias = bias;
+    a.route.topk_idx = topk_idx;
+    a.route.topk_weights = topk_weights;
+    a.H = d.H;
+    a.I = intermediate;
+    a.x = x;
+    a.residual = residual;
+    a.gate_up = gate_up;
+    a.down = down;
+    a.gate_up_scales = gate_up_scales;
+    a.down_scales = down_scales;
+    a.h = (uint8_t *)ws;
+    a.h_scales = (float *)(ws + b.h);
+    a.y = (float *)(ws + b.h + b.h_scales);
+    a.arrived = (unsigned *)(ws + b.h + b.h_scales + b.y);
+    a.out = out;
+    a.wait_clocks = ep::kWaitClocks;
+    cudaError_t e = ep::launch_moe_few(a, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "ep_moe_few launch") : EP_OK;
+}
+
+}  // extern "C"

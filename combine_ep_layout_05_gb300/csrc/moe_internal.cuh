@@ -38,6 +38,21 @@ struct ExpertArgs {
     int64_t wait_clocks;
 };
 
+constexpr int kMoeFewTokens = 64;      // most tokens of ep_moe_few: a tile of every expert holds them
+
+struct MoeFewArgs {
+    RouteArgs route;         // T, E, k, logits and where the routing goes
+    int64_t H, I;
+    const uint16_t *x, *residual;
+    const uint8_t *gate_up, *down;
+    const float *gate_up_scales, *down_scales;
+    uint8_t *h;              // workspace: [T k, I] codes, [T k, I / 128] scales, [T k, H] products, [H / 128] counters
+    float *h_scales, *y;
+    unsigned *arrived;
+    uint16_t *out;
+    int64_t wait_clocks;
+};
+
 // A dense product out[r, c] = sum over l of A(r, l) B(c, l), R x C x L, with its
 // epilogue: ep_linear, and the two products of its gradient.
 struct LinearArgs {
@@ -98,6 +113,7 @@ struct SumPartsArgs {        // out = sum of parts [rows, cols], cols a multiple
 // Parts into which the contraction L of an R x C product is split
 int linear_splits(int64_t R, int64_t C, int64_t L);
 cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st);
+cudaError_t launch_moe_few(const MoeFewArgs &a, cudaStream_t st);
 cudaError_t launch_act_grad(const ActGradArgs &a, cudaStream_t st);
 int act_grad_blocks(int64_t M, int64_t N);
 cudaError_t launch_sum_parts(SumPartsArgs a, cudaStream_t st);

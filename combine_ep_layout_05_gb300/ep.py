@@ -45,7 +45,7 @@ EXPORTS = ("ep_last_error_string", "ep_get_status", "ep_recv_rows", "ep_layout_w
            "ep_selftest_wait_timeout", "ep_combine_quantize", "ep_combine_wire", "ep_stage_rows",
            "ep_dispatch_two_level", "ep_combine_two_level", "ep_route", "ep_route_backward",
            "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu", "ep_selftest_expert_timeout", "ep_linear",
-           "ep_linear_backward_workspace_bytes", "ep_linear_backward")
+           "ep_linear_backward_workspace_bytes", "ep_linear_backward", "ep_moe_few_workspace_bytes", "ep_moe_few")
 
 
 class EpError(RuntimeError):
@@ -152,6 +152,10 @@ def _load():
     lib.ep_linear_backward_workspace_bytes.restype = sz
     lib.ep_linear_backward.argtypes = [i64, i64, i64, i, i, P, i64, P, i64, P, P, P, i64, i, P, P, P, sz, P, P]
     lib.ep_linear_backward.restype = i
+    lib.ep_moe_few_workspace_bytes.argtypes = [pp, i64]
+    lib.ep_moe_few_workspace_bytes.restype = sz
+    lib.ep_moe_few.argtypes = [pp, rp, i64, P, i, P, i64, P, P, P, P, P, P, P, P, P, P, sz, P, P]
+    lib.ep_moe_few.restype = i
     return lib
 
 
@@ -628,6 +632,36 @@ def ep_linear_backward(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None,
             _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
     _one_device(grad_out, x, w, grad_x, grad_w, grad_bias, pre, workspace, dev_status)
     return _call("ep_linear_backward", _lib.ep_linear_backward, args)
+
+
+def ep_moe_few_workspace_bytes(p: ep_problem, intermediate: int) -> int:
+    return _lib.ep_moe_few_workspace_bytes(ctypes.byref(p), intermediate)
+
+
+def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_scales, down, down_scales, out, topk_idx,
+               topk_weights, workspace, residual=None, dev_status=None, stream=None) -> None:
+    """The layer of up to 64 tokens x [T, H] bf16: routes logits [T, E] (as ep_route, into topk_idx and topk_weights),
+    runs the chosen experts (gate_up [E, 2 I, H] and down [E, H, I], e4m3 codes with fp32 scales for 128 x 128 blocks)
+    and writes out [T, H] bf16 = their weighted sum + residual; workspace uint8 of ep_moe_few_workspace_bytes()."""
+    T, H, E, n = p.num_tokens, p.hidden, p.num_experts, p.num_tokens * p.num_topk
+    N, K = _expert_shape(p, gate_up, "gate_up")
+    I = N // 2
+    if N % 256 or K != H or H % 128:
+        raise ValueError(f"gate_up must be [{E}, 2 I, {H}], H and I multiples of 128, got {list(gate_up.shape)}")
+    u8, f32, bf16 = (torch.uint8,), (torch.float32,), (torch.bfloat16,)
+    ptr, stride, dt = _logits(logits, p, "logits")
+    args = (ctypes.byref(p), ctypes.byref(r), I, _shaped(x, "x", (T, H), bf16), dt, ptr, stride,
+            _ptr(bias, torch.float32, "bias", E), _shaped(gate_up, "gate_up", (E, N, H), u8),
+            _shaped(gate_up_scales, "gate_up_scales", (E, N // 128, H // 128), f32),
+            _shaped(down, "down", (E, H, I), u8),
+            _shaped(down_scales, "down_scales", (E, H // 128, I // 128), f32),
+            _shaped(residual, "residual", (T, H), bf16), _shaped(out, "out", (T, H), bf16),
+            _ptr(topk_idx, torch.int64, "topk_idx", n), _ptr(topk_weights, torch.float32, "topk_weights", n),
+            _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
+            _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
+    _one_device(x, logits, bias, gate_up, gate_up_scales, down, down_scales, residual, out, topk_idx, topk_weights,
+                workspace, dev_status)
+    return _call("ep_moe_few", _lib.ep_moe_few, args)
 
 
 def ep_selftest_wait_timeout(words, polls: int, dev_status, stream=None) -> None:

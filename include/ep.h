@@ -571,6 +571,35 @@ int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, 
                        int grad_w_dtype, void *grad_w, float *grad_bias, void *workspace, size_t workspace_bytes,
                        int32_t *dev_status, ep_stream_t stream);
 
+/* Bytes of device workspace ep_moe_few needs (0 for an invalid problem).  Host-only. */
+size_t ep_moe_few_workspace_bytes(const ep_problem *p, int64_t intermediate);
+
+/*
+ * ep_moe_few - a whole mixture-of-experts layer for up to 64 tokens (a decode
+ * step), in two launches that read each chosen expert's matrices once.
+ *
+ * The same as ep_route, the FP8 cast of ep_dispatch, ep_expert_swiglu, an ep_expert_gemm
+ * whose output stays fp32, and
+ *   out[t] = bf16( sum over kept entries j, in j order, of topk_weights[t, j] *
+ *            y[t, j] (+ residual[t]) ),  fp32, rounded once;
+ * topk_idx and topk_weights are ep_route's.  A token without an expert gets its
+ * residual, or zeros.  p's ranks and nodes are not used: no receive
+ * buffer is made.
+ *   x, residual (NULL: none) and out [T, H] bf16; logits, bias and the routing
+ *   as in ep_route; gate_up [E, 2 I, H] and down [E, H, I] e4m3 codes with
+ *   scales as in ep_expert_swiglu and ep_expert_gemm.
+ * T <= 64, H % 128 == 0, I % 128 == 0 (I = intermediate).  x, gate_up and down 16-byte
+ * aligned, residual and out 8-byte.  workspace: 256-byte aligned, at least
+ * ep_moe_few_workspace_bytes() bytes, overwritten; calls that may run at the
+ * same time need one each.  out may be the residual; other overlaps of outputs
+ * and inputs are not allowed.  Identical outputs on every run.
+ */
+int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, const uint16_t *x, int logits_dtype,
+               const void *logits, int64_t logits_row_stride, const float *bias, const uint8_t *gate_up,
+               const float *gate_up_scales, const uint8_t *down, const float *down_scales, const uint16_t *residual,
+               uint16_t *out, int64_t *topk_idx, float *topk_weights, void *workspace, size_t workspace_bytes,
+               int32_t *dev_status, ep_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
