@@ -19,12 +19,14 @@
 // work is 128 columns of h, which are one block of its cast.  Both products of
 // those columns land in the same thread.
 // Second launch: a unit is 128 output columns of one expert.  Its products, in fp32, go
-// to y [T, k, H] in the workspace; the CTA that brings a column tile's last
-// expert (a counter for each tile, which the first launch zeroes) adds the tile's k rows
+// to y [T, k, H] in the workspace; a CTA has a run of units, column tile after
+// column tile; the one that brings a tile's last expert (a counter of units for each
+// tile, which the first launch zeroes) adds the tile's k rows
 // of each token in the order j = 0 .. k - 1.  So the sum does not depend on who comes
 // last, and y is never rounded.  y is T k H 4 bytes against the experts' 3 I H each.
 #include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include "route_device.cuh"
 #include "tcgen05.cuh"
@@ -36,7 +38,7 @@ namespace {
 constexpr int kBlock = 128;                     // channels, and matrix rows, of a scale
 constexpr int kOperand = kBlock * kBlock;       // bytes of 128 matrix rows x 128 channels
 constexpr int kThreads = 512;                   // warpgroup 0: boxes and products; 1: rows; 2, 3: accumulation
-constexpr int kIssueRegs = 64, kCopyRegs = 96, kAccRegs = 176;   // 64 + 96 + 2 * 176 = 4 * 128, the launch's registers
+constexpr int kIssueRegs = 40, kCopyRegs = 120, kAccRegs = 176;   // 40 + 120 + 2 * 176 = 4 * 128, the launch's registers
 constexpr int kRows = kMoeFewTokens;            // rows of a tile: an expert has at most one for each token
 constexpr int kCopyThreads = 128;
 constexpr int kAcc = 4;                         // accumulators
@@ -323,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
-    const int units = ch.n * tiles;
+    // this CTA's units: a run of them, so that in the second launch it has few column tiles to give word of
+    const int64_t units = (int64_t)ch.n * tiles;
+    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
     const Patience patience{&s.gave_up, a.wait_clocks};
 
     if (warp < 4) {
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 int st = 0, ph = 1, it = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                for (int u = u0; u < u1 && ok; ++u) {
                     const MoeUnit v = moe_unit<UP>(ch, tiles, u);
                     for (int kb = 0; kb < kb_n; ++kb, ++it) {
                         ok = mbar_wait(&s.done[st], ph, patience);
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dw = smem_desc(s.w[0]), dr = smem_desc(s.rows[0]);
             int st = 0, ph = 0, acc = 0, aph = 1, it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            for (int u = u0; u < u1 && ok; ++u) {
                 const MoeUnit v = moe_unit<UP>(ch, tiles, u);
                 const uint32_t idesc = mma_idesc(kBlock, (v.rows + 15) & ~15);
                 for (int kb = 0; kb < kb_n; ++kb, ++it) {
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 int st = 0, ph = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                for (int u = u0; u < u1 && ok; ++u) {
                     for (int kb = 0; kb < kb_n; ++kb) {
                         ok = mbar_wait(&s.rows_full[st], ph, patience) && mbar_wait(&s.boxes[st], ph, patience);
                         if (!ok) break;
@@ -408,67 +412,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_blocks = NB * tiles;                          // of the matrix's rows
         int st = 0, ph = 1, ring = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = u0; u < u1 && ok; ++u) {
             const MoeUnit v = moe_unit<UP>(ch, tiles, u);
-            // the rows' numbers: tokens, or entries
-            int row[kMine];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int r = i * kPass + part;
-                row[i] = r < v.rows ? v.entry[r] : 0;
-                if (UP) row[i] /= k;
-            }
-            const int scale_row = !UP && warp < 6 && place < v.rows ? v.entry[place] : -1;
             uint32_t ws = (uint32_t)(v.e * n_blocks + v.tile) * kb_n;
             if (lane == 1) ws += (uint32_t)tiles * kb_n;          // (the up block's)
-            for (int kb = 0; kb < kb_n; ++kb) {
-                const uint32_t swizzled = part * kBlock + ((piece ^ (part & 7)) << 4);
-                if (UP) {
-                    uint4 in[kMine][2];
+            const uint32_t swizzled = part * kBlock + ((piece ^ (part & 7)) << 4);
+            if (UP) {
+                // few rows: their loads run further ahead (the tokens come from L2, and a step has to take less than
+                // the copy of its matrix rows, some 1400 cycles)
+                const auto rows = [&](auto passes) {
+                    constexpr int P = decltype(passes)::value, D = P > 1 ? 1 : 4;   // passes of 16 rows; steps ahead
+                    uint32_t src[P];                              // in 16 bytes
 #pragma unroll
-                    for (int i = 0; i < kMine; ++i)
-                        if (i * kPass < v.rows) {
-                            const uint4 *p =
-                                reinterpret_cast<const uint4 *>(a.x + (int64_t)row[i] * a.H + kb * kBlock + piece * 16);
-                            in[i][0] = __ldg(p);
-                            in[i][1] = __ldg(p + 1);
+                    for (int i = 0; i < P; ++i) {
+                        const int r = i * kPass + part;
+                        src[i] = (uint32_t)(r < v.rows ? v.entry[r] / k : 0) * (uint32_t)(a.H / 8) + piece * 2;
+                    }
+                    const float *scale = a.gate_up_scales + ws;
+                    const bool has_scale = warp == 7 && lane < NB;
+                    uint4 in[D][P][2];
+                    float sw[D];
+                    const auto load = [&](int d, int kb) {
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            const uint4 *from = reinterpret_cast<const uint4 *>(a.x) + (src[i] + kb * (kBlock / 8));
+                            in[d][i][0] = __ldg(from);
+                            in[d][i][1] = __ldg(from + 1);
                         }
-                    const float sw = warp == 7 && lane < NB ? __ldg(a.gate_up_scales + (ws + kb)) : 0.f;
-                    ok = warp_wait(&s.done[st], ph, patience);
-                    if (!ok) break;
+                        sw[d] = has_scale ? __ldg(scale + kb) : 0.f;
+                    };
 #pragma unroll
-                    for (int i = 0; i < kMine; ++i)
-                        if (i * kPass < v.rows) {
-                            // the cast of ep_dispatch
-                            float f[16];
-                            const uint32_t w8[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
-                                                    in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
-                            float amax = 0.f;
+                    for (int d = 0; d < D; ++d)
+                        if (d < kb_n) load(d, d);
+                    for (int kb0 = 0; kb0 < kb_n; kb0 += D)
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                f[2 * c] = bf16_lo(w8[c]);
-                                f[2 * c + 1] = bf16_hi(w8[c]);
-                                amax = fmaxf(amax, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
+                        for (int d = 0; d < D; ++d) {
+                            const int kb = kb0 + d;
+                            if (kb >= kb_n) break;
+                            if (!warp_wait(&s.done[st], ph, patience)) return false;
+#pragma unroll
+                            for (int i = 0; i < P; ++i) {
+                                // the cast of ep_dispatch
+                                const uint4 x = in[d][i][0], y = in[d][i][1];
+                                const uint32_t w8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                                float f[16], amax = 0.f;
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    f[2 * c] = bf16_lo(w8[c]);
+                                    f[2 * c + 1] = bf16_hi(w8[c]);
+                                    amax = fmaxf(amax, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
+                                }
+#pragma unroll
+                                for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                                const float inv = amax > 0.f ? fminf(__fdiv_rn(448.f, amax), kMaxFinite) : 0.f;
+                                uint32_t q[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    q[c] = (uint32_t)pack_e4m3x2(__fmul_rn(f[4 * c], inv), __fmul_rn(f[4 * c + 1], inv)) |
+                                           (uint32_t)pack_e4m3x2(__fmul_rn(f[4 * c + 2], inv), __fmul_rn(f[4 * c + 3], inv))
+                                               << 16;
+                                if (i * kPass + part < v.rows) {
+                                    *reinterpret_cast<uint4 *>(s.rows[st] + i * kPass * kBlock + swizzled) =
+                                        make_uint4(q[0], q[1], q[2], q[3]);
+                                    if (piece == 0) s.row_scale[ring][i * kPass + part] = __fdiv_rn(amax, 448.f);
+                                }
+                                asm volatile("" ::: "memory");    // (one row after the other: registers)
                             }
-#pragma unroll
-                            for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-                            const float inv = amax > 0.f ? fminf(__fdiv_rn(448.f, amax), kMaxFinite) : 0.f;
-                            uint32_t q[4];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                q[c] = (uint32_t)pack_e4m3x2(__fmul_rn(f[4 * c], inv), __fmul_rn(f[4 * c + 1], inv)) |
-                                       (uint32_t)pack_e4m3x2(__fmul_rn(f[4 * c + 2], inv), __fmul_rn(f[4 * c + 3], inv)) << 16;
-                            if (i * kPass + part < v.rows) {
-                                *reinterpret_cast<uint4 *>(s.rows[st] + i * kPass * kBlock + swizzled) =
-                                    make_uint4(q[0], q[1], q[2], q[3]);
-                                if (piece == 0) s.row_scale[ring][i * kPass + part] = __fdiv_rn(amax, 448.f);
-                            }
+                            if (has_scale) s.w_scale[ring][lane] = sw[d];
+                            fence_async_shared();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s.rows_full[st]);
+                            if (kb + D < kb_n) load(d, kb + D);
+                            if (++st == S) { st = 0; ph ^= 1; }
+                            ring = (ring + 1) % kScaleRing;
                         }
-                    if (warp == 7 && lane < NB) s.w_scale[ring][lane] = sw;
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.rows_full[st]);
-                } else {
+                    return true;
+                };
+                if (v.rows <= 16) ok = rows(std::integral_constant<int, 1>());
+                else ok = rows(std::integral_constant<int, 4>());
+            } else {
+                int row[kMine];                                   // entries
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int r = i * kPass + part;
+                    row[i] = r < v.rows ? v.entry[r] : 0;
+                }
+                const int scale_row = warp < 6 && place < v.rows ? v.entry[place] : -1;
+                for (int kb = 0; kb < kb_n; ++kb) {
                     ok = warp_wait(&s.done[st], ph, patience);
                     if (!ok) break;
                     const uint32_t dst = smem_addr(s.rows[st]) + swizzled;
@@ -480,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cp_async4(smem_addr(&s.row_scale[ring][place]), a.h_scales + (int64_t)scale_row * kb_n + kb);
                     if (warp == 7 && lane == 0) cp_async4(smem_addr(&s.w_scale[ring][0]), a.down_scales + (ws + kb));
                     cp_async_arrive(&s.rows_full[st]);
+                    if (++st == S) { st = 0; ph ^= 1; }
+                    ring = (ring + 1) % kScaleRing;
                 }
-                if (++st == S) { st = 0; ph ^= 1; }
-                ring = (ring + 1) % kScaleRing;
             }
         }
         if (!UP) cp_async_wait_all();
@@ -495,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int chan = quarter * 32 + lane;
         const auto column = [&](int c) { return ((c >> 4) * 2 + half) * 16 + (c & 15); };   // my c-th column
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536;
-        int st = 0, ph = 0, p = 0, ring = 0, unit = 0;
+        int st = 0, ph = 0, p = 0, ring = 0, unit = 0, word = 0, mine = 0;   // (mine: units of this column tile)
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
+        for (int u = u0; u < u1 && ok; ++u, ++unit) {
             const MoeUnit v = moe_unit<UP>(ch, tiles, u);
             uint64_t acc[NB][kMine / 2];
 #pragma unroll
@@ -585,23 +615,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (column(c) >= v.rows) break;
                     y[(int64_t)v.entry[column(c)] * n_cols] = c & 1 ? hi2(acc[0][c / 2]) : lo2(acc[0][c / 2]);
                 }
-                // The tile's last expert?  Everybody's y is out before the count, and in before it is read.
+                // The last of my units of this tile: count them.  Everybody's y is out before, and in before it is read.
+                ++mine;
+                if (u + 1 < u1 && (u + 1) / ch.n == v.tile) continue;
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.joined[0]);
                 if (warp == 8) {
-                    ok = warp_wait(&s.joined[0], unit & 1, patience);
+                    ok = warp_wait(&s.joined[0], word & 1, patience);
                     if (!ok) break;
                     if (lane == 0) {
-                        s.last[unit & 1] = atomicAdd(a.arrived + v.tile, 1u) == (unsigned)ch.n - 1;
+                        s.last[word & 1] = atomicAdd(a.arrived + v.tile, (unsigned)mine) + mine == (unsigned)ch.n;
                         __threadfence();
                         mbar_arrive(&s.joined[1]);
                     }
                     __syncwarp();
                 }
-                ok = warp_wait(&s.joined[1], unit & 1, patience);
+                ok = warp_wait(&s.joined[1], word & 1, patience);
                 if (!ok) break;
-                if (s.last[unit & 1]) combine_tile(a, ch, v.tile);
+                if (s.last[word & 1]) combine_tile(a, ch, v.tile);
+                ++word;
+                mine = 0;
             }
         }
         if (!UP && ch.n == 0)                              // no token has an expert
