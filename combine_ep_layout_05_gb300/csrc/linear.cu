@@ -3,8 +3,10 @@
 //
 //   out[r, c] = act(sum_l A(r, l) B(c, l) + bias[c]) + residual[r, c]
 //
-// bf16 operands, fp32 sums in tensor memory over the whole contraction, one
-// rounding at the end.  Three forms of the same loop, which differ in the way
+// bf16 operands, fp32 sums, one rounding at the end.  The tensor core cuts its
+// sums off rather than rounding them: after a contraction of 7168 they are 8e-6 off.  Beside
+// the rounding to bf16 that is nothing, and such sums stay in tensor memory; fp32
+// results are taken out every 512 of the contraction and added in registers (LONG).  Three forms of the same loop, which differ in the way
 // the operands lie in memory:
 //   forward  A = x [M, K], B = w [N, K]: both along the contraction
 //   grad_x   A = G [M, N], B = w [N, K]: B along its rows (columns of w)
@@ -33,6 +35,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kStages = 6;                      // 192 KB of operands
 constexpr int kTile = 2 * kPart;                // rows and columns of a pair's tile
+constexpr int kSegment = 8;                     // steps of a LONG sum that stay in tensor memory
+constexpr int kIssueRegs = 88, kEndRegs = 208;  // LONG: 88 + 2 * 208 = 3 * 168, the launch's registers
 constexpr int kGroup = 8;                       // row tiles that are walked together, for L2
 
 struct LinearShared {
@@ -66,7 +70,8 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearArgs &a, int u) {
     return v;
 }
 
-template <bool SWIGLU, bool A_MN, bool B_MN>
+// LONG: fp32 results.  Their sums are taken out of tensor memory every kSegment steps and added in registers.
+template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ LinearMaps maps) {
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
@@ -97,6 +102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s.tmem;
     const Patience patience{&s.gave_up, a.wait_clocks};
 
+    if (LONG && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
         // ---- boxes ----
         if (lane == 0) {
@@ -145,67 +151,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int u = blockIdx.x >> 1; u < units && ok; u += pairs) {
                 const LinearUnit v = linear_unit(a, u);
-                ok = warp_wait<true>(&s.tempty[acc], aph, patience);
-                if (!ok) break;
-                tmem_fence_after();
-                for (int k = v.first; k < v.last; ++k) {
-                    ok = warp_wait<true>(&s.full[st], ph, patience);
+                for (int k0 = v.first; k0 < v.last && ok;) {
+                    const int k1 = LONG ? min(k0 + kSegment, v.last) : v.last;
+                    ok = warp_wait<true>(&s.tempty[acc], aph, patience);
                     if (!ok) break;
-                    acquire_shared_of_cluster();
                     tmem_fence_after();
-                    if (issue) {
-                        const uint32_t at = (uint32_t)(st * (2 * kPartBytes >> 4));
+                    for (int k = k0; k < k1; ++k) {
+                        ok = warp_wait<true>(&s.full[st], ph, patience);
+                        if (!ok) break;
+                        acquire_shared_of_cluster();
+                        tmem_fence_after();
+                        if (issue) {
+                            const uint32_t at = (uint32_t)(st * (2 * kPartBytes >> 4));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_bf16<2>(tmem + acc * kTile, da0 + at + i * ka, db0 + at + i * kb, idesc,
-                                        k > v.first || i > 0);
-                        mma_commit<2>(&s.empty[st]);
+                            for (int i = 0; i < 4; ++i)
+                                mma_bf16<2>(tmem + acc * kTile, da0 + at + i * ka, db0 + at + i * kb, idesc,
+                                            k > k0 || i > 0);
+                            mma_commit<2>(&s.empty[st]);
+                        }
+                        if (++st == S) { st = 0; ph ^= 1; }
                     }
-                    if (++st == S) { st = 0; ph ^= 1; }
+                    if (!ok) break;
+                    if (issue) mma_commit<2>(&s.tfull[acc]);
+                    acc ^= 1;
+                    aph ^= acc == 0;
+                    k0 = k1;
                 }
-                if (!ok) break;
-                if (issue) mma_commit<2>(&s.tfull[acc]);
-                acc ^= 1;
-                aph ^= acc == 0;
             }
         }
         __syncwarp();
     } else if (warp >= 4) {
+        if (LONG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEndRegs));
         // ---- epilogue ----
         const int half = (warp - 4) >> 2, quarter = warp & 3;
-        const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536;
+        constexpr int kCols = SWIGLU ? kPart / 2 : kPart;          // output columns of a thread
+        constexpr int kChunks = kCols / 32, kWide = SWIGLU ? 64 : 32;
+        const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536 + half * kCols;
         const uint32_t tempty = cluster_addr(&s.tempty[0], 0);
         int acc = 0, ph = 0;
+        // 32 columns of an accumulator (SwiGLU: of the gate, then of the up rows)
+        const auto load = [&](int q, uint32_t (&t)[kWide]) {
+            const uint32_t at = tm + acc * kTile + q * 32;
+            tmem_ld16(at, t);
+            tmem_ld16(at + 16, t + 16);
+            if (SWIGLU) {
+                tmem_ld16(at + kPart, t + kWide - 32);
+                tmem_ld16(at + kPart + 16, t + kWide - 16);
+            }
+            tmem_wait_ld<kWide>(t);
+        };
+        const auto taken_out = [&]() {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed_cluster(tempty + acc * 8);
+        };
         bool ok = true;
         for (int u = blockIdx.x >> 1; u < units && ok; u += pairs) {
             const LinearUnit v = linear_unit(a, u);
-            ok = warp_wait(&s.tfull[acc], ph, patience);
-            if (!ok) break;
-            tmem_fence_after();
             const int64_t r = (int64_t)v.row * kTile + rank * kPart + quarter * 32 + lane;
-            const bool live = r < a.R;
-            constexpr int kCols = SWIGLU ? kPart / 2 : kPart;      // output columns of a thread
             const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
-#pragma unroll 1
-            for (int q = 0; q < kCols / 32; ++q) {
-                __syncwarp();                  // (lanes whose rows do not exist come back early)
-                uint32_t t[SWIGLU ? 64 : 32];
-                const uint32_t at = tm + acc * kTile + half * kCols + q * 32;
-                tmem_ld16(at, t);
-                tmem_ld16(at + 16, t + 16);
-                if (SWIGLU) {
-                    tmem_ld16(at + kPart, t + 32);
-                    tmem_ld16(at + kPart + 16, t + 48);
-                }
-                tmem_wait_ld<(SWIGLU ? 64 : 32)>(t);
-                if (q == kCols / 32 - 1) {
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_relaxed_cluster(tempty + acc * 8);
-                }
+            const auto finish = [&](int q, const uint32_t *t) {
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
-                if (!live || n <= 0) continue;
+                if (r >= a.R || n <= 0) return;
                 float z[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(t[i]);
@@ -214,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (SWIGLU) {
                     float up[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(t[(SWIGLU ? 32 : 0) + i]);
+                    for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(t[kWide - 32 + i]);
                     if (a.bias) add_vector(a.bias + a.C + c, up, n);
                     if (a.pre) store_bf16(a.pre + r * a.pre_stride + a.C + c, up, n, a.pre_align);
 #pragma unroll
@@ -224,14 +232,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) z[i] = activate(z[i], a.act);
                 }
                 if (a.residual) add_bf16(a.residual + r * a.residual_stride + c, z, n, a.residual_align);
-                if (a.out32)
+                if (LONG)
                     store_fp32(reinterpret_cast<float *>(a.out) + v.split * a.split_stride + r * a.out_stride + c, z, n,
                                a.out_align);
                 else
                     store_bf16(reinterpret_cast<uint16_t *>(a.out) + r * a.out_stride + c, z, n, a.out_align);
+            };
+            if (LONG) {
+                float sum[kChunks][kWide];
+#pragma unroll
+                for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+                    for (int i = 0; i < kWide; ++i) sum[q][i] = 0.f;
+                for (int k = v.first; k < v.last; k += kSegment) {
+                    ok = warp_wait(&s.tfull[acc], ph, patience);
+                    if (!ok) break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (int q = 0; q < kChunks; ++q) {
+                        uint32_t t[kWide];
+                        load(q, t);
+#pragma unroll
+                        for (int i = 0; i < kWide; ++i) sum[q][i] += __uint_as_float(t[i]);
+                    }
+                    taken_out();
+                    acc ^= 1;
+                    ph ^= acc == 0;
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < kChunks; ++q) finish(q, reinterpret_cast<const uint32_t *>(sum[q]));
+            } else {
+                ok = warp_wait(&s.tfull[acc], ph, patience);
+                if (!ok) break;
+                tmem_fence_after();
+#pragma unroll 1
+                for (int q = 0; q < kChunks; ++q) {
+                    __syncwarp();              // (lanes whose rows do not exist come back early)
+                    uint32_t t[kWide];
+                    load(q, t);
+                    if (q == kChunks - 1) taken_out();
+                    finish(q, t);
+                }
+                acc ^= 1;
+                ph ^= acc == 0;
             }
-            acc ^= 1;
-            ph ^= acc == 0;
+            __syncwarp();
         }
     }
     tmem_fence_before();
@@ -252,20 +298,24 @@ cudaError_t operand_map(const LinearOperand &o, bool mn, CUtensorMap *map) {
     return encode_map(map, 2, o.p, dims, strides, box);
 }
 
-template <bool SWIGLU, bool A_MN, bool B_MN>
+template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG>
 cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st) {
     constexpr int bytes = sizeof(LinearShared);
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
     cached_per_device(ready, [&](int) {
-        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        // the warpgroups' register shares are drawn from what the block was launched with
+        cudaFuncAttributes f{};
+        if (!e) e = cudaFuncGetAttributes(&f, linear_kernel<SWIGLU, A_MN, B_MN, LONG>);
+        if (!e && LONG && f.numRegs * 3 < kIssueRegs + 2 * kEndRegs) e = cudaErrorInvalidDeviceFunction;
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
     const int64_t units = (int64_t)a.row_tiles * a.col_tiles * a.splits;
     const int grid = (int)std::min<int64_t>(num_sms() & ~1, 2 * units);
-    linear_kernel<SWIGLU, A_MN, B_MN><<<grid, kThreads, bytes, st>>>(a, maps);
+    linear_kernel<SWIGLU, A_MN, B_MN, LONG><<<grid, kThreads, bytes, st>>>(a, maps);
     return cudaGetLastError();
 }
 
@@ -287,19 +337,32 @@ int linear_splits(int64_t R, int64_t C, int64_t L) {
     return best;
 }
 
+// What a launch of this kernel takes, in us, fitted to measurements from a graph: 28 tiles of 4, 16, 32 and 112 steps
+// 7.1, 11.1, 15.4 and 36.8 us; 84 tiles of 32 steps 25.0.
+double linear_time(int64_t rows, int64_t col_tiles, int64_t steps) {
+    const int64_t turns = ((rows + kTile - 1) / kTile * col_tiles + 75) / 76;
+    return 5.8 + turns * (0.27 * steps + 1.0);
+}
+
 cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st) {
     const bool swiglu = form == kFormForward && a.act == EP_ACT_SWIGLU;
-    LinearMaps maps;
-    if (cudaError_t e = operand_map(A, form == kFormGradW, &maps.a)) return e;
-    if (cudaError_t e = operand_map(B, form != kFormForward, &maps.b)) return e;
     const int cols = swiglu ? kPart : kTile;
     a.row_tiles = (int)((a.R + kTile - 1) / kTile);
     a.col_tiles = (int)((a.C + cols - 1) / cols);
     a.steps = (int)((a.L + kStep - 1) / kStep);
     a.split_steps = (a.steps + a.splits - 1) / a.splits;
-    if (form == kFormGradX) return launch<false, false, true>(a, maps, st);
-    if (form == kFormGradW) return launch<false, true, true>(a, maps, st);
-    return swiglu ? launch<true, false, false>(a, maps, st) : launch<false, false, false>(a, maps, st);
+    if (form == kFormForward && linear_few_time(a) < linear_time(a.R, a.col_tiles, a.steps))
+        return launch_linear_few(a, A, B, st);
+    LinearMaps maps;
+    if (cudaError_t e = operand_map(A, form == kFormGradW, &maps.a)) return e;
+    if (cudaError_t e = operand_map(B, form != kFormForward, &maps.b)) return e;
+    if (form == kFormGradX)
+        return a.out32 ? launch<false, false, true, true>(a, maps, st) : launch<false, false, true, false>(a, maps, st);
+    if (form == kFormGradW)
+        return a.out32 ? launch<false, true, true, true>(a, maps, st) : launch<false, true, true, false>(a, maps, st);
+    if (swiglu)
+        return a.out32 ? launch<true, false, false, true>(a, maps, st) : launch<true, false, false, false>(a, maps, st);
+    return a.out32 ? launch<false, false, false, true>(a, maps, st) : launch<false, false, false, false>(a, maps, st);
 }
 
 }  // namespace ep

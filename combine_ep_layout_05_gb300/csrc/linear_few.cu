@@ -1,0 +1,364 @@
+// Dense products with an epilogue for few rows: the matrix is read once, and
+// that is what takes the time.
+//
+// Same operation as the forward form of linear.cu with the operands' parts
+// exchanged: 128 rows of the matrix are the tensor core's M (SwiGLU: 64 gate and 64
+// up rows), the rows of x its N (16, 32, .. as many as there are, in one box).
+// A tile of 128 matrix rows alone would leave most SMs idle (a gate of 256 experts has
+// two), so the CTAs of a cluster share a tile's contraction: each sums its part in
+// tensor memory, puts it into its shared memory, and then finishes a share of
+// the tile's outputs, whose parts it reads from the shared memory of every CTA of the
+// cluster, in the order of their ranks.  No workspace, no atomics, one order of the sums.
+// Two CTAs to an SM, so that one streams while the other starts or ends.
+//
+// The tensor core cuts its sums off rather than rounding them: over a contraction of
+// 7168 in one accumulator the result is 8e-6 off.  Every kChain steps go to an
+// accumulator of their own (as far as there are), and these are added in fp32.
+#include <algorithm>
+#include <cstddef>
+
+#include "linear_device.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 256;                   // warp 0: boxes, 1: products; all: the end
+constexpr int kMaxStages = 6;
+constexpr int kRing = 112 * 1024;               // bytes of operands: two CTAs an SM
+constexpr int kColumns = 256;                   // of tensor memory, likewise
+constexpr int kChain = 8;                       // steps in one accumulator, if accumulators suffice
+
+struct FewBarriers {
+    uint64_t full[kMaxStages], empty[kMaxStages], summed;
+    uint32_t tmem;
+    int gave_up;
+};
+
+struct FewMaps {
+    CUtensorMap x, w;
+};
+
+// How a launch is cut
+struct FewPlan {
+    int col_tiles, tile_rows;    // rows of x in a tile
+    int rows;                // the same up to a multiple of 16, in a box
+    int stage, stages;       // bytes of a step's operands, buffers
+    int steps, split_steps;  // of the contraction, and at most of a CTA
+    int chain, accs;         // steps of an accumulator, accumulators
+};
+
+// 4 numbers of the shared memory of a CTA of the cluster
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+// v += N CTAs' numbers at `at`, from rank q on, loads first
+template <int N>
+__device__ __forceinline__ void add_parts(float (&v)[4], const float *at, uint32_t q) {
+    float4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = load_cluster(cluster_addr(at, q + i));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[0] += x[i].x;
+        v[1] += x[i].y;
+        v[2] += x[i].z;
+        v[3] += x[i].w;
+    }
+}
+// the same of all CTAs (a power of two of them)
+__device__ __forceinline__ void add_all(float (&v)[4], const float *at, uint32_t size) {
+    if (size >= 8)
+        for (uint32_t q = 0; q < size; q += 8) add_parts<8>(v, at, q);
+    else if (size == 4) add_parts<4>(v, at, 0);
+    else if (size == 2) add_parts<2>(v, at, 0);
+    else add_parts<1>(v, at, 0);
+}
+// 4 consecutive bf16 of a row, of which n exist; vec: 8-byte accesses are aligned
+__device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4], int n, bool vec) {
+    const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+    if (vec && n >= 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    } else {
+        p[0] = (uint16_t)lo;
+        if (n > 1) p[1] = (uint16_t)(lo >> 16);
+        if (n > 2) p[2] = (uint16_t)hi;
+        if (n > 3) p[3] = (uint16_t)(hi >> 16);
+    }
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 2)
+    linear_few_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ FewMaps maps, const FewPlan p) {
+    extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
+    FewBarriers &s = *reinterpret_cast<FewBarriers *>(raw + p.stage * p.stages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    // the tile: column tiles of a row tile follow one another
+    const int tile = blockIdx.x / size, col = tile % p.col_tiles;
+    const int64_t row0 = (int64_t)(tile / p.col_tiles) * p.tile_rows;
+    const int rows = (int)min((int64_t)p.tile_rows, a.R - row0);
+    const int first = min((int)rank * p.split_steps, p.steps), last = min(first + p.split_steps, p.steps);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        mbar_init(&s.summed, 1);
+        s.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
+                     "n"(kColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s.tmem;
+    const Patience patience{&s.gave_up, a.wait_clocks};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // the tile's two halves of 64 matrix rows
+            const int w0 = col * (SWIGLU ? kPart / 2 : kPart), w1 = SWIGLU ? (int)a.C + w0 : w0 + kPart / 2;
+            int st = 0, ph = 1, it = 0;
+            for (int k = first; k < last; ++k, ++it) {
+                if (!mbar_wait(&s.empty[st], ph, patience)) break;
+                mbar_expect_tx(&s.full[st], p.stage);
+                unsigned char *buf = raw + st * p.stage;
+                tma_load_2d(buf, &maps.w, k * kStep * 2, w0, &s.full[st]);
+                tma_load_2d(buf + kPartBytes / 2, &maps.w, k * kStep * 2, w1, &s.full[st]);
+                tma_load_2d(buf + kPartBytes, &maps.x, k * kStep * 2, (int)row0, &s.full[st]);
+                if (++st == p.stages) { st = 0; ph ^= 1; }
+            }
+            // what has been issued lands, whether its products were or not (together within a second)
+            const long long t0 = clock64();
+            for (int i = max(0, it - p.stages); i < it; ++i)
+                while (!mbar_try_wait(&s.full[i % p.stages], i / p.stages & 1))
+                    if (clock64() - t0 > (1ll << 31)) break;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool issue = elect_one();
+        const uint32_t idesc = mma_idesc_bf16(kPart, p.rows, false, false);
+        const uint64_t desc = smem_desc(raw);
+        int st = 0, ph = 0;
+        bool ok = true;
+        for (int k = first; k < last; ++k) {
+            ok = warp_wait(&s.full[st], ph, patience);
+            if (!ok) break;
+            tmem_fence_after();
+            if (issue) {
+                const uint64_t da = desc + (uint32_t)(st * p.stage >> 4), db = da + (kPartBytes >> 4);
+                const int at = k - first, acc = at / p.chain;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_bf16<1>(tmem + acc * p.rows, da + i * 2, db + i * 2, idesc, at % p.chain > 0 || i > 0);
+                mma_commit<1>(&s.empty[st]);
+            }
+            if (++st == p.stages) { st = 0; ph ^= 1; }
+        }
+        if (issue) mma_commit<1>(&s.summed);      // (of all that were issued, given up or not)
+        __syncwarp();
+    }
+    // ---- this CTA's part of the sums -> shared memory, [row of x][matrix row]; the operands are done with ----
+    __syncwarp();
+    float *part = reinterpret_cast<float *>(raw);
+    if (!warp_wait(&s.summed, 0, patience)) {
+        const long long t0 = clock64();            // (issued products end by themselves)
+        while (!mbar_try_wait(&s.summed, 0))
+            if (clock64() - t0 > (1ll << 31)) break;
+        __syncwarp();
+    }
+    tmem_fence_after();
+    __syncthreads();                               // (the boxes have landed, too)
+    {
+        const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+        const int accs = (last - first + p.chain - 1) / p.chain;
+        for (int c = half * 16; c < p.rows; c += 32) {
+            float v[16] = {};
+            for (int i = 0; i < accs; ++i) {
+                uint32_t t[16];
+                tmem_ld16(tmem + (uint32_t)(quarter * 32) * 65536 + i * p.rows + c, t);
+                tmem_wait_ld<16>(t);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(t[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < rows) part[(c + j) * kPart + mine] = v[j];
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    // ---- a share of the outputs, 4 columns a turn ----
+    {
+        constexpr int W = (SWIGLU ? kPart / 2 : kPart) / 4;
+        const int items = rows * W, share = (items + (int)size - 1) / (int)size;
+        const int end = min(items, (int)(rank + 1) * share);
+        for (int i = (int)rank * share + threadIdx.x; i < end; i += kThreads) {
+            const int r = i / W, at = i % W * 4;
+            const int64_t m = row0 + r, c = (int64_t)col * (W * 4) + at;
+            const int n = (int)min(a.C - c, (int64_t)4);
+            if (n <= 0) continue;
+            float z[4] = {}, up[4] = {};
+            add_all(z, &part[r * kPart + at], size);
+            if (SWIGLU) add_all(up, &part[r * kPart + W * 4 + at], size);
+            if (a.bias) add_vector(a.bias + c, z, n);
+            if (SWIGLU && a.bias) add_vector(a.bias + a.C + c, up, n);
+            if (a.pre) {
+                uint16_t *pre = a.pre + m * a.pre_stride + c;
+                store4(pre, z, n, a.pre_align >= 16);
+                if (SWIGLU) store4(pre + a.C, up, n, a.pre_align >= 16);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = SWIGLU ? swiglu(z[j], up[j]) : activate(z[j], a.act);
+            if (a.residual) {
+                const uint16_t *res = a.residual + m * a.residual_stride + c;
+                if (n >= 4 && a.residual_align >= 16) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(res);
+                    z[0] += bf16_lo(v.x);
+                    z[1] += bf16_hi(v.x);
+                    z[2] += bf16_lo(v.y);
+                    z[3] += bf16_hi(v.y);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < n) z[j] += __uint_as_float((uint32_t)res[j] << 16);
+                }
+            }
+            if (a.out32) {
+                float *out = reinterpret_cast<float *>(a.out) + m * a.out_stride + c;
+                if (n >= 4 && a.out_align >= 16) {
+                    *reinterpret_cast<float4 *>(out) = make_float4(z[0], z[1], z[2], z[3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < n) out[j] = z[j];
+                }
+            } else {
+                store4(reinterpret_cast<uint16_t *>(a.out) + m * a.out_stride + c, z, n, a.out_align >= 16);
+            }
+        }
+    }
+    cluster_sync();                                // nobody reads this CTA's part any more
+    if (warp == 1) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kColumns));
+    }
+    if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+}
+
+template <bool SWIGLU>
+cudaError_t launch(const LinearArgs &a, const FewMaps &maps, const FewPlan &p, int tiles, int size, cudaStream_t st) {
+    static std::atomic<int> ready[kCacheDevices];
+    cudaError_t e = cudaSuccess;
+    cached_per_device(ready, [&](int) {
+        e = cudaFuncSetAttribute(linear_few_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kRing + (int)sizeof(FewBarriers));
+        if (!e) e = cudaFuncSetAttribute(linear_few_kernel<SWIGLU>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e == cudaSuccess ? 1 : 0;
+    });
+    if (e) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(tiles * size));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = p.stage * p.stages + sizeof(FewBarriers);
+    c.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, linear_few_kernel<SWIGLU>, a, maps, p);
+}
+
+}  // namespace
+
+namespace {
+
+// How few rows are cut, and by how many CTAs to a tile.
+//
+// The CTAs of a cluster take, in us (measured from a graph, fitted to 16 to 128 rows of a tile, 2 to 112 steps and 1 to
+// 16 CTAs to a tile): each step 0.2 and 0.0016 a row, 0.42 where two CTAs share an SM; the exchange of the parts 0.0022 a row
+// and CTA of the cluster; all CTAs 0.008 each to start, 5 in all.  Clusters of 16 find their places slowly: 128 of their
+// CTAs took 13.2 us for what 64 CTAs of clusters of 8 did in 11.9, 64 of them 10.4 against 11.7.
+FewPlan few_plan(const LinearArgs &a, int &size, int64_t &tiles, double &time) {
+    const bool swiglu = a.act == EP_ACT_SWIGLU;
+    FewPlan best;
+    FewPlan p;
+    // (fp32 results: half the rows, for twice the accumulators)
+    const int most = a.out32 ? kPart / 2 : kPart, outs = swiglu ? kPart / 2 : kPart;
+    const int64_t row_tiles = (a.R + most - 1) / most;
+    p.tile_rows = (int)((a.R + row_tiles - 1) / row_tiles);
+    p.rows = (p.tile_rows + 15) / 16 * 16;
+    p.stage = kPartBytes + p.rows * kStep * 2;
+    p.stages = std::min(kMaxStages, kRing / p.stage);
+    p.steps = (int)((a.L + kStep - 1) / kStep);
+    p.col_tiles = (int)((a.C + outs - 1) / outs);
+    tiles = row_tiles * p.col_tiles;
+    time = 1e30;
+    for (int c = 1; c <= 16; c *= 2) {
+        const int64_t ctas = tiles * c;
+        if (c > 1 && (c > p.steps || ctas > (c == 16 ? 64 : 304))) break;
+        p.split_steps = (p.steps + c - 1) / c;
+        p.accs = std::min(kColumns / p.rows, (p.split_steps + kChain - 1) / kChain);
+        p.chain = (p.split_steps + p.accs - 1) / p.accs;
+        const double turns = (double)((ctas + 303) / 304);
+        const double step = ctas > 152 ? 0.42 : 0.2 + 0.0016 * p.rows;
+        const double bytes = 2.0 * a.L * (outs * (swiglu ? 2 : 1)) * p.col_tiles;
+        double t = 5.0 + 0.008 * std::min<int64_t>(ctas, 304) + 0.0022 * c * p.rows +
+                   std::max(turns * step * p.split_steps, bytes / 5.5e6);
+        // a longer chain would cost fp32 results digits
+        if (a.out32 && p.chain > kChain) t += 1e6;
+        if (t < time) {
+            time = t;
+            best = p;
+            size = c;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+double linear_few_time(const LinearArgs &a) {
+    int size;
+    int64_t tiles;
+    double time;
+    few_plan(a, size, tiles, time);
+    return time;
+}
+
+cudaError_t launch_linear_few(const LinearArgs &a, const LinearOperand &x, const LinearOperand &w, cudaStream_t st) {
+    int size;
+    int64_t tiles;
+    double time;
+    const FewPlan p = few_plan(a, size, tiles, time);
+    FewMaps maps;
+    const cuuint64_t xd[2] = {(cuuint64_t)x.cols * 2, (cuuint64_t)x.rows}, xs[1] = {(cuuint64_t)x.stride * 2};
+    const cuuint64_t wd[2] = {(cuuint64_t)w.cols * 2, (cuuint64_t)w.rows}, ws[1] = {(cuuint64_t)w.stride * 2};
+    const cuuint32_t xb[2] = {128, (cuuint32_t)p.rows}, wb[2] = {128, (cuuint32_t)kPart / 2};
+    if (cudaError_t e = encode_map(&maps.x, 2, x.p, xd, xs, xb)) return e;
+    if (cudaError_t e = encode_map(&maps.w, 2, w.p, wd, ws, wb)) return e;
+    return a.act == EP_ACT_SWIGLU ? launch<true>(a, maps, p, (int)tiles, size, st)
+                                  : launch<false>(a, maps, p, (int)tiles, size, st);
+}
+
+}  // namespace ep

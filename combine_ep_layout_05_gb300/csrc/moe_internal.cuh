@@ -112,6 +112,8 @@ struct SumPartsArgs {        // out = sum of parts [rows, cols], cols a multiple
 
 // Parts into which the contraction L of an R x C product is split
 int linear_splits(int64_t R, int64_t C, int64_t L);
+double linear_few_time(const LinearArgs &a);         // us that launch_linear_few takes
+cudaError_t launch_linear_few(const LinearArgs &a, const LinearOperand &x, const LinearOperand &w, cudaStream_t st);
 cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st);
 cudaError_t launch_moe_few(const MoeFewArgs &a, cudaStream_t st);
 cudaError_t launch_act_grad(const ActGradArgs &a, cudaStream_t st);
