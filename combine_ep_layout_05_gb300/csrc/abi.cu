@@ -968,7 +968,7 @@ namespace {
 
 // The parts of ep_moe_few's workspace, each from a multiple of 256 bytes on
 struct MoeFewParts {
-    size_t h, h_scales, y, arrived, total;
+    size_t x, x_scales, h, h_scales, y, arrived, total;
 };
 bool moe_few_parts(const ep::Dims &d, int64_t I, MoeFewParts &b) {
     if (d.T > ep::kMoeFewTokens)
@@ -979,11 +979,13 @@ bool moe_few_parts(const ep::Dims &d, int64_t I, MoeFewParts &b) {
     if (d.H * I >= (int64_t)1 << 39) return fail(EP_ERR_INVALID_ARG, "hidden * intermediate must be below 2^39"), false;
     const auto round = [](size_t n) { return (n + 255) & ~(size_t)255; };
     const size_t rows = (size_t)d.T * d.k;
+    b.x = round((size_t)d.T * d.H);
+    b.x_scales = round((size_t)d.T * (d.H / 128) * 4);
     b.h = round(rows * I);
     b.h_scales = round(rows * (I / 128) * 4);
     b.y = round(rows * d.H * 4);
     b.arrived = round(d.H / 128 * 4);
-    b.total = b.h + b.h_scales + b.y + b.arrived;
+    b.total = b.x + b.x_scales + b.h + b.h_scales + b.y + b.arrived;
     return true;
 }
 
@@ -1034,10 +1036,12 @@ int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, co
     a.down = down;
     a.gate_up_scales = gate_up_scales;
     a.down_scales = down_scales;
-    a.h = (uint8_t *)ws;
-    a.h_scales = (float *)(ws + b.h);
-    a.y = (float *)(ws + b.h + b.h_scales);
-    a.arrived = (unsigned *)(ws + b.h + b.h_scales + b.y);
+    a.xq = (uint8_t *)ws;
+    a.x_scales = (float *)(ws += b.x);
+    a.h = (uint8_t *)(ws += b.x_scales);
+    a.h_scales = (float *)(ws += b.h);
+    a.y = (float *)(ws += b.h_scales);
+    a.arrived = (unsigned *)(ws + b.y);
     a.out = out;
     a.wait_clocks = ep::kWaitClocks;
     cudaError_t e = ep::launch_moe_few(a, (cudaStream_t)stream);

@@ -296,8 +296,8 @@ namespace {
 // How few rows are cut, and by how many CTAs to a tile.
 //
 // The CTAs of a cluster take, in us (measured from a graph, fitted to 16 to 128 rows of a tile, 2 to 112 steps and 1 to
-// 16 CTAs to a tile): each step 0.2 and 0.0016 a row, 0.42 where two CTAs share an SM; the exchange of the parts 0.0022 a row
-// and CTA of the cluster; all CTAs 0.008 each to start, 5 in all.  Clusters of 16 find their places slowly: 128 of their
+// 16 CTAs to a tile): each step 0.24 and 0.002 a row, little more where two CTAs share an SM, but not less than the memory;
+// the exchange of the parts 0.0015 a row and CTA of the cluster; each CTA 0.006 to start, and 5 in all.  Clusters of 16 find their places slowly: 128 of their
 // CTAs took 13.2 us for what 64 CTAs of clusters of 8 did in 11.9, 64 of them 10.4 against 11.7.
 FewPlan few_plan(const LinearArgs &a, int &size, int64_t &tiles, double &time) {
     const bool swiglu = a.act == EP_ACT_SWIGLU;
@@ -321,10 +321,10 @@ FewPlan few_plan(const LinearArgs &a, int &size, int64_t &tiles, double &time) {
         p.accs = std::min(kColumns / p.rows, (p.split_steps + kChain - 1) / kChain);
         p.chain = (p.split_steps + p.accs - 1) / p.accs;
         const double turns = (double)((ctas + 303) / 304);
-        const double step = ctas > 152 ? 0.42 : 0.2 + 0.0016 * p.rows;
+        const double step = (0.24 + 0.002 * p.rows) * (ctas > 152 ? 1.05 : 1.0);
         const double bytes = 2.0 * a.L * (outs * (swiglu ? 2 : 1)) * p.col_tiles;
-        double t = 5.0 + 0.008 * std::min<int64_t>(ctas, 304) + 0.0022 * c * p.rows +
-                   std::max(turns * step * p.split_steps, bytes / 5.5e6);
+        double t = 5.0 + 0.006 * std::min<int64_t>(ctas, 304) + 0.0015 * c * p.rows +
+                   std::max(turns * step * p.split_steps, bytes / 6.8e6);
         // a longer chain would cost fp32 results digits
         if (a.out32 && p.chain > kChain) t += 1e6;
         if (t < time) {

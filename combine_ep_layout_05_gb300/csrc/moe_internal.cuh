@@ -46,7 +46,9 @@ struct MoeFewArgs {
     const uint16_t *x, *residual;
     const uint8_t *gate_up, *down;
     const float *gate_up_scales, *down_scales;
-    uint8_t *h;              // workspace: [T k, I] codes, [T k, I / 128] scales, [T k, H] products, [H / 128] counters
+    uint8_t *xq;             // workspace: [T, H] codes, [T, H / 128] scales of x
+    float *x_scales;
+    uint8_t *h;              // [T k, I] codes, [T k, I / 128] scales, [T k, H] products, [H / 128] counters
     float *h_scales, *y;
     unsigned *arrived;
     uint16_t *out;
