@@ -968,7 +968,7 @@ namespace {
 
 // The parts of ep_moe_few's workspace, each from a multiple of 256 bytes on
 struct MoeFewParts {
-    size_t x, x_scales, h, h_scales, y, arrived, total;
+    size_t x, x_scales, h, h_scales, y, arrived, parts, total;
 };
 bool moe_few_parts(const ep::Dims &d, int64_t I, MoeFewParts &b) {
     if (d.T > ep::kMoeFewTokens)
@@ -985,7 +985,8 @@ bool moe_few_parts(const ep::Dims &d, int64_t I, MoeFewParts &b) {
     b.h_scales = round(rows * (I / 128) * 4);
     b.y = round(rows * d.H * 4);
     b.arrived = round(d.H / 128 * 4);
-    b.total = b.x + b.x_scales + b.h + b.h_scales + b.y + b.arrived;
+    b.parts = (size_t)ep::kMoeCtas * 2 * ep::moe_part_floats((int)(d.T + 15) / 16 * 16) * 4;
+    b.total = b.x + b.x_scales + b.h + b.h_scales + b.y + b.arrived + b.parts + 2 * ep::kMoeCtas * 4;
     return true;
 }
 
@@ -1041,7 +1042,9 @@ int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, co
     a.h = (uint8_t *)(ws += b.x_scales);
     a.h_scales = (float *)(ws += b.h);
     a.y = (float *)(ws += b.h_scales);
-    a.arrived = (unsigned *)(ws + b.y);
+    a.arrived = (unsigned *)(ws += b.y);
+    a.parts = (float *)(ws += b.arrived);
+    a.split = (unsigned *)(ws + b.parts);
     a.out = out;
     a.wait_clocks = ep::kWaitClocks;
     cudaError_t e = ep::launch_moe_few(a, (cudaStream_t)stream);

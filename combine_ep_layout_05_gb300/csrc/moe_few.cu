@@ -56,8 +56,9 @@ struct MoeBarriers {
     uint64_t tempty[kAcc];                                  // accumulators taken out
     uint64_t joined[2];                                     // UP: a warpgroup's maxima are written; else: y is, and who
                                                             // is last is known
+    uint64_t split[2];                                      // a part is written, and who is last is known
     float w_scale[kScaleRing][2];
-    int last[2];
+    int last[2], last_part[2];
     uint32_t tmem;
     int n, gave_up;                                         // chosen experts
 };
@@ -156,16 +157,51 @@ __device__ __forceinline__ void list_chosen(const MoeShared<UP> &s, int E, int T
     __syncthreads();
 }
 
-// A unit of work
-struct MoeUnit {
-    int e, tile, rows;
+// A part of a unit of work: blocks [kb0, kb1) of the contraction of a column tile of an expert
+struct MoePart {
+    int64_t unit;
+    int e, tile, rows, kb0, kb1;
     const short *entry;
 };
+// A CTA's run of steps, all units' steps laid end to end: of whole units, or, where these would leave SMs idle that the
+// memory needs, in equal runs that may begin and end within a unit.  One SM takes 70 GB/s at most (measured: 8 units alone
+// take 0.45 us a step of 32 KB) and some 100 of them all there is; a split unit costs an exchange of some 4 us.  (One
+// token's 128 units of 56 steps: 77 us whole, 89 split; 8 units of 56 steps 47 us split.)
 template <bool UP>
-__device__ __forceinline__ MoeUnit moe_unit(const MoeShared<UP> &c, int tiles, int n, int u) {
-    // first launch: an expert's column tiles follow one another; second: a column tile's experts
-    const int at = UP ? u / tiles : u % n;
-    return MoeUnit{c.expert[at], UP ? u - at * tiles : u / n, c.start[at + 1] - c.start[at], c.entry + c.start[at]};
+struct MoeRun {
+    int64_t total, at, end;
+    int n;                               // CTAs that have steps (split)
+    __device__ __forceinline__ MoeRun(int64_t units, int kb_n) {
+        constexpr int kExchange = UP ? 9 : 18, kLeast = UP ? 4 : 8;     // steps: of 4 us, and of a run
+        const int64_t ctas = gridDim.x, c = blockIdx.x, all = units * kb_n;
+        total = all;
+        n = (int)min(ctas, (all + kLeast - 1) / kLeast);
+        if (max((units + ctas - 1) / ctas * kb_n, all / 100) <= all / 100 + kExchange) {
+            at = units * c / ctas * kb_n;
+            end = units * (c + 1) / ctas * kb_n;
+        } else {
+            at = c < n ? all * c / n : 0;
+            end = c < n ? all * (c + 1) / n : 0;
+        }
+    }
+    // the CTA that has a step of a split unit
+    __device__ __forceinline__ int owner(int64_t step) const { return (int)(((step + 1) * n - 1) / total); }
+};
+// the run's next part; what follows it starts at run.at
+template <bool UP, typename S>
+__device__ __forceinline__ MoePart next_part(const S &s, int tiles, int chosen, int kb_n, MoeRun<UP> &run) {
+    MoePart v;
+    v.unit = run.at / kb_n;
+    v.kb0 = (int)(run.at - v.unit * kb_n);
+    v.kb1 = (int)min((int64_t)kb_n, v.kb0 + (run.end - run.at));
+    run.at += v.kb1 - v.kb0;
+    // second launch: an expert's column tiles follow one another; third: a column tile's experts
+    const int at = (int)(UP ? v.unit / tiles : v.unit % chosen);
+    v.tile = (int)(UP ? v.unit - (int64_t)at * tiles : v.unit / chosen);
+    v.e = s.expert[at];
+    v.rows = s.start[at + 1] - s.start[at];
+    v.entry = s.entry + s.start[at];
+    return v;
 }
 
 // out[t, columns of a tile] by the 256 accumulating threads
@@ -195,9 +231,29 @@ __device__ __forceinline__ void combine_tile(const MoeFewArgs &a, const MoeShare
     }
 }
 
+// one box towards L2
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// a box that is read once
+__device__ __forceinline__ void tma_load_once_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// Steps of the third launch whose matrix rows the second one asks for ahead, so that the memory has work while it ends and
+// the third begins: at most 640 KB a CTA, 97 MB of an L2 of 129.
+constexpr int kAhead = 40;
+
 template <bool UP>
 __global__ void __launch_bounds__(kThreads, 1)
-    moe_few_kernel(const __grid_constant__ MoeFewArgs a, const __grid_constant__ CUtensorMap map_w, const int S) {
+    moe_few_kernel(const __grid_constant__ MoeFewArgs a, const __grid_constant__ CUtensorMap map_w,
+                   const __grid_constant__ CUtensorMap map_next, const int S) {
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
     constexpr int NB = UP ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,6 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kAcc; ++i) mbar_init(&bar.tempty[i], 8);
         mbar_init(&bar.joined[0], UP ? 4 : 8);
         mbar_init(&bar.joined[1], UP ? 4 : 1);
+        mbar_init(&bar.split[0], 8);
+        mbar_init(&bar.split[1], 1);
         bar.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -237,9 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = bar.tmem;
     const int chosen = bar.n;
-    // this CTA's units: a run of them, so that in the second launch it has few column tiles to give word of
-    const int64_t units = (int64_t)chosen * tiles;
-    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    const MoeRun<UP> whole_run((int64_t)chosen * tiles, kb_n);
     const Patience patience{&bar.gave_up, a.wait_clocks};
 
     if (warp < 4) {
@@ -247,19 +303,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             // ---- matrix rows ----
             if (lane == 0) {
+                const uint64_t once = l2_policy<1>();
                 int st = 0, ph = 1, it = 0;
                 bool ok = true;
-                for (int u = u0; u < u1 && ok; ++u) {
-                    const MoeUnit v = moe_unit<UP>(s, tiles, chosen, u);
-                    for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                for (MoeRun<UP> run = whole_run; run.at < run.end && ok;) {
+                    const MoePart v = next_part<UP>(s, tiles, chosen, kb_n, run);
+                    for (int kb = v.kb0; kb < v.kb1; ++kb, ++it) {
                         ok = mbar_wait(&bar.done[st], ph, patience);
                         if (!ok) break;
                         mbar_expect_tx(&bar.boxes[st], NB * kOperand);
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
-                            tma_load_3d(s.w + st * (NB * kOperand) + b * kOperand, &map_w, kb * kBlock, v.tile * kBlock + b * n_cols, v.e,
-                                        &bar.boxes[st]);
+                            tma_load_once_3d(s.w + st * (NB * kOperand) + b * kOperand, &map_w, kb * kBlock,
+                                             v.tile * kBlock + b * n_cols, v.e, &bar.boxes[st], once);
                         if (++st == S) { st = 0; ph ^= 1; }
+                    }
+                }
+                if (UP) {
+                    const int next_kb = (int)(a.I / kBlock), next_tiles = (int)(a.H / kBlock);
+                    int left = kAhead;
+                    for (MoeRun<false> run((int64_t)chosen * next_tiles, next_kb); run.at < run.end && left > 0;) {
+                        const MoePart v = next_part<false>(s, next_tiles, chosen, next_kb, run);
+                        for (int kb = v.kb0; kb < v.kb1 && left > 0; ++kb, --left)
+                            tma_prefetch_3d(&map_next, kb * kBlock, v.tile * kBlock, v.e);
                     }
                 }
                 drain_ring(bar.boxes, S, it);
@@ -271,10 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dw = smem_desc(s.w), dr = smem_desc(s.rows);
             int st = 0, ph = 0, acc = 0, aph = 1, it = 0;
             bool ok = true;
-            for (int u = u0; u < u1 && ok; ++u) {
-                const MoeUnit v = moe_unit<UP>(s, tiles, chosen, u);
+            for (MoeRun<UP> run = whole_run; run.at < run.end && ok;) {
+                const MoePart v = next_part<UP>(s, tiles, chosen, kb_n, run);
                 const uint32_t idesc = mma_idesc(kBlock, (v.rows + 15) & ~15);
-                for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                for (int kb = v.kb0; kb < v.kb1; ++kb, ++it) {
                     ok = warp_wait(&bar.full[st], ph, patience) && warp_wait(&bar.tempty[acc], aph, patience);
                     if (!ok) break;
                     tmem_fence_after();
@@ -302,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 int st = 0, ph = 0;
                 bool ok = true;
-                for (int u = u0; u < u1 && ok; ++u) {
-                    for (int kb = 0; kb < kb_n; ++kb) {
+                {
+                    for (int64_t at = whole_run.at; at < whole_run.end; ++at) {
                         ok = mbar_wait(&bar.rows_full[st], ph, patience) && mbar_wait(&bar.boxes[st], ph, patience);
                         if (!ok) break;
                         fence_async_shared();
@@ -324,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_blocks = NB * tiles;                          // of the matrix's rows
         int st = 0, ph = 1, ring = 0;
         bool ok = true;
-        for (int u = u0; u < u1 && ok; ++u) {
-            const MoeUnit v = moe_unit<UP>(s, tiles, chosen, u);
+        for (MoeRun<UP> run = whole_run; run.at < run.end && ok;) {
+            const MoePart v = next_part<UP>(s, tiles, chosen, kb_n, run);
             uint32_t ws = (uint32_t)(v.e * n_blocks + v.tile) * kb_n;
             if (lane == 1) ws += (uint32_t)tiles * kb_n;          // (the up block's)
             const uint32_t swizzled = part * kBlock + ((piece ^ (part & 7)) << 4);
@@ -339,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *row_scales = (UP ? a.x_scales : a.h_scales) + (int64_t)scale_row * kb_n;
             const float *w_scales = (UP ? a.gate_up_scales : a.down_scales) + ws;
             const uint8_t *src = (UP ? a.xq : a.h) + piece * 16;
-            for (int kb = 0; kb < kb_n; ++kb) {
+            for (int kb = v.kb0; kb < v.kb1; ++kb) {
                 ok = warp_wait(&bar.done[st], ph, patience);
                 if (!ok) break;
                 const uint32_t dst = smem_addr(s.rows + st * s.rows_bytes) + swizzled;
@@ -364,16 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int chan = quarter * 32 + lane;
         const auto column = [&](int c) { return ((c >> 4) * 2 + half) * 16 + (c & 15); };   // my c-th column
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536;
-        int st = 0, ph = 0, p = 0, ring = 0, unit = 0, word = 0, mine = 0;   // (mine: units of this column tile)
+        const int thread = threadIdx.x - 256;
+        int st = 0, ph = 0, p = 0, ring = 0;
+        int parts = 0, unit = 0, word = 0, mine = 0;         // (mine: units of this column tile that ended here)
         bool ok = true;
-        for (int u = u0; u < u1 && ok; ++u, ++unit) {
-            const MoeUnit v = moe_unit<UP>(s, tiles, chosen, u);
+        for (MoeRun<UP> run = whole_run; run.at < run.end && ok;) {
+            const MoePart v = next_part<UP>(s, tiles, chosen, kb_n, run);
             uint64_t acc[NB][kMine / 2];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int c = 0; c < kMine / 2; ++c) acc[b][c] = 0;
-            for (int kb = 0; kb < kb_n; ++kb) {
+            for (int kb = v.kb0; kb < v.kb1; ++kb) {
                 ok = warp_wait(&bar.done[st], ph, patience);
                 if (!ok) break;
                 tmem_fence_after();
@@ -411,7 +479,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ring = (ring + 1) % kScaleRing;
             }
             if (!ok) break;
+            bool complete = true;
+            if (v.kb1 - v.kb0 < kb_n) {
+                // A part of the unit's contraction: written down, and counted in steps with the CTA that has the first.  Who
+                // brings the last adds the parts, in the order of the contraction.
+                const int c0 = run.owner(v.unit * kb_n), c1 = run.owner(v.unit * kb_n + kb_n - 1), me = blockIdx.x;
+                const auto part_of = [&](int c) {
+                    return a.parts + (int64_t)(c * 2 + (c == c0)) * moe_part_floats(pad) + thread;
+                };
+                const int cols = moe_part_columns(pad);
+                const auto each = [&](auto f) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int c = 0; c < kMine; c += 2)
+                            if (column(c) < v.rows) f(acc[b][c / 2], (b * cols + c) * 256);
+                };
+                float *own = part_of(me);
+                each([&](uint64_t &x, int at) {
+                    own[at] = lo2(x);
+                    own[at + 256] = hi2(x);
+                });
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.split[0]);
+                if (warp == 8) {
+                    ok = warp_wait(&bar.split[0], parts & 1, patience);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const unsigned steps = v.kb1 - v.kb0;
+                        bar.last_part[parts & 1] = atomicAdd(a.split + (UP ? 0 : kMoeCtas) + c0, steps) + steps == (unsigned)kb_n;
+                        __threadfence();
+                        mbar_arrive(&bar.split[1]);
+                    }
+                    __syncwarp();
+                }
+                ok = warp_wait(&bar.split[1], parts & 1, patience);
+                if (!ok) break;
+                complete = bar.last_part[parts & 1];
+                ++parts;
+                if (complete) {
+                    const auto add = [&](int c) {
+                        const float *other = part_of(c);
+                        each([&](uint64_t &x, int at) {
+                            x = pair2(__float_as_uint(lo2(x) + __ldcg(other + at)),
+                                      __float_as_uint(hi2(x) + __ldcg(other + at + 256)));
+                        });
+                    };
+                    if (me > c0) {                       // (mine is in its place in the order again)
+                        each([&](uint64_t &x, int) { x = 0; });
+                        for (int c = c0; c <= me; ++c) add(c);
+                    }
+                    for (int c = me + 1; c <= c1; ++c) add(c);
+                }
+            }
             if (UP) {
+                if (!complete) continue;
                 // h of my columns; their maxima over the warp's 32 channels, then over the four warps
                 uint32_t top = 0;                          // lane c: of column c
 #pragma unroll
@@ -447,16 +570,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q[(int64_t)v.entry[column(c)] * n_cols] =
                         (uint8_t)pack_e4m3x2(h * __shfl_sync(kFull, inv, c), 0.f);
                 }
+                ++unit;
             } else {
                 float *y = a.y + v.tile * kBlock + chan;
 #pragma unroll
                 for (int c = 0; c < kMine; ++c) {
-                    if (column(c) >= v.rows) break;
+                    if (!complete || column(c) >= v.rows) break;
                     y[(int64_t)v.entry[column(c)] * n_cols] = c & 1 ? hi2(acc[0][c / 2]) : lo2(acc[0][c / 2]);
                 }
                 // The last of my units of this tile: count them.  Everybody's y is out before, and in before it is read.
-                ++mine;
-                if (u + 1 < u1 && (u + 1) / chosen == v.tile) continue;
+                mine += complete;
+                if (mine == 0 || (run.at < run.end && run.at / kb_n / chosen == v.tile)) continue;
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.joined[0]);
@@ -489,14 +613,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && bar.gave_up) raise_status(a.route.dev_status, EP_STATUS_TIMEOUT);
 }
 
-template <bool UP>
-cudaError_t launch(const MoeFewArgs &a, cudaStream_t st) {
-    const int64_t K = UP ? a.H : a.I, N = UP ? 2 * a.I : a.H;
+struct MoeMaps {
+    CUtensorMap gate_up, down;
+};
+cudaError_t moe_map(const MoeFewArgs &a, const void *w, int64_t N, int64_t K, CUtensorMap *map) {
     const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)a.route.E};
     const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)(N * K)};
     const cuuint32_t box[3] = {kBlock, kBlock, 1};
-    CUtensorMap w;
-    if (cudaError_t e = encode_map(&w, 3, UP ? a.gate_up : a.down, dims, strides, box)) return e;
+    return encode_map(map, 3, w, dims, strides, box);
+}
+
+template <bool UP>
+cudaError_t launch(const MoeFewArgs &a, const MoeMaps &maps, cudaStream_t st) {
     const int T = (int)a.route.T, pad = (T + 15) & ~15;
     MoeShared<UP> s;
     int stages = kMaxStages;
@@ -514,7 +642,7 @@ cudaError_t launch(const MoeFewArgs &a, cudaStream_t st) {
     });
     if (e) return e;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)num_sms());
+    c.gridDim = dim3((unsigned)std::min(num_sms(), kMoeCtas));
     c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = s.carve(nullptr, stages, pad, (int)a.route.E, T * (int)a.route.k);
     c.stream = st;
@@ -524,7 +652,7 @@ cudaError_t launch(const MoeFewArgs &a, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &attr;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, moe_few_kernel<UP>, a, w, stages);
+    return cudaLaunchKernelEx(&c, moe_few_kernel<UP>, a, UP ? maps.gate_up : maps.down, maps.down, stages);
 }
 
 }  // namespace
@@ -560,6 +688,7 @@ __global__ void __launch_bounds__(kCastThreads) moe_few_start_kernel(const __gri
             }
         } else if (t == 0) {
             for (int i = threadIdx.x - 32; i < (int)(a.H / kBlock); i += kCastThreads - 32) a.arrived[i] = 0;
+            for (int i = threadIdx.x - 32; i < 2 * kMoeCtas; i += kCastThreads - 32) a.split[i] = 0;
         }
         return;
     }
@@ -605,10 +734,13 @@ cudaError_t launch_start(const MoeFewArgs &a, const LaneMap &map, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_moe_few(const MoeFewArgs &a, cudaStream_t st) {
+    MoeMaps maps;
+    if (cudaError_t e = moe_map(a, a.gate_up, 2 * a.I, a.H, &maps.gate_up)) return e;
+    if (cudaError_t e = moe_map(a, a.down, a.H, a.I, &maps.down)) return e;
     const LaneMap map = lane_map(a.route);
     if (cudaError_t e = map.each <= 8 ? launch_start<8>(a, map, st) : launch_start<32>(a, map, st)) return e;
-    if (cudaError_t e = launch<true>(a, st)) return e;
-    return launch<false>(a, st);
+    if (cudaError_t e = launch<true>(a, maps, st)) return e;
+    return launch<false>(a, maps, st);
 }
 
 }  // namespace ep

@@ -40,6 +40,12 @@ struct ExpertArgs {
 
 constexpr int kMoeFewTokens = 64;      // most tokens of ep_moe_few: a tile of every expert holds them
 
+constexpr int kMoeCtas = 152;          // and most CTAs that work on it
+
+// A part of a unit: sums of two blocks of 128 matrix rows by 256 threads, which have every other 16 columns
+__host__ __device__ constexpr int moe_part_columns(int pad) { return (pad + 31) / 32 * 16; }
+__host__ __device__ constexpr int moe_part_floats(int pad) { return 2 * moe_part_columns(pad) * 256; }
+
 struct MoeFewArgs {
     RouteArgs route;         // T, E, k, logits and where the routing goes
     int64_t H, I;
@@ -51,6 +57,8 @@ struct MoeFewArgs {
     uint8_t *h;              // [T k, I] codes, [T k, I / 128] scales, [T k, H] products, [H / 128] counters
     float *h_scales, *y;
     unsigned *arrived;
+    float *parts;            // [kMoeCtas][2][moe_part_floats]: parts of units
+    unsigned *split;         // [2][kMoeCtas]: their steps
     uint16_t *out;
     int64_t wait_clocks;
 };
