@@ -40,20 +40,20 @@ constexpr int kThreads = 512;                   // warpgroup 0: boxes and produc
 constexpr int kIssueRegs = 80, kCopyRegs = 80, kAccRegs = 176;   // 80 + 80 + 2 * 176 = 4 * 128, the launch's registers
 constexpr int kRows = kMoeFewTokens;            // rows of a tile: an expert has at most one for each token
 constexpr int kCopyThreads = 128;
-constexpr int kAcc = 4;                         // accumulators
+constexpr int kMaxAcc = 16;                     // accumulators, as many as tensor memory holds
 constexpr int kMaxStages = 12;                  // operand buffers, as many as shared memory holds
 constexpr int kSharedBytes = 227 * 1024;
 // Steps whose scales are kept: a step's copies wait for the products `stages`
-// steps before, those for the loads of the accumulation kAcc steps before
+// steps before, those for the loads of the accumulation kMaxAcc steps before
 // them, which may still be using that step's scales.
 constexpr int kScaleRing = 32;
-static_assert(kScaleRing > kMaxStages + kAcc + 1, "scales are still in use when they are overwritten");
+static_assert(kScaleRing > kMaxStages + kMaxAcc + 1, "scales are still in use when they are overwritten");
 
 struct MoeBarriers {
     uint64_t boxes[kMaxStages];                             // matrix rows
     uint64_t rows_full[kMaxStages], full[kMaxStages];       // rows and scales; all operands
     uint64_t done[kMaxStages];                              // a step's products: buffers free, sums and scales ready
-    uint64_t tempty[kAcc];                                  // accumulators taken out
+    uint64_t tempty[kMaxAcc];                                  // accumulators taken out
     uint64_t joined[2];                                     // UP: a warpgroup's maxima are written; else: y is, and who
                                                             // is last is known
     uint64_t split[2];                                      // a part is written, and who is last is known
@@ -231,6 +231,9 @@ __device__ __forceinline__ void combine_tile(const MoeFewArgs &a, const MoeShare
     }
 }
 
+// what the launch before this one wrote is there
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // one box towards L2
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
@@ -260,13 +263,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int T = (int)a.route.T, k = (int)a.route.k, E = (int)a.route.E;
     const int K = (int)(UP ? a.H : a.I), n_cols = (int)(UP ? a.I : a.H), kb_n = K / kBlock, tiles = n_cols / kBlock;
     const int pad = (T + 15) & ~15;
+    // Accumulators: 512 columns hold 16 of 16 tokens (UP), 4 of 64.  No more than stages: the accumulation tells a stage's
+    // phases apart by their parity, so the products may not be further ahead of it than one round.
+    const int accs = min(min(kMaxAcc, S), 512 / (NB * pad));
     MoeShared<UP> s;
     s.carve(raw, S, pad, E, T * k);
     MoeBarriers &bar = *s.bar;
 
     if (threadIdx.x == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
     for (int e = threadIdx.x; e < E; e += kThreads) s.tokens[e] = 0;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == kThreads - 1) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&bar.rows_full[i], kCopyThreads);   // the copies' own arrivals
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.done[i], 2);        // the products' commit, word of the operands
         }
-        for (int i = 0; i < kAcc; ++i) mbar_init(&bar.tempty[i], 8);
+        for (int i = 0; i < accs; ++i) mbar_init(&bar.tempty[i], 8);
         mbar_init(&bar.joined[0], UP ? 4 : 8);
         mbar_init(&bar.joined[1], UP ? 4 : 1);
         mbar_init(&bar.split[0], 8);
@@ -283,10 +288,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 14) tmem_alloc<1>(&bar.tmem);
-    asm volatile("griddepcontrol.wait;" ::: "memory");     // what the launches before wrote is there
+    // The second launch waits for the routing before it lets the third begin, so that one finds the routing there (in L2:
+    // it is read past L1) and fills its stages with matrix rows; it waits for the second where it takes h.
+    if (UP) {
+        wait_for_launch_before();
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
     for (int i = threadIdx.x; i < T * k; i += kThreads) {
-        s.idx[i] = (short)a.route.topk_idx[i];
-        if (!UP) s.weight[i] = a.route.topk_weights[i];
+        s.idx[i] = (short)__ldcg(reinterpret_cast<const long long *>(a.route.topk_idx) + i);
+        if (!UP) s.weight[i] = __ldcg(a.route.topk_weights + i);
     }
     __syncthreads();
     list_chosen(s, E, T, k);
@@ -351,13 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int b = 0; b < NB; ++b)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)   // 32 channels a step
-                                mma_f8<1>(tmem + (acc * NB + b) * kRows, da + (b * (kOperand >> 4) + i * 2), db + i * 2,
+                                mma_f8<1>(tmem + (acc * NB + b) * pad, da + (b * (kOperand >> 4) + i * 2), db + i * 2,
                                           idesc, i > 0);
                         mma_commit<1>(&bar.done[st]);
                     }
                     if (++st == S) { st = 0; ph ^= 1; }
-                    acc = (acc + 1) % kAcc;
-                    aph ^= acc == 0;
+                    if (++acc == accs) { acc = 0; aph ^= 1; }
                 }
             }
             drain_ring(bar.done, S, it);
@@ -383,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        if (!UP) wait_for_launch_before();
         // ---- rows and scales: eight lanes bring a row's 128 channels ----
         constexpr int kPass = kCopyThreads / 8, kMine = kRows / kPass;
         const int part = (threadIdx.x - 128) >> 3, piece = lane & 7;
@@ -430,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int chan = quarter * 32 + lane;
         const auto column = [&](int c) { return ((c >> 4) * 2 + half) * 16 + (c & 15); };   // my c-th column
         const uint32_t tm = tmem + (uint32_t)(quarter * 32) * 65536;
+        if (!UP) wait_for_launch_before();                   // (before anything is written, and before this launch ends)
         const int thread = threadIdx.x - 256;
         int st = 0, ph = 0, p = 0, ring = 0;
         int parts = 0, unit = 0, word = 0, mine = 0;         // (mine: units of this column tile that ended here)
@@ -451,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < kMine / 16; ++q)
                         if (column(q * 16) < v.rows)
-                            tmem_ld16(tm + (p * NB + b) * kRows + column(q * 16), t + b * kMine + q * 16);
+                            tmem_ld16(tm + (p * NB + b) * pad + column(q * 16), t + b * kMine + q * 16);
                 tmem_wait_ld<NB * kMine>(t);
                 tmem_fence_before();
                 __syncwarp();
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (++st == S) { st = 0; ph ^= 1; }
-                p = (p + 1) % kAcc;
+                if (++p == accs) p = 0;
                 ring = (ring + 1) % kScaleRing;
             }
             if (!ok) break;
@@ -519,18 +530,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 complete = bar.last_part[parts & 1];
                 ++parts;
                 if (complete) {
-                    const auto add = [&](int c) {
-                        const float *other = part_of(c);
-                        each([&](uint64_t &x, int at) {
-                            x = pair2(__float_as_uint(lo2(x) + __ldcg(other + at)),
-                                      __float_as_uint(hi2(x) + __ldcg(other + at + 256)));
-                        });
+                    const auto add = [&](int from, int to) {
+                        // four parts at a time: their loads are under way together
+                        for (int c = from; c < to; c += 4) {
+                            const float *other[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) other[i] = part_of(min(c + i, to - 1));
+                            each([&](uint64_t &x, int at) {
+                                float lo[4], hi[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    lo[i] = __ldcg(other[i] + at);
+                                    hi[i] = __ldcg(other[i] + at + 256);
+                                }
+                                float l = lo2(x), h = hi2(x);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (c + i < to) {
+                                        l += lo[i];
+                                        h += hi[i];
+                                    }
+                                x = pair2(__float_as_uint(l), __float_as_uint(h));
+                            });
+                        }
                     };
                     if (me > c0) {                       // (mine is in its place in the order again)
                         each([&](uint64_t &x, int) { x = 0; });
-                        for (int c = c0; c <= me; ++c) add(c);
+                        add(c0, me + 1);
                     }
-                    for (int c = me + 1; c <= c1; ++c) add(c);
+                    add(me + 1, c1 + 1);
                 }
             }
             if (UP) {
