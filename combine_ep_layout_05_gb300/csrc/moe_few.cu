@@ -163,20 +163,21 @@ struct MoePart {
     int e, tile, rows, kb0, kb1;
     const short *entry;
 };
-// A CTA's run of steps, all units' steps laid end to end: of whole units, or, where these would leave SMs idle that the
-// memory needs, in equal runs that may begin and end within a unit.  One SM takes 70 GB/s at most (measured: 8 units alone
-// take 0.45 us a step of 32 KB) and some 100 of them all there is; a split unit costs an exchange of some 4 us.  (One
-// token's 128 units of 56 steps: 77 us whole, 89 split; 8 units of 56 steps 47 us split.)
+// A CTA's run of steps, all units' steps laid end to end: of whole units, or in equal runs that may begin and end within
+// a unit.  With every CTA at work a step of 32 KB takes 0.69 us; a CTA whose neighbours are done takes 0.45 (measured: 8
+// units alone), so that whole units end with a tail in which the memory idles; a split unit costs an exchange of some 4
+// us.  (One token's 128 units of 56 steps: 77 us whole, 89 split; 8 such units 47 us whole, 34 split.)
 template <bool UP>
 struct MoeRun {
     int64_t total, at, end;
     int n;                               // CTAs that have steps (split)
     __device__ __forceinline__ MoeRun(int64_t units, int kb_n) {
-        constexpr int kExchange = UP ? 9 : 18, kLeast = UP ? 4 : 8;     // steps: of 4 us, and of a run
+        constexpr int kExchange = UP ? 6 : 12, kLeast = UP ? 4 : 8;     // steps: of 4 us, and of a run
         const int64_t ctas = gridDim.x, c = blockIdx.x, all = units * kb_n;
+        const int64_t full = units > 0 ? (units - 1) / ctas : 0, rest = units - full * ctas;   // rounds of all, then of the rest
         total = all;
         n = (int)min(ctas, (all + kLeast - 1) / kLeast);
-        if (max((units + ctas - 1) / ctas * kb_n, all / 100) <= all / 100 + kExchange) {
+        if (full * kb_n * 100 + kb_n * max((int64_t)65, 100 * rest / ctas) <= 100 * all / ctas + 100 * kExchange) {
             at = units * c / ctas * kb_n;
             end = units * (c + 1) / ctas * kb_n;
         } else {
