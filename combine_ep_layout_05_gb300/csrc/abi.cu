@@ -826,6 +826,12 @@ cudaError_t backward_product(int form, int64_t R, int64_t C, int64_t L, int spli
     a.splits = splits;
     a.dev_status = dev_status;
     a.wait_clocks = ep::kWaitClocks;
+    a.out32 = out32;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.out_align = ep::row_align(out, out_stride * (out32 ? 4 : 2));
+    if (ep::linear_few_time(form, a) < ep::linear_time(R, C, L, false, splits))
+        return ep::launch_linear_few(form, a, A, B, st);
     const bool split = splits > 1;
     a.out32 = split || out32;
     a.out = split ? parts : out;
@@ -880,8 +886,11 @@ int ep_linear(int64_t rows, int64_t in_features, int64_t out_features, int activ
     a.splits = 1;
     a.dev_status = dev_status;
     a.wait_clocks = ep::kWaitClocks;
-    cudaError_t e = ep::launch_linear(ep::kFormForward, a, ep::LinearOperand{x, d.M, d.K, x_stride},
-                                      ep::LinearOperand{w, d.wide, d.K, d.K}, (cudaStream_t)stream);
+    const ep::LinearOperand X{x, d.M, d.K, x_stride}, W{w, d.wide, d.K, d.K};
+    const bool few = ep::linear_few_time(ep::kFormForward, a) <
+                     ep::linear_time(d.M, d.N, d.K, activation == EP_ACT_SWIGLU, 1);
+    cudaError_t e = few ? ep::launch_linear_few(ep::kFormForward, a, X, W, (cudaStream_t)stream)
+                        : ep::launch_linear(ep::kFormForward, a, X, W, (cudaStream_t)stream);
     return e ? cuda_fail(e, "ep_linear launch") : EP_OK;
 }
 

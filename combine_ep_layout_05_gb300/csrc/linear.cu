@@ -321,27 +321,26 @@ cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st)
 
 }  // namespace
 
-// By the time that the pairs' turns take, in us: a step of 64 some 0.3, a unit's start and end 1.5, the parts' sum their
-// bytes at 5 TB/s and a launch.
-int linear_splits(int64_t R, int64_t C, int64_t L) {
-    const int64_t tiles = ((R + kTile - 1) / kTile) * ((C + kTile - 1) / kTile), steps = (L + kStep - 1) / kStep;
-    int best = 1;
-    double least = 1e30;
-    for (int64_t s = 1; s <= std::min<int64_t>(steps, 16); ++s) {
-        const int64_t per = (steps + s - 1) / s;
-        if ((steps + per - 1) / per != s) continue;          // every part has steps
-        const double turns = (double)((tiles * s + 75) / 76);
-        const double t = turns * (0.3 * per + 1.5) + (s > 1 ? 3.0 + 4e-6 * R * C * (s + 1) / 5.0 : 0.0);
-        if (t < least) { least = t; best = (int)s; }
-    }
-    return best;
+// What a launch of this kernel takes, in us, fitted to measurements from a graph: 28 tiles of 4, 16, 32 and 112 steps
+// 7.1, 11.1, 15.4 and 36.8 us; 84 tiles of 32 steps 25.0.  A split contraction adds the parts' sum: their bytes at 5
+// TB/s and a launch.
+double linear_time(int64_t R, int64_t C, int64_t L, bool swiglu, int splits) {
+    const int64_t cols = swiglu ? kPart : kTile, tiles = ((R + kTile - 1) / kTile) * ((C + cols - 1) / cols);
+    const int64_t steps = ((L + kStep - 1) / kStep + splits - 1) / splits, turns = (tiles * splits + 75) / 76;
+    return 5.8 + turns * (0.27 * steps + 1.0) + (splits > 1 ? 3.0 + 4e-6 * R * C * (splits + 1) / 5.0 : 0.0);
 }
 
-// What a launch of this kernel takes, in us, fitted to measurements from a graph: 28 tiles of 4, 16, 32 and 112 steps
-// 7.1, 11.1, 15.4 and 36.8 us; 84 tiles of 32 steps 25.0.
-double linear_time(int64_t rows, int64_t col_tiles, int64_t steps) {
-    const int64_t turns = ((rows + kTile - 1) / kTile * col_tiles + 75) / 76;
-    return 5.8 + turns * (0.27 * steps + 1.0);
+int linear_splits(int64_t R, int64_t C, int64_t L) {
+    const int64_t steps = (L + kStep - 1) / kStep;
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= std::min<int64_t>(steps, 16); ++s) {
+        const int64_t per = (steps + s - 1) / s;
+        if ((steps + per - 1) / per != s) continue;          // every part has steps
+        const double t = linear_time(R, C, L, false, s);
+        if (t < least) { least = t; best = s; }
+    }
+    return best;
 }
 
 cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st) {
@@ -351,8 +350,6 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
     a.col_tiles = (int)((a.C + cols - 1) / cols);
     a.steps = (int)((a.L + kStep - 1) / kStep);
     a.split_steps = (a.steps + a.splits - 1) / a.splits;
-    if (form == kFormForward && linear_few_time(a) < linear_time(a.R, a.col_tiles, a.steps))
-        return launch_linear_few(a, A, B, st);
     LinearMaps maps;
     if (cudaError_t e = operand_map(A, form == kFormGradW, &maps.a)) return e;
     if (cudaError_t e = operand_map(B, form != kFormForward, &maps.b)) return e;

@@ -1,9 +1,9 @@
-// Dense products with an epilogue for few rows: the matrix is read once, and
-// that is what takes the time.
+// Dense products with an epilogue for few rows, and their gradients where tiles are few:
+// the matrix is read once, and that is what takes the time.
 //
-// Same operation as the forward form of linear.cu with the operands' parts
-// exchanged: 128 rows of the matrix are the tensor core's M (SwiGLU: 64 gate and 64
-// up rows), the rows of x its N (16, 32, .. as many as there are, in one box).
+// Same operation as linear.cu, in the same three forms, with the operands' parts
+// exchanged: 128 columns of the output are the tensor core's M (forward: 128 rows of the
+// matrix; SwiGLU: 64 gate and 64 up rows), its rows the N (16, 32, .. 128).
 // A tile of 128 matrix rows alone would leave most SMs idle (a gate of 256 experts has
 // two), so the CTAs of a cluster share a tile's contraction: each sums its part in
 // tensor memory, puts it into its shared memory, and then finishes a share of
@@ -36,7 +36,7 @@ struct FewBarriers {
 };
 
 struct FewMaps {
-    CUtensorMap x, w;
+    CUtensorMap r, c;        // the operands of the rows, and of the columns
 };
 
 // How a launch is cut
@@ -97,7 +97,8 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 
-template <bool SWIGLU>
+// R_MN, C_MN: operands along their rows, as in linear.cu (A_MN and B_MN there)
+template <bool SWIGLU, bool R_MN, bool C_MN>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_few_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ FewMaps maps, const FewPlan p) {
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
@@ -133,16 +134,22 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (warp == 0) {
         if (lane == 0) {
-            // the tile's two halves of 64 matrix rows
-            const int w0 = col * (SWIGLU ? kPart / 2 : kPart), w1 = SWIGLU ? (int)a.C + w0 : w0 + kPart / 2;
+            // the tile's two halves of 64 columns
+            const int c0 = col * (SWIGLU ? kPart / 2 : kPart), c1 = SWIGLU ? (int)a.C + c0 : c0 + kPart / 2;
             int st = 0, ph = 1, it = 0;
             for (int k = first; k < last; ++k, ++it) {
                 if (!mbar_wait(&s.empty[st], ph, patience)) break;
                 mbar_expect_tx(&s.full[st], p.stage);
                 unsigned char *buf = raw + st * p.stage;
-                tma_load_2d(buf, &maps.w, k * kStep * 2, w0, &s.full[st]);
-                tma_load_2d(buf + kPartBytes / 2, &maps.w, k * kStep * 2, w1, &s.full[st]);
-                tma_load_2d(buf + kPartBytes, &maps.x, k * kStep * 2, (int)row0, &s.full[st]);
+                tma_load_2d(buf, &maps.c, C_MN ? c0 * 2 : k * kStep * 2, C_MN ? k * kStep : c0, &s.full[st]);
+                tma_load_2d(buf + kPartBytes / 2, &maps.c, C_MN ? c1 * 2 : k * kStep * 2, C_MN ? k * kStep : c1,
+                            &s.full[st]);
+                buf += kPartBytes;
+                if (R_MN)
+                    for (int i = 0; i < p.rows; i += 64)
+                        tma_load_2d(buf + i * 128, &maps.r, (int)row0 * 2 + i * 2, k * kStep, &s.full[st]);
+                else
+                    tma_load_2d(buf, &maps.r, k * kStep * 2, (int)row0, &s.full[st]);
                 if (++st == p.stages) { st = 0; ph ^= 1; }
             }
             // what has been issued lands, whether its products were or not (together within a second)
@@ -154,8 +161,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
     } else if (warp == 1) {
         const bool issue = elect_one();
-        const uint32_t idesc = mma_idesc_bf16(kPart, p.rows, false, false);
-        const uint64_t desc = smem_desc(raw);
+        const uint32_t idesc = mma_idesc_bf16(kPart, p.rows, C_MN, R_MN);
+        const uint64_t dc = C_MN ? smem_desc_mn(raw, kPartBytes / 2) : smem_desc(raw);
+        const uint64_t dr = R_MN ? smem_desc_mn(raw + kPartBytes, kPartBytes / 2) : smem_desc(raw + kPartBytes);
+        // 16 of the contraction: 32 bytes along a row, or 16 lines of 128 bytes
+        constexpr uint32_t kc = C_MN ? 2048 >> 4 : 32 >> 4, kr = R_MN ? 2048 >> 4 : 32 >> 4;
         int st = 0, ph = 0;
         bool ok = true;
         for (int k = first; k < last; ++k) {
@@ -163,11 +173,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (!ok) break;
             tmem_fence_after();
             if (issue) {
-                const uint64_t da = desc + (uint32_t)(st * p.stage >> 4), db = da + (kPartBytes >> 4);
+                const uint32_t buf = (uint32_t)(st * p.stage >> 4);
                 const int at = k - first, acc = at / p.chain;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mma_bf16<1>(tmem + acc * p.rows, da + i * 2, db + i * 2, idesc, at % p.chain > 0 || i > 0);
+                    mma_bf16<1>(tmem + acc * p.rows, dc + buf + i * kc, dr + buf + i * kr, idesc, at % p.chain > 0 || i > 0);
                 mma_commit<1>(&s.empty[st]);
             }
             if (++st == p.stages) { st = 0; ph ^= 1; }
@@ -264,14 +274,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool R_MN, bool C_MN>
 cudaError_t launch(const LinearArgs &a, const FewMaps &maps, const FewPlan &p, int tiles, int size, cudaStream_t st) {
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
     cached_per_device(ready, [&](int) {
-        e = cudaFuncSetAttribute(linear_few_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(linear_few_kernel<SWIGLU, R_MN, C_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kRing + (int)sizeof(FewBarriers));
-        if (!e) e = cudaFuncSetAttribute(linear_few_kernel<SWIGLU>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (!e) e = cudaFuncSetAttribute(linear_few_kernel<SWIGLU, R_MN, C_MN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
@@ -286,7 +296,7 @@ cudaError_t launch(const LinearArgs &a, const FewMaps &maps, const FewPlan &p, i
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     c.attrs = &attr;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, linear_few_kernel<SWIGLU>, a, maps, p);
+    return cudaLaunchKernelEx(&c, linear_few_kernel<SWIGLU, R_MN, C_MN>, a, maps, p);
 }
 
 }  // namespace
@@ -299,16 +309,19 @@ namespace {
 // 16 CTAs to a tile): each step 0.24 and 0.002 a row, little more where two CTAs share an SM, but not less than the memory;
 // the exchange of the parts 0.0015 a row and CTA of the cluster; each CTA 0.006 to start, and 5 in all.  Clusters of 16 find their places slowly: 128 of their
 // CTAs took 13.2 us for what 64 CTAs of clusters of 8 did in 11.9, 64 of them 10.4 against 11.7.
-FewPlan few_plan(const LinearArgs &a, int &size, int64_t &tiles, double &time) {
+FewPlan few_plan(int form, const LinearArgs &a, int &size, int64_t &tiles, double &time) {
     const bool swiglu = a.act == EP_ACT_SWIGLU;
     FewPlan best;
     FewPlan p;
     // (fp32 results: half the rows, for twice the accumulators)
     const int most = a.out32 ? kPart / 2 : kPart, outs = swiglu ? kPart / 2 : kPart;
     const int64_t row_tiles = (a.R + most - 1) / most;
-    p.tile_rows = (int)((a.R + row_tiles - 1) / row_tiles);
+    // (tiles of equal rows; but boxes of an operand along its rows have to start at multiples of 16 bytes, so these tiles are
+    // whole boxes of 64 rows)
+    p.tile_rows = (int)(row_tiles > 1 && form == kFormGradW ? most : (a.R + row_tiles - 1) / row_tiles);
     p.rows = (p.tile_rows + 15) / 16 * 16;
-    p.stage = kPartBytes + p.rows * kStep * 2;
+    // (an operand along its rows comes in boxes of 64 of them)
+    p.stage = kPartBytes + (form == kFormGradW ? (p.rows + 63) / 64 * 64 : p.rows) * kStep * 2;
     p.stages = std::min(kMaxStages, kRing / p.stage);
     p.steps = (int)((a.L + kStep - 1) / kStep);
     p.col_tiles = (int)((a.C + outs - 1) / outs);
@@ -338,27 +351,33 @@ FewPlan few_plan(const LinearArgs &a, int &size, int64_t &tiles, double &time) {
 
 }  // namespace
 
-double linear_few_time(const LinearArgs &a) {
+double linear_few_time(int form, const LinearArgs &a) {
     int size;
     int64_t tiles;
     double time;
-    few_plan(a, size, tiles, time);
+    few_plan(form, a, size, tiles, time);
     return time;
 }
 
-cudaError_t launch_linear_few(const LinearArgs &a, const LinearOperand &x, const LinearOperand &w, cudaStream_t st) {
+cudaError_t launch_linear_few(int form, const LinearArgs &a, const LinearOperand &A, const LinearOperand &B,
+                              cudaStream_t st) {
     int size;
     int64_t tiles;
     double time;
-    const FewPlan p = few_plan(a, size, tiles, time);
+    const FewPlan p = few_plan(form, a, size, tiles, time);
+    const bool r_mn = form == kFormGradW, c_mn = form != kFormForward;
     FewMaps maps;
-    const cuuint64_t xd[2] = {(cuuint64_t)x.cols * 2, (cuuint64_t)x.rows}, xs[1] = {(cuuint64_t)x.stride * 2};
-    const cuuint64_t wd[2] = {(cuuint64_t)w.cols * 2, (cuuint64_t)w.rows}, ws[1] = {(cuuint64_t)w.stride * 2};
-    const cuuint32_t xb[2] = {128, (cuuint32_t)p.rows}, wb[2] = {128, (cuuint32_t)kPart / 2};
-    if (cudaError_t e = encode_map(&maps.x, 2, x.p, xd, xs, xb)) return e;
-    if (cudaError_t e = encode_map(&maps.w, 2, w.p, wd, ws, wb)) return e;
-    return a.act == EP_ACT_SWIGLU ? launch<true>(a, maps, p, (int)tiles, size, st)
-                                  : launch<false>(a, maps, p, (int)tiles, size, st);
+    const auto map = [](const LinearOperand &o, int rows, CUtensorMap *m) {
+        const cuuint64_t dims[2] = {(cuuint64_t)o.cols * 2, (cuuint64_t)o.rows}, strides[1] = {(cuuint64_t)o.stride * 2};
+        const cuuint32_t box[2] = {128, (cuuint32_t)rows};
+        return encode_map(m, 2, o.p, dims, strides, box);
+    };
+    if (cudaError_t e = map(A, r_mn ? kStep : p.rows, &maps.r)) return e;
+    if (cudaError_t e = map(B, c_mn ? kStep : kPart / 2, &maps.c)) return e;
+    if (form == kFormGradX) return launch<false, false, true>(a, maps, p, (int)tiles, size, st);
+    if (form == kFormGradW) return launch<false, true, true>(a, maps, p, (int)tiles, size, st);
+    return a.act == EP_ACT_SWIGLU ? launch<true, false, false>(a, maps, p, (int)tiles, size, st)
+                                  : launch<false, false, false>(a, maps, p, (int)tiles, size, st);
 }
 
 }  // namespace ep

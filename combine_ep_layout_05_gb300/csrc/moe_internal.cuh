@@ -122,8 +122,10 @@ struct SumPartsArgs {        // out = sum of parts [rows, cols], cols a multiple
 
 // Parts into which the contraction L of an R x C product is split
 int linear_splits(int64_t R, int64_t C, int64_t L);
-double linear_few_time(const LinearArgs &a);         // us that launch_linear_few takes
-cudaError_t launch_linear_few(const LinearArgs &a, const LinearOperand &x, const LinearOperand &w, cudaStream_t st);
+// What the two kernels take, in us: linear.cu's in `splits` parts, and linear_few.cu's
+double linear_time(int64_t R, int64_t C, int64_t L, bool swiglu, int splits);
+double linear_few_time(int form, const LinearArgs &a);
+cudaError_t launch_linear_few(int form, const LinearArgs &a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st);
 cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st);
 cudaError_t launch_moe_few(const MoeFewArgs &a, cudaStream_t st);
 cudaError_t launch_act_grad(const ActGradArgs &a, cudaStream_t st);

@@ -214,6 +214,14 @@ def test_backward(m, act, M, K, N):
     check_backward(m, M, K, N, act, True, True, seed=1)
 
 
+@pytest.mark.parametrize("M,K,N", [(20, 128, 1000), (64, 256, 300), (200, 1000, 65), (96, 520, 129)])
+@pytest.mark.parametrize("w32", [False, True])
+def test_backward_tiles_of_rows(m, M, K, N, w32):
+    """Rows of the matrix's gradient in several tiles, which start where copies may start."""
+    check_backward(m, M, K, N, "none", False, w32)
+    check_backward(m, M, K, N, "swiglu", True, w32)
+
+
 @pytest.mark.parametrize("which", ["x", "w", "b", "xw", "wb"])
 def test_backward_some_outputs(m, which):
     check_backward(m, 100, 128, 96, "none", False, True, which=which)
