@@ -815,10 +815,11 @@ BackwardParts backward_parts(const LinearSizes &d) {
     return b;
 }
 
-// One product of the backward pass: straight into its output, or in parts that are summed
+// One product of the backward pass: straight into its output, or in parts that are summed.  order: how it follows the
+// launches before it, and how the next may.
 cudaError_t backward_product(int form, int64_t R, int64_t C, int64_t L, int splits, const ep::LinearOperand &A,
                              const ep::LinearOperand &B, bool out32, void *out, int64_t out_stride, float *parts,
-                             int32_t *dev_status, cudaStream_t st) {
+                             int &order, bool &parts_used, int32_t *dev_status, cudaStream_t st) {
     ep::LinearArgs a{};
     a.R = R;
     a.C = C;
@@ -830,9 +831,13 @@ cudaError_t backward_product(int form, int64_t R, int64_t C, int64_t L, int spli
     a.out = out;
     a.out_stride = out_stride;
     a.out_align = ep::row_align(out, out_stride * (out32 ? 4 : 2));
+    a.order = order;
+    order = ep::kBeside;       // (what comes next does not read this product)
     if (ep::linear_few_time(form, a) < ep::linear_time(R, C, L, false, splits))
         return ep::launch_linear_few(form, a, A, B, st);
     const bool split = splits > 1;
+    if (split && parts_used && a.order == ep::kBeside) a.order = ep::kAfter;   // the parts before are being summed
+    parts_used |= split;
     a.out32 = split || out32;
     a.out = split ? parts : out;
     a.out_stride = split ? C : out_stride;
@@ -942,6 +947,8 @@ int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, 
     const bool direct = activation == EP_ACT_NONE && !grad32 && grad_stride % 8 == 0 &&
                         grad_stride < (int64_t)1 << 38 && aligned(grad_out, 16);
     const bool products = grad_x || grad_w;
+    int order = ep::kFirst;
+    bool parts_used = false;
     cudaError_t e = cudaSuccess;
     if (grad_bias || (products && !direct)) {
         ep::ActGradArgs a{};
@@ -959,15 +966,17 @@ int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, 
         a.bias = grad_bias;
         e = ep::launch_act_grad(a, st);
         if (e) return cuda_fail(e, "ep_linear_backward launch");
+        // the products need G, not the columns' sums, whose own launch has waited for G
+        order = grad_bias ? ep::kBeside : ep::kAfter;
     }
     const ep::LinearOperand G{direct ? (const uint16_t *)grad_out : (const uint16_t *)ws, d.M, d.wide,
                               direct ? grad_stride : b.g_stride};
     if (grad_x)
         e = backward_product(ep::kFormGradX, d.M, d.K, d.wide, b.splits_x, G, ep::LinearOperand{w, d.wide, d.K, d.K},
-                             false, grad_x, grad_x_stride, parts, dev_status, st);
+                             false, grad_x, grad_x_stride, parts, order, parts_used, dev_status, st);
     if (!e && grad_w)
         e = backward_product(ep::kFormGradW, d.wide, d.K, d.M, b.splits_w, G, ep::LinearOperand{x, d.M, d.K, x_stride},
-                             w32, grad_w, d.K, parts, dev_status, st);
+                             w32, grad_w, d.K, parts, order, parts_used, dev_status, st);
     return e ? cuda_fail(e, "ep_linear_backward launch") : EP_OK;
 }
 

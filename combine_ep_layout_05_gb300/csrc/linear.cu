@@ -101,6 +101,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
     const Patience patience{&s.gave_up, a.wait_clocks};
+    if (a.order == kAfter) wait_for_launch_before();
+    let_next_launch_begin();
 
     if (LONG && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
@@ -288,6 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_free<2>(tmem);
     }
     if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+    if (a.order == kBeside) wait_for_launch_before();
 }
 
 // The operand as a tensor map of bytes.  Along the contraction: boxes of 128
@@ -315,8 +318,7 @@ cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st)
     if (e) return e;
     const int64_t units = (int64_t)a.row_tiles * a.col_tiles * a.splits;
     const int grid = (int)std::min<int64_t>(num_sms() & ~1, 2 * units);
-    linear_kernel<SWIGLU, A_MN, B_MN, LONG><<<grid, kThreads, bytes, st>>>(a, maps);
-    return cudaGetLastError();
+    return launch_in_order(a.order, linear_kernel<SWIGLU, A_MN, B_MN, LONG>, dim3(grid), kThreads, bytes, 0, st, a, maps);
 }
 
 }  // namespace

@@ -80,6 +80,7 @@ __device__ __forceinline__ void store8(uint16_t *p, int n, bool vec, const float
 // aligned to 16 bytes at every 8th column.
 template <typename L, bool SWIGLU>
 __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(const ActGradArgs a, int vec) {
+    let_next_launch_begin();
     constexpr int P = SWIGLU ? 2 : 1;
     __shared__ float part[kLanes][P][kCols];
     const int group = threadIdx.x & 31, row_lane = threadIdx.x >> 5;
@@ -141,6 +142,8 @@ __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(const ActGradArg
 
 // bias[c] = sum over the blocks of sums[block][c]: 8 threads a column
 __global__ void __launch_bounds__(kGradThreads) sum_blocks_kernel(const float *sums, int blocks, int64_t cols, float *bias) {
+    wait_for_launch_before();
+    let_next_launch_begin();
     __shared__ float part[kLanes][32];
     const int x = threadIdx.x & 31, l = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
@@ -159,6 +162,8 @@ __global__ void __launch_bounds__(kGradThreads) sum_blocks_kernel(const float *s
 
 // out[r, c] = sum over the parts of parts[part][r, c], 8 columns (which divide a row) a thread
 __global__ void __launch_bounds__(kGradThreads) sum_parts_kernel(const SumPartsArgs a) {
+    wait_for_launch_before();
+    let_next_launch_begin();
     const int64_t i = ((int64_t)blockIdx.x * kGradThreads + threadIdx.x) * 8;
     if (i >= a.rows * a.cols) return;
     float v[8] = {};
@@ -206,15 +211,14 @@ cudaError_t launch_act_grad(const ActGradArgs &a, cudaStream_t st) {
     }
     if (cudaError_t e = cudaGetLastError()) return e;
     if (!a.sums) return cudaSuccess;
-    sum_blocks_kernel<<<(unsigned)((wide + 31) / 32), kGradThreads, 0, st>>>(a.sums, a.blocks, wide, a.bias);
-    return cudaGetLastError();
+    return launch_in_order(kAfter, sum_blocks_kernel, dim3((unsigned)((wide + 31) / 32)), kGradThreads, 0, 0, st, a.sums,
+                           a.blocks, wide, a.bias);
 }
 
 cudaError_t launch_sum_parts(SumPartsArgs a, cudaStream_t st) {
     a.vec = aligned16(a.out, a.stride * 2);
     const int64_t n = (a.rows * a.cols / 8 + kGradThreads - 1) / kGradThreads;
-    sum_parts_kernel<<<(unsigned)n, kGradThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_in_order(kAfter, sum_parts_kernel, dim3((unsigned)n), kGradThreads, 0, 0, st, a);
 }
 
 }  // namespace ep

@@ -2,6 +2,7 @@
 // activations and the rows of an epilogue.
 #pragma once
 
+#include "launch_order.cuh"
 #include "tcgen05.cuh"
 #include "vec8.cuh"
 

@@ -131,6 +131,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_fence_after();
     const uint32_t tmem = s.tmem;
     const Patience patience{&s.gave_up, a.wait_clocks};
+    if (a.order == kAfter) wait_for_launch_before();
+    let_next_launch_begin();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -272,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kColumns));
     }
     if (threadIdx.x == 0 && s.gave_up) raise_status(a.dev_status, EP_STATUS_TIMEOUT);
+    if (a.order == kBeside) wait_for_launch_before();
 }
 
 template <bool SWIGLU, bool R_MN, bool C_MN>
@@ -285,18 +288,8 @@ cudaError_t launch(const LinearArgs &a, const FewMaps &maps, const FewPlan &p, i
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(tiles * size));
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = p.stage * p.stages + sizeof(FewBarriers);
-    c.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)size;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    c.attrs = &attr;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, linear_few_kernel<SWIGLU, R_MN, C_MN>, a, maps, p);
+    return launch_in_order(a.order, linear_few_kernel<SWIGLU, R_MN, C_MN>, dim3((unsigned)(tiles * size)), kThreads,
+                           p.stage * p.stages + sizeof(FewBarriers), size, st, a, maps, p);
 }
 
 }  // namespace

@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <cstddef>
 
+#include "launch_order.cuh"
 #include "route_device.cuh"
 #include "tcgen05.cuh"
 
@@ -232,9 +233,6 @@ __device__ __forceinline__ void combine_tile(const MoeFewArgs &a, const MoeShare
     }
 }
 
-// what the launch before this one wrote is there
-__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // one box towards L2
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
@@ -293,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // it is read past L1) and fills its stages with matrix rows; it waits for the second where it takes h.
     if (UP) {
         wait_for_launch_before();
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        let_next_launch_begin();
     }
     for (int i = threadIdx.x; i < T * k; i += kThreads) {
         s.idx[i] = (short)__ldcg(reinterpret_cast<const long long *>(a.route.topk_idx) + i);
@@ -670,18 +668,10 @@ cudaError_t launch(const MoeFewArgs &a, const MoeMaps &maps, cudaStream_t st) {
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)std::min(num_sms(), kMoeCtas));
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = s.carve(nullptr, stages, pad, (int)a.route.E, T * (int)a.route.k);
-    c.stream = st;
-    // it may start while the launch before it ends, and waits before it reads what that one wrote
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &attr;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, moe_few_kernel<UP>, a, UP ? maps.gate_up : maps.down, maps.down, stages);
+    // it begins while the launch before it ends, and waits before it reads what that one wrote
+    return launch_in_order(kAfter, moe_few_kernel<UP>, dim3((unsigned)std::min(num_sms(), kMoeCtas)), kThreads,
+                           s.carve(nullptr, stages, pad, (int)a.route.E, T * (int)a.route.k), 0, st, a,
+                           UP ? maps.gate_up : maps.down, maps.down, stages);
 }
 
 }  // namespace
@@ -694,7 +684,7 @@ constexpr int kCastThreads = 128;
 // j), the others cast 16 blocks of 128 channels each, as ep_dispatch does.
 template <int V, int KEY>
 __global__ void __launch_bounds__(kCastThreads) moe_few_start_kernel(const __grid_constant__ MoeFewArgs a, const LaneMap map) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_launch_begin();
     const RouteArgs &r = a.route;
     const int t = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0) {

@@ -6,6 +6,14 @@
 
 namespace ep {
 
+// How a launch follows the one before it on its stream.  kAfter and kBeside begin while that one runs (programmatic
+// dependent launch) once each of its CTAs has said that they may; each says so behind its own wait, if it has one.
+//   kFirst   an ordinary launch, the first of a call
+//   kAfter   waits at its start for the launch before it: it reads what that one writes
+//   kBeside  runs beside it and waits at its end: it reads only what launches before that one wrote (which are over:
+//            that one has waited for them, or began behind one that had) and writes nothing that one reads or writes
+enum { kFirst, kAfter, kBeside };
+
 struct RouteArgs {
     int64_t T, E, k;
     ep_router r;
@@ -79,6 +87,7 @@ struct LinearArgs {
     int out_align, pre_align, residual_align;   // see row_align
     int splits;              // parts of the contraction (at least 1; every part has steps)
     int row_tiles, col_tiles, split_steps, steps;           // by the launcher
+    int order;               // kFirst, kAfter or kBeside
     int64_t split_stride;    // elements between the partial sums of two splits
     int32_t *dev_status;
     int64_t wait_clocks;
@@ -117,7 +126,7 @@ struct SumPartsArgs {        // out = sum of parts [rows, cols], cols a multiple
     bool out32;
     void *out;
     int64_t stride;          // elements between rows of out
-    bool vec;                // by the launcher
+    bool vec;                // by the launcher (always kAfter)
 };
 
 // Parts into which the contraction L of an R x C product is split
