@@ -539,41 +539,58 @@ def ep_selftest_expert_timeout(p: ep_problem, kernel: int, a, a_scales, w, w_sca
         _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
 
 
-def _rows(t, name, rows, cols, dtypes=(torch.bfloat16,)):
+_F16, _F32 = (torch.bfloat16,), (torch.float32,)
+# the current device; the private call costs a fifth of the public one, which first asks whether CUDA is initialised (it
+# is: there are tensors)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _rows(t, name, rows, cols, dtypes=_F16):
     """(pointer, row stride) of a [rows, cols] tensor whose rows are contiguous (any row stride); None: (None, 0)."""
     if t is None:
         return None, 0
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == (rows, cols):
+        stride, step = t.stride()
+        if rows <= 1:
+            stride = cols
+        if (step == 1 or cols <= 1) and stride >= cols:
+            return t.data_ptr(), stride
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    stride = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or stride < cols:
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), stride
+    raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
 
 
 def _shaped(t, name, shape, dtypes):
     """Pointer of a contiguous tensor of this shape (None: None)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape):
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
         raise ValueError(f"{name} must be a tensor {list(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     return _ptr(t, None, name)
 
 
-def _one_device(*tensors):
-    """The library launches on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
+def _stream_here(stream, *tensors):
+    """Handle of the stream.  The library launches on the current device: the stream and every tensor have to be there."""
+    dev = _current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return _raw_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{dev}")
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _linear_sizes(x, w, activation):
@@ -583,13 +600,12 @@ def _linear_sizes(x, w, activation):
         raise ValueError(f"w must be a tensor [rows, {x.shape[1]}]")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    wide = w.shape[0]
-    if activation == "swiglu" and wide % 2:
+    (M, K), wide = x.shape, w.shape[0]
+    if activation != "swiglu":
+        return M, K, wide, wide
+    if wide % 2:
         raise ValueError("w must have an even number of rows with swiglu")
-    return x.shape[0], x.shape[1], wide // 2 if activation == "swiglu" else wide, wide
-
-
-_F16, _F32 = (torch.bfloat16,), (torch.float32,)
+    return M, K, wide // 2, wide
 
 
 def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "none", dev_status=None,
@@ -604,8 +620,8 @@ def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "
         raise ValueError("out must be a tensor")
     args = (M, K, N, ACTIVATIONS[activation], xp, xs, _shaped(w, "w", (wide, K), _F16),
             _shaped(bias, "bias", (wide,), _F32), rp, rs, EP_FP32 if out.dtype == torch.float32 else EP_BF16, op, os_,
-            _shaped(pre, "pre", (M, wide), _F16), _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
-    _one_device(x, w, out, bias, residual, pre, dev_status)
+            _shaped(pre, "pre", (M, wide), _F16), _ptr(dev_status, torch.int32, "dev_status", 1),
+            _stream_here(stream, x, w, out, bias, residual, pre, dev_status))
     return _call("ep_linear", _lib.ep_linear, args)
 
 
@@ -629,8 +645,8 @@ def ep_linear_backward(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None,
             _shaped(pre, "pre", (M, wide), _F16), gxp, gxs, code(grad_w),
             _shaped(grad_w, "grad_w", (wide, K), _F16 + _F32), _shaped(grad_bias, "grad_bias", (wide,), _F32),
             _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
-            _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
-    _one_device(grad_out, x, w, grad_x, grad_w, grad_bias, pre, workspace, dev_status)
+            _ptr(dev_status, torch.int32, "dev_status", 1),
+            _stream_here(stream, grad_out, x, w, grad_x, grad_w, grad_bias, pre, workspace, dev_status))
     return _call("ep_linear_backward", _lib.ep_linear_backward, args)
 
 
@@ -648,7 +664,7 @@ def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_sc
     I = N // 2
     if N % 256 or K != H or H % 128:
         raise ValueError(f"gate_up must be [{E}, 2 I, {H}], H and I multiples of 128, got {list(gate_up.shape)}")
-    u8, f32, bf16 = (torch.uint8,), (torch.float32,), (torch.bfloat16,)
+    u8, f32, bf16 = (torch.uint8,), _F32, _F16
     ptr, stride, dt = _logits(logits, p, "logits")
     args = (ctypes.byref(p), ctypes.byref(r), I, _shaped(x, "x", (T, H), bf16), dt, ptr, stride,
             _ptr(bias, torch.float32, "bias", E), _shaped(gate_up, "gate_up", (E, N, H), u8),
@@ -658,9 +674,9 @@ def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_sc
             _shaped(residual, "residual", (T, H), bf16), _shaped(out, "out", (T, H), bf16),
             _ptr(topk_idx, torch.int64, "topk_idx", n), _ptr(topk_weights, torch.float32, "topk_weights", n),
             _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
-            _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream))
-    _one_device(x, logits, bias, gate_up, gate_up_scales, down, down_scales, residual, out, topk_idx, topk_weights,
-                workspace, dev_status)
+            _ptr(dev_status, torch.int32, "dev_status", 1),
+            _stream_here(stream, x, logits, bias, gate_up, gate_up_scales, down, down_scales, residual, out, topk_idx,
+                         topk_weights, workspace, dev_status))
     return _call("ep_moe_few", _lib.ep_moe_few, args)
 
 

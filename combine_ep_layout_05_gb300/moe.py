@@ -1,5 +1,6 @@
-"""A mixture-of-experts layer over the library: routing, FP8 dispatch, FP8
-experts and combine, with the gradients that reach the router.
+"""A mixture-of-experts layer over the library: the gate, routing, FP8 dispatch,
+FP8 experts, combine and a shared expert, with the gradients that reach the
+router, the gate and the shared expert.
 
 ``MoeLayer`` keeps the device buffers of one problem and issues, on one stream,
 
@@ -7,9 +8,14 @@ experts and combine, with the gradients that reach the router.
              -> ep_expert_gemm -> ep_combine
 
 every step in the library's kernels, nothing on the host in between, so that a
-forward pass can be recorded into a CUDA graph.  ``router_grad`` is the way back
-from the output's gradient to the logits': ep_combine_backward, then
-ep_route_backward.  (The experts are served in FP8 and take no gradient.)
+forward pass can be recorded into a CUDA graph.  The gate (ep_linear: the logits
+from the tokens) and a shared expert (two of ep_linear: SwiGLU, and the down
+product onto the routed experts' sum) are part of it where the layer has them.
+With ``few`` the routed part is one call, ep_moe_few, for up to 64 tokens.
+``router_grad`` is the way back from the output's gradient to the logits':
+ep_combine_backward, then ep_route_backward; ``gate_grad`` goes on to the gate
+and the tokens, ``shared_grad`` through the shared expert.  (The routed experts
+are served in FP8 and take no gradient.)
 """
 from __future__ import annotations
 
@@ -38,26 +44,71 @@ def quantize_blocks(w):
 
 class MoeLayer:
     def __init__(self, T: int, H: int, I: int, E: int, k: int, R: int, gate_up, gate_up_scales, down, down_scales,
-                 router: ep.ep_router | None = None, bias=None, device="cuda"):
+                 router: ep.ep_router | None = None, bias=None, device="cuda", gate=None, shared_gate_up=None,
+                 shared_down=None, few: bool = False):
         """T tokens of R source ranks, hidden H, E experts of intermediate size I, k a token.  gate_up [E, 2 I, H]
         and down [E, H, I] are e4m3 codes (uint8) with fp32 scales for 128 x 128 blocks (see quantize_blocks);
-        bias [E] fp32 moves the choice of experts (None: no bias)."""
+        bias [E] fp32 moves the choice of experts (None: no bias).  gate [E, H] bf16 makes the logits from the tokens
+        (None: forward is given them); shared_gate_up [2 S, H] and shared_down [H, S] bf16 are a shared expert (None:
+        none).  few: the routed experts in one call that makes no receive buffers, for T <= 64; such a layer has no
+        router_grad."""
         if tuple(gate_up.shape) != (E, 2 * I, H) or tuple(down.shape) != (E, H, I):
             raise ValueError(f"gate_up must be [{E}, {2 * I}, {H}] and down [{E}, {H}, {I}]")
-        self.pipe = EpPipeline(T, H, k, E, R, layout="expert_major", dtype="fp8_e4m3", device=device)
-        self.p, self.status = self.pipe.p, self.pipe.status
+        if gate is not None and tuple(gate.shape) != (E, H):
+            raise ValueError(f"gate must be [{E}, {H}]")
+        if (shared_gate_up is None) != (shared_down is None):
+            raise ValueError("a shared expert has both matrices")
+        if shared_down is not None and (shared_down.dim() != 2 or shared_down.shape[0] != H or
+                                        tuple(shared_gate_up.shape) != (2 * shared_down.shape[1], H)):
+            raise ValueError(f"shared_gate_up must be [2 S, {H}] and shared_down [{H}, S]")
+        self.few = few
+        buffer = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=device)
+        if few:
+            self.p = ep.problem(T, H, k, E, R)
+            bytes_ = ep.ep_moe_few_workspace_bytes(self.p, I)
+            if not bytes_:
+                raise ValueError(ep.ep_last_error_string())
+            self.workspace, self.out = buffer(bytes_, dtype=torch.uint8), buffer(T, H)
+            self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        else:
+            self.pipe = EpPipeline(T, H, k, E, R, layout="expert_major", dtype="fp8_e4m3", device=device)
+            self.p, self.status = self.pipe.p, self.pipe.status
+            self.act = buffer(self.pipe.rows, I, dtype=torch.uint8)
+            self.act_scales = buffer(self.pipe.rows, I // 128, dtype=torch.float32)
+            self.grad_weights = buffer(T, k, dtype=torch.float32)
         self.router = ep.router() if router is None else router
         self.bias = bias
         self.gate_up, self.gate_up_scales, self.down, self.down_scales = gate_up, gate_up_scales, down, down_scales
-        self.idx = torch.empty((T, k), dtype=torch.int64, device=device)
-        self.weights = torch.empty((T, k), dtype=torch.float32, device=device)
-        self.act = torch.empty((self.pipe.rows, I), dtype=torch.uint8, device=device)
-        self.act_scales = torch.empty((self.pipe.rows, I // 128), dtype=torch.float32, device=device)
-        self.grad_weights = torch.empty((T, k), dtype=torch.float32, device=device)
+        self.idx = buffer(T, k, dtype=torch.int64)
+        self.weights = buffer(T, k, dtype=torch.float32)
+        self.gate = gate
+        self.logits = None if gate is None else buffer(T, E, dtype=torch.float32)
+        self.shared_gate_up, self.shared_down = shared_gate_up, shared_down
+        if shared_down is not None:
+            S = shared_down.shape[1]
+            self.shared_pre, self.shared_act = buffer(T, 2 * S), buffer(T, S)
 
-    def forward(self, x, logits, stream=None, out=None):
-        """x [T, H] bf16 and gate logits [T, E] (bf16 or fp32) -> [T, H] bf16.  self.idx, self.weights and
-        self.pipe.buf.tokens_per_expert hold the routing; ep_get_status(self.status) tells of bad logits."""
+    def forward(self, x, logits=None, stream=None, out=None):
+        """x [T, H] bf16 and gate logits [T, E] (bf16 or fp32; None: the gate's, kept in self.logits) -> [T, H] bf16.
+        self.idx, self.weights and (not few) self.pipe.buf.tokens_per_expert hold the routing;
+        ep_get_status(self.status) tells of bad logits."""
+        if logits is None:
+            if self.gate is None:
+                raise ValueError("a layer without a gate needs logits")
+            logits = self.logits
+            ep.ep_linear(x, self.gate, logits, dev_status=self.status, stream=stream)
+        shared = self.shared_down is not None
+        if shared:
+            ep.ep_linear(x, self.shared_gate_up, self.shared_act, pre=self.shared_pre, activation="swiglu",
+                         dev_status=self.status, stream=stream)
+        if self.few:
+            out = self.out if out is None else out
+            if shared:
+                ep.ep_linear(self.shared_act, self.shared_down, out, dev_status=self.status, stream=stream)
+            ep.ep_moe_few(self.p, self.router, x, logits, self.bias, self.gate_up, self.gate_up_scales, self.down,
+                          self.down_scales, out, self.idx, self.weights, self.workspace,
+                          residual=out if shared else None, dev_status=self.status, stream=stream)
+            return out
         p, q = self.p, self.pipe
         ep.ep_route(p, self.router, logits, self.bias, self.idx, self.weights, self.status, stream)
         if q.fused:
@@ -69,41 +120,85 @@ class MoeLayer:
         ep.ep_expert_swiglu(p, q.recv, q.recv_scales, self.gate_up, self.gate_up_scales, counts, self.act,
                             self.act_scales, self.status, stream)
         ep.ep_expert_gemm(p, self.act, self.act_scales, self.down, self.down_scales, counts, q.y, self.status, stream)
-        return q.combine_step(self.idx, self.weights, stream, out)
+        out = q.combine_step(self.idx, self.weights, stream, out)
+        if shared:
+            ep.ep_linear(self.shared_act, self.shared_down, out, residual=out, dev_status=self.status, stream=stream)
+        return out
 
     def router_grad(self, grad_out, logits, grad_logits, stream=None):
         """After forward: writes the gradient of the loss with respect to the logits [T, E], through the routing
         weights (the choice of experts is a constant), from grad_out [T, H] bf16."""
+        if self.few:
+            raise ValueError("a layer with few=True keeps no expert rows: it has no router_grad")
         p, q = self.p, self.pipe
         ep.ep_combine_backward(p, "expert_major", grad_out, q.y, self.idx, self.weights, q.buf.rank_slot,
                                q.buf.expert_slot, None, self.grad_weights, self.status, stream)
         ep.ep_route_backward(p, self.router, logits, self.idx, self.grad_weights, grad_logits, self.status, stream)
         return grad_logits
 
+    def _linear_backward(self, grad_out, x, w, grad_x, grad_w, pre, activation, stream):
+        wide = w.shape[0]
+        need = ep.ep_linear_backward_workspace_bytes(x.shape[0], x.shape[1], wide // 2 if activation == "swiglu" else wide,
+                                                     activation)
+        ws = getattr(self, "backward_workspace", None)
+        if ws is None or ws.numel() < need:
+            self.backward_workspace = ws = torch.empty(max(16, need), dtype=torch.uint8, device=x.device)
+        ep.ep_linear_backward(grad_out, x, w, grad_x=grad_x, grad_w=grad_w, pre=pre, activation=activation, workspace=ws,
+                              dev_status=self.status, stream=stream)
+
+    def gate_grad(self, grad_logits, x, grad_x=None, grad_gate=None, stream=None):
+        """Gradients of the logits' product, from router_grad's: grad_x [T, H] bf16 (the tokens', through the gate
+        alone) and grad_gate [E, H] bf16 or fp32; None: not computed."""
+        self._linear_backward(grad_logits, x, self.gate, grad_x, grad_gate, None, "none", stream)
+
+    def shared_grad(self, grad_out, x, grad_x=None, grad_gate_up=None, grad_down=None, stream=None):
+        """After forward: gradients through the shared expert from grad_out [T, H] bf16: the tokens' (bf16) and its
+        matrices' (bf16 or fp32); None: not computed."""
+        grad_act = None
+        if grad_x is not None or grad_gate_up is not None:
+            grad_act = torch.empty_like(self.shared_act)
+        self._linear_backward(grad_out, self.shared_act, self.shared_down, grad_act, grad_down, None, "none", stream)
+        if grad_act is not None:
+            self._linear_backward(grad_act, x, self.shared_gate_up, grad_x, grad_gate_up, self.shared_pre, "swiglu",
+                                  stream)
+
 
 def demo(T: int = 256, H: int = 7168, I: int = 2048, E: int = 64, k: int = 8, R: int = 8) -> None:
-    """One forward and router-gradient pass over random weights, with its time (python -m
-    combine_ep_layout_05_gb300.moe)."""
+    """One forward and backward pass of a layer with a gate and a shared expert over random weights, and a decode step of
+    8 tokens, with their times (python -m combine_ep_layout_05_gb300.moe)."""
     dev = "cuda"
     g = torch.Generator(dev).manual_seed(0)
     rand = lambda *s: torch.randn(*s, generator=g, device=dev)
-    layer = MoeLayer(T, H, I, E, k, R, *quantize_blocks(rand(E, 2 * I, H) * H ** -0.5),
-                     *quantize_blocks(rand(E, H, I) * I ** -0.5),
-                     router=ep.router("sigmoid", num_groups=8, topk_groups=4, group_best=2, scale=2.5),
-                     bias=torch.zeros(E, device=dev))
-    x, logits, grad = rand(T, H).bfloat16(), rand(T, E), torch.empty(T, E, device=dev)
+    experts = (*quantize_blocks(rand(E, 2 * I, H) * H ** -0.5), *quantize_blocks(rand(E, H, I) * I ** -0.5))
+    kept = dict(router=ep.router("sigmoid", num_groups=8, topk_groups=4, group_best=2, scale=2.5),
+                bias=torch.zeros(E, device=dev), gate=(rand(E, H) * H ** -0.5).bfloat16(),
+                shared_gate_up=(rand(2 * I, H) * H ** -0.5).bfloat16(), shared_down=(rand(H, I) * I ** -0.5).bfloat16())
+    layer = MoeLayer(T, H, I, E, k, R, *experts, **kept)
+    x, grad = rand(T, H).bfloat16(), torch.empty(T, E, device=dev)
+    grad_x, grad_gate = torch.empty_like(x), torch.empty_like(kept["gate"])
+    grad_up, grad_down = torch.empty_like(kept["shared_gate_up"]), torch.empty_like(kept["shared_down"])
+
+    def backward(out):
+        layer.router_grad(out, layer.logits, grad)
+        layer.gate_grad(grad, x, grad_x, grad_gate)
+        layer.shared_grad(out, x, grad_x, grad_up, grad_down)
+    few = MoeLayer(8, H, I, E, k, 1, *experts, **kept, few=True)
     for _ in range(3):
-        out = layer.forward(x, logits)
-        layer.router_grad(out, logits, grad)
-    t0, t1, t2 = (torch.cuda.Event(enable_timing=True) for _ in range(3))
-    t0.record()
-    out = layer.forward(x, logits)
-    t1.record()
-    layer.router_grad(out, logits, grad)
-    t2.record()
-    ep_status = ep.ep_get_status(layer.status)
-    print(f"{T} tokens, {E} experts of {H} x {I}, top-{k}: forward {t0.elapsed_time(t1) * 1e3:.0f} us, router gradient "
-          f"{t1.elapsed_time(t2) * 1e3:.0f} us, status {ep_status}, |out| {float(out.float().abs().mean()):.4f}")
+        out = layer.forward(x)
+        backward(out)
+        few.forward(x[:8])
+    t = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
+    t[0].record()
+    out = layer.forward(x)
+    t[1].record()
+    backward(out)
+    t[2].record()
+    few.forward(x[:8])
+    t[3].record()
+    status = ep.ep_get_status(layer.status) | ep.ep_get_status(few.status)
+    us = [a.elapsed_time(b) * 1e3 for a, b in zip(t, t[1:])]
+    print(f"{T} tokens, {E} experts of {H} x {I}, top-{k}, one shared: forward {us[0]:.0f} us, gradients {us[1]:.0f} us; "
+          f"8 tokens {us[2]:.0f} us; status {status}, |out| {float(out.float().abs().mean()):.4f}")
 
 
 if __name__ == "__main__":
