@@ -48,6 +48,7 @@ constexpr int kSharedBytes = 227 * 1024;
 // steps before, those for the loads of the accumulation kMaxAcc steps before
 // them, which may still be using that step's scales.
 constexpr int kScaleRing = 32;
+static_assert(kMaxStages <= 16 && kMaxAcc == 16, "a lane for each barrier");
 static_assert(kScaleRing > kMaxStages + kMaxAcc + 1, "scales are still in use when they are overwritten");
 
 struct MoeBarriers {
@@ -206,29 +207,40 @@ __device__ __forceinline__ MoePart next_part(const S &s, int tiles, int chosen, 
     return v;
 }
 
-// out[t, columns of a tile] by the 256 accumulating threads
+// out[t, columns of a tile] by the 256 accumulating threads: 4 columns a thread, a token a warp; eight rows of y are under
+// way together
 template <bool UP>
 __device__ __forceinline__ void combine_tile(const MoeFewArgs &a, const MoeShared<UP> &c, int tile) {
     const int thread = threadIdx.x - 256, col = tile * kBlock + (thread & 31) * 4, k = (int)a.route.k;
+    const float *y = a.y + col;
     for (int t = thread >> 5; t < (int)a.route.T; t += 8) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int j = 0; j < k; ++j) {
-            if (c.idx[t * k + j] < 0) continue;
-            const float w = c.weight[t * k + j];
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.y + (int64_t)(t * k + j) * a.H + col));
-            v.x += w * y.x;
-            v.y += w * y.y;
-            v.z += w * y.z;
-            v.w += w * y.w;
+        uint2 r = make_uint2(0, 0);
+        if (a.residual) r = *reinterpret_cast<const uint2 *>(a.residual + t * a.H + col);
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            float4 in[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = t * k + j0 + j;
+                in[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < k && c.idx[at] >= 0) in[j] = __ldcg(reinterpret_cast<const float4 *>(y + at * a.H));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = t * k + j0 + j;
+                if (j0 + j < k && c.idx[at] >= 0) {
+                    const float w = c.weight[at];
+                    v.x += w * in[j].x;
+                    v.y += w * in[j].y;
+                    v.z += w * in[j].z;
+                    v.w += w * in[j].w;
+                }
+            }
         }
-        if (a.residual) {
-            const uint2 r = *reinterpret_cast<const uint2 *>(a.residual + t * a.H + col);
-            v.x += bf16_lo(r.x);
-            v.y += bf16_hi(r.x);
-            v.z += bf16_lo(r.y);
-            v.w += bf16_hi(r.y);
-        }
+        v.x += bf16_lo(r.x);
+        v.y += bf16_hi(r.x);
+        v.z += bf16_lo(r.y);
+        v.w += bf16_hi(r.y);
         *reinterpret_cast<uint2 *>(a.out + t * a.H + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
@@ -271,19 +283,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
     for (int e = threadIdx.x; e < E; e += kThreads) s.tokens[e] = 0;
-    if (threadIdx.x == kThreads - 1) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&bar.rows_full[i], kCopyThreads);   // the copies' own arrivals
-            mbar_init(&bar.boxes[i], 1);
-            mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.done[i], 2);        // the products' commit, word of the operands
+    if (warp == 15) {
+        if (lane < S) {
+            mbar_init(&bar.rows_full[lane], kCopyThreads);    // the copies' own arrivals
+            mbar_init(&bar.boxes[lane], 1);
+            mbar_init(&bar.full[lane], 1);
+            mbar_init(&bar.done[lane], 2);                    // the products' commit, word of the operands
+        } else if (lane >= 16) {
+            mbar_init(&bar.tempty[lane - 16], 8);
         }
-        for (int i = 0; i < accs; ++i) mbar_init(&bar.tempty[i], 8);
-        mbar_init(&bar.joined[0], UP ? 4 : 8);
-        mbar_init(&bar.joined[1], UP ? 4 : 1);
-        mbar_init(&bar.split[0], 8);
-        mbar_init(&bar.split[1], 1);
-        bar.gave_up = 0;
+        if (lane == 0) {
+            mbar_init(&bar.joined[0], UP ? 4 : 8);
+            mbar_init(&bar.joined[1], UP ? 4 : 1);
+            mbar_init(&bar.split[0], 8);
+            mbar_init(&bar.split[1], 1);
+            bar.gave_up = 0;
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 14) tmem_alloc<1>(&bar.tmem);
