@@ -212,6 +212,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const LinearUnit v = linear_unit(a, u);
             const int64_t r = (int64_t)v.row * kTile + rank * kPart + quarter * 32 + lane;
             const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
+            // the residual of 32 columns: asked for one step ahead of them
+            uint32_t res[16];
+            const auto ask = [&](int q) {
+                const int64_t c = c0 + q * 32;
+                const int n = (int)min(a.C - c, (int64_t)32);
+                if (a.residual && r < a.R && n > 0)
+                    load_bf16<32>(a.residual + r * a.residual_stride + c, res, n, a.residual_align);
+            };
+            ask(0);
             const auto finish = [&](int q, const uint32_t *t) {
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
@@ -233,7 +242,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) z[i] = activate(z[i], a.act);
                 }
-                if (a.residual) add_bf16(a.residual + r * a.residual_stride + c, z, n, a.residual_align);
+                if (a.residual) add_bf16<32>(res, z);
+                if (q + 1 < kChunks) ask(q + 1);
                 if (LONG)
                     store_fp32(reinterpret_cast<float *>(a.out) + v.split * a.split_stride + r * a.out_stride + c, z, n,
                                a.out_align);

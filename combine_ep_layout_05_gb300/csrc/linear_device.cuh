@@ -116,32 +116,49 @@ __device__ __forceinline__ void store_fp32(float *p, const float (&v)[N], int n,
         }
     }
 }
-// v += N consecutive bf16 of a row, as far as they exist
+// N consecutive bf16 of a row, as far as they exist (the rest are 0), two in a word
 template <int N>
-__device__ __forceinline__ void add_bf16(const uint16_t *p, float (&v)[N], int n, int align) {
+__device__ __forceinline__ void load_bf16(const uint16_t *p, uint32_t (&o)[N / 2], int n, int align) {
 #pragma unroll
-    for (int i = 0; i < N; i += 16) {
-        if (n - i >= 16 && align >= 16) {
-            const uint4 a = ld_stream(p + i), b = ld_stream(p + i + 8);
-            const uint32_t o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i + 2 * j] += bf16_lo(o[j]);
-                v[i + 2 * j + 1] += bf16_hi(o[j]);
-            }
+    for (int i = 0; i < N; i += 8) {
+        if (n - i >= 8 && align >= 16) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(p + i);   // (may be what the same thread overwrites later)
+            o[i / 2] = a.x;
+            o[i / 2 + 1] = a.y;
+            o[i / 2 + 2] = a.z;
+            o[i / 2 + 3] = a.w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (i + j < n) v[i + j] += __uint_as_float((uint32_t)p[i + j] << 16);
+            for (int j = 0; j < 8; j += 2)
+                o[(i + j) / 2] = (i + j < n ? p[i + j] : 0u) | (i + j + 1 < n ? (uint32_t)p[i + j + 1] << 16 : 0u);
         }
+    }
+}
+template <int N>
+__device__ __forceinline__ void add_bf16(const uint32_t (&o)[N / 2], float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        v[2 * j] += bf16_lo(o[j]);
+        v[2 * j + 1] += bf16_hi(o[j]);
     }
 }
 // v += N consecutive numbers of a vector (the same for every lane), as far as they exist
 template <int N>
 __device__ __forceinline__ void add_vector(const float *p, float (&v)[N], int n) {
+    if (n >= N && ((uintptr_t)p & 15) == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < n) v[i] += __ldg(p + i);
+        for (int i = 0; i < N; i += 4) {
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(p + i));
+            v[i] += b.x;
+            v[i + 1] += b.y;
+            v[i + 2] += b.z;
+            v[i + 3] += b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) v[i] += __ldg(p + i);
+    }
 }
 
 }  // namespace

@@ -207,41 +207,55 @@ __device__ __forceinline__ MoePart next_part(const S &s, int tiles, int chosen, 
     return v;
 }
 
-// out[t, columns of a tile] by the 256 accumulating threads: 4 columns a thread, a token a warp; eight rows of y are under
-// way together
+// out[t, columns of a tile] by the 256 accumulating threads: 4 columns a thread, two tokens a warp at a time; eight rows
+// of y of each are under way together
 template <bool UP>
 __device__ __forceinline__ void combine_tile(const MoeFewArgs &a, const MoeShared<UP> &c, int tile) {
-    const int thread = threadIdx.x - 256, col = tile * kBlock + (thread & 31) * 4, k = (int)a.route.k;
+    const int thread = threadIdx.x - 256, col = tile * kBlock + (thread & 31) * 4, k = (int)a.route.k, T = (int)a.route.T;
     const float *y = a.y + col;
-    for (int t = thread >> 5; t < (int)a.route.T; t += 8) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        uint2 r = make_uint2(0, 0);
-        if (a.residual) r = *reinterpret_cast<const uint2 *>(a.residual + t * a.H + col);
-        for (int j0 = 0; j0 < k; j0 += 8) {
-            float4 in[8];
+    for (int t0 = thread >> 5; t0 < T; t0 += 16) {
+        float4 v[2];
+        uint2 r[2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = t * k + j0 + j;
-                in[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j0 + j < k && c.idx[at] >= 0) in[j] = __ldcg(reinterpret_cast<const float4 *>(y + at * a.H));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = t * k + j0 + j;
-                if (j0 + j < k && c.idx[at] >= 0) {
-                    const float w = c.weight[at];
-                    v.x += w * in[j].x;
-                    v.y += w * in[j].y;
-                    v.z += w * in[j].z;
-                    v.w += w * in[j].w;
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 8 * i;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            r[i] = make_uint2(0, 0);
+            if (a.residual && t < T) r[i] = *reinterpret_cast<const uint2 *>(a.residual + t * a.H + col);
         }
-        v.x += bf16_lo(r.x);
-        v.y += bf16_hi(r.x);
-        v.z += bf16_lo(r.y);
-        v.w += bf16_hi(r.y);
-        *reinterpret_cast<uint2 *>(a.out + t * a.H + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            float4 in[2][8];
+            float w[2][8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = t0 + 8 * i, at = t * k + j0 + j;
+                    in[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[i][j] = 0.f;
+                    if (t < T && j0 + j < k && c.idx[at] >= 0) {
+                        in[i][j] = __ldcg(reinterpret_cast<const float4 *>(y + at * a.H));
+                        w[i][j] = c.weight[at];
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[i].x += w[i][j] * in[i][j].x;
+                    v[i].y += w[i][j] * in[i][j].y;
+                    v[i].z += w[i][j] * in[i][j].z;
+                    v[i].w += w[i][j] * in[i][j].w;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 8 * i;
+            if (t < T)
+                *reinterpret_cast<uint2 *>(a.out + t * a.H + col) =
+                    make_uint2(pack_bf16x2(v[i].x + bf16_lo(r[i].x), v[i].y + bf16_hi(r[i].x)),
+                               pack_bf16x2(v[i].z + bf16_lo(r[i].y), v[i].w + bf16_hi(r[i].y)));
+        }
     }
 }
 
