@@ -300,7 +300,8 @@ namespace {
 //
 // The CTAs of a cluster take, in us (measured from a graph, fitted to 16 to 128 rows of a tile, 2 to 112 steps and 1 to
 // 16 CTAs to a tile): each step 0.24 and 0.002 a row, little more where two CTAs share an SM, but not less than the memory;
-// the exchange of the parts 0.0015 a row and CTA of the cluster; each CTA 0.006 to start, and 5 in all.  Clusters of 16 find their places slowly: 128 of their
+// the exchange of the parts 0.0015 a row and CTA of the cluster; each CTA 0.006 to start, and 5 in all, which every turn of
+// the SMs costs again (32768 x 7168 of 64: 458 us here, 47 turns; some 105 by the other kernel).  Clusters of 16 find their places slowly: 128 of their
 // CTAs took 13.2 us for what 64 CTAs of clusters of 8 did in 11.9, 64 of them 10.4 against 11.7.
 FewPlan few_plan(int form, const LinearArgs &a, int &size, int64_t &tiles, double &time) {
     const bool swiglu = a.act == EP_ACT_SWIGLU;
@@ -329,8 +330,8 @@ FewPlan few_plan(int form, const LinearArgs &a, int &size, int64_t &tiles, doubl
         const double turns = (double)((ctas + 303) / 304);
         const double step = (0.24 + 0.002 * p.rows) * (ctas > 152 ? 1.05 : 1.0);
         const double bytes = 2.0 * a.L * (outs * (swiglu ? 2 : 1)) * p.col_tiles;
-        double t = 5.0 + 0.006 * std::min<int64_t>(ctas, 304) + 0.0015 * c * p.rows +
-                   std::max(turns * step * p.split_steps, bytes / 6.8e6);
+        const double start = 5.0 + 0.006 * std::min<int64_t>(ctas, 304) + 0.0015 * c * p.rows;
+        double t = turns * start + std::max(turns * step * p.split_steps, bytes / 6.8e6);
         // a longer chain would cost fp32 results digits
         if (a.out32 && p.chain > kChain) t += 1e6;
         if (t < time) {

@@ -222,6 +222,13 @@ def test_backward_tiles_of_rows(m, M, K, N, w32):
     check_backward(m, M, K, N, "swiglu", True, w32)
 
 
+@pytest.mark.parametrize("M,K,N", [(2500, 9000, 64), (2100, 8712, 200), (19500, 1040, 256), (2300, 9216, 33)])
+def test_backward_short_contractions(m, M, K, N):
+    """grad_x of a few outputs and many inputs: a part of the matrix stays in shared memory."""
+    check_backward(m, M, K, N, "none", False, False, which="x")
+    check_backward(m, M, K, N, "silu", True, False, which="x", gs=8)
+
+
 @pytest.mark.parametrize("which", ["x", "w", "b", "xw", "wb"])
 def test_backward_some_outputs(m, which):
     check_backward(m, 100, 128, 96, "none", False, True, which=which)
