@@ -306,3 +306,24 @@ def test_linear_on_another_stream_and_in_a_graph(m):
     got = [t.clone() for t in (out, pre, gx, gw, gb)]
     both()
     assert all(torch.equal(a, t) for a, t in zip(got, (out, pre, gx, gw, gb)))
+
+
+@pytest.mark.parametrize("M,K,N,act", [(300, 264, 200, "swiglu"), (2100, 1040, 64, "none"), (64, 1024, 700, "gelu")])
+def test_calls_behind_each_other_share_a_workspace(m, M, K, N, act):
+    """Gradients' launches begin before the ones in front of them end: many calls in a row on one workspace, each with
+    other inputs, give what each gives alone."""
+    x, w, _, rand, wide = make(M, K, N, act, 5)
+    gs = [rand(M, N).bfloat16() for _ in range(6)]
+    pre = None if act == "none" else rand(M, wide).bfloat16()
+    ws = torch.empty(m.ep_linear_backward_workspace_bytes(M, K, N, act), dtype=torch.uint8, device=DEV)
+    outs = lambda: (torch.empty_like(x), torch.empty(wide, K, device=DEV), torch.empty(wide, device=DEV))
+    want, got = [outs() for _ in gs], [outs() for _ in gs]
+    for g, o in zip(gs, want):
+        ws.fill_(255)
+        m.ep_linear_backward(g, x, w, *o, pre, act, ws)
+        torch.cuda.synchronize()
+    for _ in range(3):
+        for g, o in zip(gs, got):
+            m.ep_linear_backward(g, x, w, *o, pre, act, ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o, q in zip(want, got) for a, b in zip(o, q))

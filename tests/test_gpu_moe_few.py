@@ -216,3 +216,33 @@ def test_on_two_streams_at_once(m):
             x.run(s)
     torch.cuda.synchronize()
     assert all(torch.equal(x.out, w) for x, w in zip(layers, want))
+
+
+def test_calls_behind_each_other_share_a_workspace(m):
+    """The launches of a call begin before the ones in front of them end: many calls in a row on one workspace, each with
+    other inputs, give what each gives alone."""
+    layers = [Layer(m, 24, 48, 5, 384, 256, 11 + s) for s in range(5)]
+    want = []
+    for x in layers:
+        x.ws = layers[0].ws
+        want.append(x.run().clone())
+        torch.cuda.synchronize()
+    for _ in range(4):
+        for x in layers:
+            x.out.fill_(7)
+        for x in layers:
+            x.run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x.out, w) for x, w in zip(layers, want))
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 4, 2, 2048, 128), (40, 3, 2, 1536, 128), (7, 2, 1, 4096, 256), (16, 5, 2, 128, 2048)])
+def test_split_units(m, T, E, k, H, I):
+    """Few experts and long contractions: a unit of work is shared by several SMs."""
+    for seed in range(2):
+        layer = Layer(m, T, E, k, H, I, seed)
+        first = layer.run().clone()
+        assert m.ep_get_status(layer.status) == 0
+        layer.check()
+        for _ in range(5):
+            assert torch.equal(first, layer.run())
