@@ -251,20 +251,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_relaxed_cluster(tempty + acc * 8);
         };
         bool ok = true;
+        int stored = 0;                                         // boxes: they alternate by their number, not by the tile's
         for (int u = u0; u < units && ok; u += du) {
             const LinearUnit v = linear_unit<KEEP>(a, u);
             const int64_t r = (int64_t)v.row * kTile + rank * kPart + quarter * 32 + lane;
             const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
-            // the residual of 32 columns: asked for one step ahead of them
+            // the residual of 32 columns: where rows are aligned, asked for one step ahead of them
             uint32_t res[16];
             const auto ask = [&](int q) {
                 if (PLAIN) return;
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
-                if (a.residual && r < a.R && n > 0)
+                if (a.residual && a.residual_align >= 16 && r < a.R && n > 0)
                     load_bf16<32>(a.residual + r * a.residual_stride + c, res, n, a.residual_align);
             };
             ask(0);
+            const int64_t row0 = r - lane;                      // the warp's rows, and how many exist
+            const int n_rows = (int)min(max(a.R - row0, (int64_t)0), (int64_t)32);
             // Results leave through shared memory, in boxes of 32 rows x 128 bytes, where out can be a tensor map (each thread
             // storing 32 bytes a time along its row, a warp's store touches 32 lines: 32768 x 7168 of 256 took 115 us, 4.1
             // TB/s).  The swizzle keeps rows' 16 bytes apart.
@@ -273,60 +276,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const auto finish = [&](int q, const uint32_t *t) {
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
-                const bool live = r < a.R && n > 0;
-                unsigned char *rows = own + q / kHalves % kBoxes * kBoxBytes;
+                if (n <= 0) return;                             // (for the whole warp)
+                const bool live = r < a.R;
+                unsigned char *rows = own + stored % kBoxes * kBoxBytes;
                 if (a.boxes && q % kHalves == 0) {
                     if (lane == 0) bulk_wait_read<kBoxes - 1>(); // (what was in this box has been read)
                     __syncwarp();
                 }
-                if (live) {
-                    float z[32];
+                float z[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(t[i]);
-                    if (!PLAIN && a.bias) add_vector(a.bias + c, z, n);
-                    if (!PLAIN && a.pre) store_bf16(a.pre + r * a.pre_stride + c, z, n, a.pre_align);
+                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(t[i]);
+                if (!PLAIN) {
+                    // bf16 pre-activations, as far as they are wanted
+                    const auto keep = [&](const float(&v)[32], int64_t at) {
+                        if (!a.pre) return;
+                        if (a.pre_align >= 16) {
+                            if (live) store_bf16(a.pre + r * a.pre_stride + at, v, n, a.pre_align);
+                        } else {
+                            put_row(own, v);
+                            copy_out(own, a.pre + row0 * a.pre_stride + at, a.pre_stride, n_rows, n);
+                        }
+                    };
+                    if (a.bias) add_vector(a.bias + c, z, n);
+                    keep(z, c);
                     if (SWIGLU) {
                         float up[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(t[kWide - 32 + i]);
                         if (a.bias) add_vector(a.bias + a.C + c, up, n);
-                        if (a.pre) store_bf16(a.pre + r * a.pre_stride + a.C + c, up, n, a.pre_align);
+                        keep(up, a.C + c);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) z[i] = swiglu(z[i], up[i]);
-                    } else if (!PLAIN && a.act != EP_ACT_NONE) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) z[i] = activate(z[i], a.act);
-                    }
-                    if (!PLAIN && a.residual) add_bf16<32>(res, z);
-                    if (q + 1 < kChunks) ask(q + 1);
-                    if (a.boxes) {
-                        uint4 *to = reinterpret_cast<uint4 *>(rows + lane * 128);
-#pragma unroll
-                        for (int i = 0; i < (LONG ? 8 : 4); ++i) {
-                            const int at = (LONG ? i : q % kHalves * 4 + i) ^ (lane & 7);
-                            if (LONG)
-                                to[at] = make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]),
-                                                    __float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3]));
-                            else
-                                to[at] = make_uint4(pack_bf16x2(z[8 * i % 32], z[(8 * i + 1) % 32]),
-                                                    pack_bf16x2(z[(8 * i + 2) % 32], z[(8 * i + 3) % 32]),
-                                                    pack_bf16x2(z[(8 * i + 4) % 32], z[(8 * i + 5) % 32]),
-                                                    pack_bf16x2(z[(8 * i + 6) % 32], z[(8 * i + 7) % 32]));
-                        }
-                    } else if (LONG) {
-                        store_fp32(reinterpret_cast<float *>(a.out) + v.split * a.split_stride + r * a.out_stride + c, z, n,
-                                   a.out_align);
                     } else {
-                        store_bf16(reinterpret_cast<uint16_t *>(a.out) + r * a.out_stride + c, z, n, a.out_align);
+                        activate(z, a.act);
+                    }
+                    if (a.residual) {
+                        if (a.residual_align < 16)
+                            copy_in(own, a.residual + row0 * a.residual_stride + c, a.residual_stride, n_rows, n, res);
+                        if (live) add_bf16<32>(res, z);
+                        if (q + 1 < kChunks) ask(q + 1);
                     }
                 }
-                if (a.boxes && q % kHalves == kHalves - 1) {
-                    fence_async_shared();
-                    __syncwarp();
-                    const int64_t first = c0 + (q - (kHalves - 1)) * 32, row = r - lane;
-                    if (lane == 0 && first < a.C && row < a.R) {
-                        tma_store_3d(&maps.out, (int)first * (LONG ? 4 : 2), (int)row, v.split, rows);
-                        bulk_commit();
+                if (a.boxes) {
+                    uint4 *to = reinterpret_cast<uint4 *>(rows + lane * 128);
+#pragma unroll
+                    for (int i = 0; i < (LONG ? 8 : 4); ++i) {
+                        const int at = (LONG ? i : q % kHalves * 4 + i) ^ (lane & 7);
+                        if (LONG)
+                            to[at] = make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]),
+                                                __float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3]));
+                        else
+                            to[at] = make_uint4(pack_bf16x2(z[8 * i % 32], z[(8 * i + 1) % 32]),
+                                                pack_bf16x2(z[(8 * i + 2) % 32], z[(8 * i + 3) % 32]),
+                                                pack_bf16x2(z[(8 * i + 4) % 32], z[(8 * i + 5) % 32]),
+                                                pack_bf16x2(z[(8 * i + 6) % 32], z[(8 * i + 7) % 32]));
+                    }
+                    if (q % kHalves == kHalves - 1 || a.C - c <= 32) {
+                        fence_async_shared();
+                        __syncwarp();
+                        stored += n_rows > 0;
+                        if (lane == 0 && n_rows > 0) {
+                            tma_store_3d(&maps.out, (int)(c - q % kHalves * 32) * (LONG ? 4 : 2), (int)row0, v.split, rows);
+                            bulk_commit();
+                        }
+                    }
+                } else if (LONG) {
+                    float *out = reinterpret_cast<float *>(a.out) + v.split * a.split_stride;
+                    if (a.out_align >= 16) {
+                        if (live) store_fp32(out + r * a.out_stride + c, z, n, a.out_align);
+                    } else {
+                        put_row_fp32(rows, z);
+                        copy_out_fp32(rows, out + row0 * a.out_stride + c, a.out_stride, n_rows, n);
+                    }
+                } else {
+                    uint16_t *out = reinterpret_cast<uint16_t *>(a.out);
+                    if (a.out_align >= 16) {
+                        if (live) store_bf16(out + r * a.out_stride + c, z, n, a.out_align);
+                    } else {
+                        put_row(rows, z);
+                        copy_out(rows, out + row0 * a.out_stride + c, a.out_stride, n_rows, n);
                     }
                 }
             };
@@ -449,7 +477,9 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
     if (cudaError_t e = operand_map(B, form != kFormForward, &maps.b)) return e;
     // (rows and their strides in multiples of 16 bytes; the parts of a split contraction are its third dimension)
     const int64_t size = a.out32 ? 4 : 2, stride = a.out_stride * size, part = (a.splits > 1 ? a.split_stride : a.out_stride) * size;
-    a.boxes = a.out_align >= 16 && a.C * size % 16 == 0 && stride < (int64_t)1 << 40 && part < (int64_t)1 << 40;
+    // (not where the pre-activations or the residual need that memory)
+    a.boxes = a.out_align >= 16 && a.C * size % 16 == 0 && stride < (int64_t)1 << 40 && part < (int64_t)1 << 40 &&
+              !(a.pre && a.pre_align < 16) && !(a.residual && a.residual_align < 16);
     maps.out = maps.a;
     if (a.boxes) {
         const cuuint64_t dims[3] = {(cuuint64_t)(a.C * size), (cuuint64_t)a.R, (cuuint64_t)a.splits};

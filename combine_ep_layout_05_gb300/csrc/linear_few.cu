@@ -238,8 +238,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 store4(pre, z, n, a.pre_align >= 16);
                 if (SWIGLU) store4(pre + a.C, up, n, a.pre_align >= 16);
             }
+            if (SWIGLU) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = SWIGLU ? swiglu(z[j], up[j]) : activate(z[j], a.act);
+                for (int j = 0; j < 4; ++j) z[j] = swiglu(z[j], up[j]);
+            } else {
+                activate(z, a.act);
+            }
             if (a.residual) {
                 const uint16_t *res = a.residual + m * a.residual_stride + c;
                 if (n >= 4 && a.residual_align >= 16) {

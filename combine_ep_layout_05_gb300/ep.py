@@ -545,45 +545,55 @@ _F16, _F32 = (torch.bfloat16,), (torch.float32,)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _rows(t, name, rows, cols, dtypes=_F16):
-    """(pointer, row stride) of a [rows, cols] tensor whose rows are contiguous (any row stride); None: (None, 0)."""
-    if t is None:
-        return None, 0
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == (rows, cols):
-        stride, step = t.stride()
-        if rows <= 1:
-            stride = cols
-        if (step == 1 or cols <= 1) and stride >= cols:
-            return t.data_ptr(), stride
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+def _refuse(t, name, shape, dtypes, dev):
+    """Raises what is wrong with a tensor that should have this shape, dtype and device and rows without gaps."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous" if len(shape) != 2 else f"{name} must have contiguous rows that do not overlap")
 
 
-def _shaped(t, name, shape, dtypes):
-    """Pointer of a contiguous tensor of this shape (None: None)."""
+def _rows(t, name, rows, cols, dev, dtypes=_F16):
+    """(pointer, row stride) of a [rows, cols] tensor on device dev whose rows are contiguous (any row stride); None:
+    (None, 0)."""
+    if t is None:
+        return None, 0
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (rows, cols) and t.get_device() == dev:
+        stride, step = t.stride()
+        if rows <= 1:
+            stride = cols
+        if (step == 1 or cols <= 1) and stride >= cols:
+            return t.data_ptr(), stride
+    _refuse(t, name, (rows, cols), dtypes, dev)
+
+
+def _shaped(t, name, shape, dtypes, dev):
+    """Pointer of a contiguous tensor of this shape on device dev (None: None)."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
         return t.data_ptr()
-    if not isinstance(t, torch.Tensor) or t.shape != shape:
-        raise ValueError(f"{name} must be a tensor {list(shape)}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    return _ptr(t, None, name)
+    _refuse(t, name, shape, dtypes, dev)
 
 
-def _stream_here(stream, *tensors):
-    """Handle of the stream.  The library launches on the current device: the stream and every tensor have to be there."""
-    dev = _current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+def _buffer(t, name, dtype, numel, dev):
+    """Pointer of a contiguous tensor of at least numel elements on device dev (None: None)."""
+    ptr = _ptr(t, dtype, name, numel)
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return ptr
+
+
+def _stream_here(stream, dev):
+    """Handle of the stream.  The library launches on the current device: the stream has to be there."""
     if stream is None:
         return _raw_stream(dev)
     if isinstance(stream, torch.cuda.Stream):
@@ -591,6 +601,13 @@ def _stream_here(stream, *tensors):
             raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{dev}")
         return stream.cuda_stream
     return int(stream)
+
+
+def _device_of(t, name):
+    """The current device, where the library launches, if t is a CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _current_device()
 
 
 def _linear_sizes(x, w, activation):
@@ -613,15 +630,16 @@ def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "
     """out [M, N] (bf16 or fp32) = act(x [M, K] @ w.T + bias) + residual; w [N, K], with "swiglu" [2 N, K] (gate rows
     first), bias fp32, residual [M, N] bf16 (may be out itself), pre [M, w's rows] bf16 receives the pre-activations."""
     M, K, N, wide = _linear_sizes(x, w, activation)
-    xp, xs = _rows(x, "x", M, K)
-    op, os_ = _rows(out, "out", M, N, _F16 + _F32)
-    rp, rs = _rows(residual, "residual", M, N)
+    dev = _device_of(x, "x")
     if out is None:
         raise ValueError("out must be a tensor")
-    args = (M, K, N, ACTIVATIONS[activation], xp, xs, _shaped(w, "w", (wide, K), _F16),
-            _shaped(bias, "bias", (wide,), _F32), rp, rs, EP_FP32 if out.dtype == torch.float32 else EP_BF16, op, os_,
-            _shaped(pre, "pre", (M, wide), _F16), _ptr(dev_status, torch.int32, "dev_status", 1),
-            _stream_here(stream, x, w, out, bias, residual, pre, dev_status))
+    xp, xs = _rows(x, "x", M, K, dev)
+    op, os_ = _rows(out, "out", M, N, dev, _F16 + _F32)
+    rp, rs = _rows(residual, "residual", M, N, dev)
+    args = (M, K, N, ACTIVATIONS[activation], xp, xs, _shaped(w, "w", (wide, K), _F16, dev),
+            _shaped(bias, "bias", (wide,), _F32, dev), rp, rs, EP_FP32 if out.dtype == torch.float32 else EP_BF16, op, os_,
+            _shaped(pre, "pre", (M, wide), _F16, dev), _buffer(dev_status, "dev_status", torch.int32, 1, dev),
+            _stream_here(stream, dev))
     return _call("ep_linear", _lib.ep_linear, args)
 
 
@@ -635,18 +653,18 @@ def ep_linear_backward(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None,
     and grad_bias fp32, each left out if None; pre as ep_linear wrote it (not needed for "none"); workspace uint8 of
     ep_linear_backward_workspace_bytes()."""
     M, K, N, wide = _linear_sizes(x, w, activation)
-    xp, xs = _rows(x, "x", M, K)
-    gp, gs = _rows(grad_out, "grad_out", M, N, _F16 + _F32)
-    gxp, gxs = _rows(grad_x, "grad_x", M, K)
+    dev = _device_of(x, "x")
     if grad_out is None:
         raise ValueError("grad_out must be a tensor")
+    xp, xs = _rows(x, "x", M, K, dev)
+    gp, gs = _rows(grad_out, "grad_out", M, N, dev, _F16 + _F32)
+    gxp, gxs = _rows(grad_x, "grad_x", M, K, dev)
     code = lambda t: EP_FP32 if t is not None and t.dtype == torch.float32 else EP_BF16
-    args = (M, K, N, ACTIVATIONS[activation], code(grad_out), gp, gs, xp, xs, _shaped(w, "w", (wide, K), _F16),
-            _shaped(pre, "pre", (M, wide), _F16), gxp, gxs, code(grad_w),
-            _shaped(grad_w, "grad_w", (wide, K), _F16 + _F32), _shaped(grad_bias, "grad_bias", (wide,), _F32),
-            _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
-            _ptr(dev_status, torch.int32, "dev_status", 1),
-            _stream_here(stream, grad_out, x, w, grad_x, grad_w, grad_bias, pre, workspace, dev_status))
+    args = (M, K, N, ACTIVATIONS[activation], code(grad_out), gp, gs, xp, xs, _shaped(w, "w", (wide, K), _F16, dev),
+            _shaped(pre, "pre", (M, wide), _F16, dev), gxp, gxs, code(grad_w),
+            _shaped(grad_w, "grad_w", (wide, K), _F16 + _F32, dev), _shaped(grad_bias, "grad_bias", (wide,), _F32, dev),
+            _buffer(workspace, "workspace", torch.uint8, None, dev), workspace.numel() if workspace is not None else 0,
+            _buffer(dev_status, "dev_status", torch.int32, 1, dev), _stream_here(stream, dev))
     return _call("ep_linear_backward", _lib.ep_linear_backward, args)
 
 
@@ -664,19 +682,19 @@ def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_sc
     I = N // 2
     if N % 256 or K != H or H % 128:
         raise ValueError(f"gate_up must be [{E}, 2 I, {H}], H and I multiples of 128, got {list(gate_up.shape)}")
-    u8, f32, bf16 = (torch.uint8,), _F32, _F16
+    dev, u8 = _device_of(x, "x"), (torch.uint8,)
     ptr, stride, dt = _logits(logits, p, "logits")
-    args = (ctypes.byref(p), ctypes.byref(r), I, _shaped(x, "x", (T, H), bf16), dt, ptr, stride,
-            _ptr(bias, torch.float32, "bias", E), _shaped(gate_up, "gate_up", (E, N, H), u8),
-            _shaped(gate_up_scales, "gate_up_scales", (E, N // 128, H // 128), f32),
-            _shaped(down, "down", (E, H, I), u8),
-            _shaped(down_scales, "down_scales", (E, H // 128, I // 128), f32),
-            _shaped(residual, "residual", (T, H), bf16), _shaped(out, "out", (T, H), bf16),
-            _ptr(topk_idx, torch.int64, "topk_idx", n), _ptr(topk_weights, torch.float32, "topk_weights", n),
-            _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
-            _ptr(dev_status, torch.int32, "dev_status", 1),
-            _stream_here(stream, x, logits, bias, gate_up, gate_up_scales, down, down_scales, residual, out, topk_idx,
-                         topk_weights, workspace, dev_status))
+    if logits.get_device() != dev:
+        raise ValueError(f"logits is on {logits.device}, the current device is cuda:{dev}")
+    args = (ctypes.byref(p), ctypes.byref(r), I, _shaped(x, "x", (T, H), _F16, dev), dt, ptr, stride,
+            _buffer(bias, "bias", torch.float32, E, dev), _shaped(gate_up, "gate_up", (E, N, H), u8, dev),
+            _shaped(gate_up_scales, "gate_up_scales", (E, N // 128, H // 128), _F32, dev),
+            _shaped(down, "down", (E, H, I), u8, dev),
+            _shaped(down_scales, "down_scales", (E, H // 128, I // 128), _F32, dev),
+            _shaped(residual, "residual", (T, H), _F16, dev), _shaped(out, "out", (T, H), _F16, dev),
+            _buffer(topk_idx, "topk_idx", torch.int64, n, dev), _buffer(topk_weights, "topk_weights", torch.float32, n, dev),
+            _buffer(workspace, "workspace", torch.uint8, None, dev), workspace.numel() if workspace is not None else 0,
+            _buffer(dev_status, "dev_status", torch.int32, 1, dev), _stream_here(stream, dev))
     return _call("ep_moe_few", _lib.ep_moe_few, args)
 
 

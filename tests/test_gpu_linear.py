@@ -93,7 +93,8 @@ def check_forward(m, M, K, N, act, bias, residual, out32, pre, xs=0, extra=0, se
 
 
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("M,K,N", [(1, 64, 8), (3, 8, 1), (40, 200, 77), (130, 136, 300), (257, 512, 129), (600, 72, 515)])
+@pytest.mark.parametrize("M,K,N", [(1, 64, 8), (3, 8, 1), (40, 200, 77), (130, 136, 300), (257, 512, 129), (600, 72, 515),
+                                   (1500, 64, 1030), (1300, 136, 1807), (1400, 200, 1284)])
 def test_linear(m, act, M, K, N):
     check_forward(m, M, K, N, act, True, True, False, True)
     check_forward(m, M, K, N, act, False, False, True, False, seed=1)
