@@ -24,7 +24,6 @@
 // products (first CTA), 4 to 11 the epilogue: a thread owns a row of a half of
 // the columns.
 #include <algorithm>
-#include <cstddef>
 
 #include "linear_device.cuh"
 
@@ -33,10 +32,8 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kStages = 6;                      // 192 KB of operands; KEEP: 64 KB of B that stay, and
-constexpr int kKeepStages = 6, kKept = 4;       // A's parts of 16 KB; the most steps whose B stays
+constexpr int kStages = 6;                      // 192 KB of operands
 constexpr int kTile = 2 * kPart;                // rows and columns of a pair's tile
-constexpr int kKeepRows = 8;                    // least row tiles for KEEP: a new B waits for the products with the last
 constexpr int kSegment = 8;                     // steps of a LONG sum that stay in tensor memory
 constexpr int kIssueRegs = 88, kEndRegs = 208;  // LONG: 88 + 2 * 208 = 3 * 168, the launch's registers
 constexpr int kGroup = 8;                       // row tiles that are walked together, for L2
@@ -44,9 +41,8 @@ constexpr int kGroup = 8;                       // row tiles that are walked tog
 struct LinearShared {
     unsigned char buf[kStages][2 * kPartBytes];  // A, then B
     unsigned char rows[8][32 * 128];            // a warp's results on their way out: 32 rows of 128 bytes
-    uint64_t full[kKeepStages];                 // (the first CTA's) both CTAs' operands
-    uint64_t empty[kKeepStages];                // a step's products are done
-    uint64_t kept, used;                        // KEEP: B is there (the first CTA's); a column tile's products are done
+    uint64_t full[kStages];                     // (the first CTA's) both CTAs' operands
+    uint64_t empty[kStages];                    // a step's products are done
     uint64_t tfull[2];                          // an accumulator is complete
     uint64_t tempty[2];                         // (the first CTA's) taken out by both CTAs
     uint32_t tmem;
@@ -61,9 +57,7 @@ struct LinearMaps {
 struct LinearUnit {
     int row, col, split, first, last;           // tile, part, steps [first, last)
 };
-template <bool KEEP>
 __device__ __forceinline__ LinearUnit linear_unit(const LinearArgs &a, int u) {
-    if (KEEP) return LinearUnit{u % a.row_tiles, u / a.row_tiles, 0, 0, a.steps};
     const int tiles = a.row_tiles * a.col_tiles;
     LinearUnit v;
     v.split = u / tiles;
@@ -77,27 +71,17 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearArgs &a, int u) {
 }
 
 // LONG: fp32 results.  Their sums are taken out of tensor memory every kSegment steps and added in registers.
-// KEEP: for short contractions and many tiles.  A pair has a run of row tiles of one column tile after the other, and
-// that column tile's B stays in shared memory: otherwise each tile of 4 steps brings 256 KB through L2 for 128 KB
-// of results.
-template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG, bool KEEP>
+template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ LinearMaps maps) {
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
     LinearShared &s = *reinterpret_cast<LinearShared *>(raw);
-    constexpr int S = KEEP ? kKeepStages : kStages, kStageBytes = KEEP ? kPartBytes : 2 * kPartBytes;
-    unsigned char *ring = s.buf[0] + (KEEP ? kKept * kPartBytes : 0);
-    static_assert(offsetof(LinearShared, full) % 8 == 0, "");
-    // results on their way out: a warp's boxes (KEEP: two, behind the operands' 160 KB)
-    constexpr int kBoxes = KEEP ? 2 : 1, kBoxBytes = sizeof(s.rows[0]);
-    static_assert((kKept + kKeepStages) * kPartBytes + 8 * 2 * kBoxBytes <= offsetof(LinearShared, full), "");
+    constexpr int S = kStages, kStageBytes = sizeof(s.buf[0]);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int64_t all = (int64_t)a.row_tiles * a.col_tiles * a.splits;     // (below 2^31: checked on the host)
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    // units of this pair: every so many, or a run
-    const int u0 = KEEP ? (int)(all * pair / pairs) : pair, du = KEEP ? 1 : pairs;
-    const int units = KEEP ? (int)(all * (pair + 1) / pairs) : (int)all;
+    const int units = (int)all;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
@@ -108,8 +92,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&s.tfull[i], 1);
             mbar_init(&s.tempty[i], 16);
         }
-        mbar_init(&s.kept, 1);
-        mbar_init(&s.used, 1);
         s.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -127,34 +109,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---- boxes ----
         if (lane == 0) {
-            const uint32_t full = cluster_addr(&s.full[0], 0), kept = cluster_addr(&s.kept, 0);
-            int st = 0, ph = 1, it = 0, held = -1, columns = 0;
+            const uint32_t full = cluster_addr(&s.full[0], 0);
+            int st = 0, ph = 1, it = 0;
             bool ok = true;
-            const auto load_b = [&](unsigned char *pb, int k, int c0, uint32_t bar) {
-                if (B_MN) {
-                    tma_load_2d_pair(pb, &maps.b, c0 * 2, k * kStep, bar);
-                    tma_load_2d_pair(pb + kPartBytes / 2, &maps.b, c0 * 2 + 128, k * kStep, bar);
-                } else {
-                    tma_load_2d_pair(pb, &maps.b, k * kStep * 2, c0, bar);
-                }
-            };
-            for (int u = u0; u < units && ok; u += du) {
-                const LinearUnit v = linear_unit<KEEP>(a, u);
+            for (int u = pair; u < units && ok; u += pairs) {
+                const LinearUnit v = linear_unit(a, u);
                 const int r0 = v.row * kTile + rank * kPart;
                 const int c0 = SWIGLU ? rank * (int)a.C + v.col * kPart : v.col * kTile + rank * kPart;
-                if (KEEP && v.col != held) {
-                    ok = columns == 0 || mbar_wait(&s.used, (columns - 1) & 1, patience);
-                    if (!ok) break;
-                    if (rank == 0) mbar_expect_tx(&s.kept, a.steps * 2 * kPartBytes);
-                    for (int k = 0; k < a.steps; ++k) load_b(s.buf[0] + k * kPartBytes, k, c0, kept);
-                    held = v.col;
-                    ++columns;
-                }
                 for (int k = v.first; k < v.last; ++k, ++it) {
                     ok = mbar_wait(&s.empty[st], ph, patience);
                     if (!ok) break;
                     if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kStageBytes);
-                    unsigned char *pa = ring + st * kStageBytes;
+                    unsigned char *pa = s.buf[st];
                     const uint32_t bar = full + st * 8;
                     if (A_MN) {
                         tma_load_2d_pair(pa, &maps.a, r0 * 2, k * kStep, bar);
@@ -162,11 +128,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else {
                         tma_load_2d_pair(pa, &maps.a, k * kStep * 2, r0, bar);
                     }
-                    if (!KEEP) load_b(pa + kPartBytes, k, c0, bar);
+                    unsigned char *pb = pa + kPartBytes;
+                    if (B_MN) {
+                        tma_load_2d_pair(pb, &maps.b, c0 * 2, k * kStep, bar);
+                        tma_load_2d_pair(pb + kPartBytes / 2, &maps.b, c0 * 2 + 128, k * kStep, bar);
+                    } else {
+                        tma_load_2d_pair(pb, &maps.b, k * kStep * 2, c0, bar);
+                    }
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
             }
-            // the products of a step follow its boxes, and a kept B's
+            // the products of a step follow its boxes
             drain<S>(s.empty, it);
         }
         __syncwarp();
@@ -175,21 +147,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             constexpr uint32_t idesc = mma_idesc_bf16(kTile, kTile, A_MN, B_MN);
             const bool issue = elect_one();
-            const unsigned char *b0 = KEEP ? s.buf[0] : ring + kPartBytes;
-            const uint64_t da0 = A_MN ? smem_desc_mn(ring, kPartBytes / 2) : smem_desc(ring);
-            const uint64_t db0 = B_MN ? smem_desc_mn(b0, kPartBytes / 2) : smem_desc(b0);
+            const uint64_t da0 = A_MN ? smem_desc_mn(s.buf[0], kPartBytes / 2) : smem_desc(s.buf[0]);
+            const uint64_t db0 = B_MN ? smem_desc_mn(s.buf[0] + kPartBytes, kPartBytes / 2) : smem_desc(s.buf[0] + kPartBytes);
             // 16 of the contraction: 32 bytes along a row, or 16 lines of 128 bytes
             constexpr uint32_t ka = A_MN ? 2048 >> 4 : 32 >> 4, kb = B_MN ? 2048 >> 4 : 32 >> 4;
-            int st = 0, ph = 0, acc = 0, aph = 1, held = -1, columns = 0;
+            int st = 0, ph = 0, acc = 0, aph = 1;
             bool ok = true;
-            for (int u = u0; u < units && ok; u += du) {
-                const LinearUnit v = linear_unit<KEEP>(a, u);
-                if (KEEP && v.col != held) {
-                    ok = warp_wait<true>(&s.kept, columns & 1, patience);
-                    if (!ok) break;
-                    held = v.col;
-                    ++columns;
-                }
+            for (int u = pair; u < units && ok; u += pairs) {
+                const LinearUnit v = linear_unit(a, u);
                 for (int k0 = v.first; k0 < v.last && ok;) {
                     const int k1 = LONG ? min(k0 + kSegment, v.last) : v.last;
                     ok = warp_wait<true>(&s.tempty[acc], aph, patience);
@@ -202,10 +167,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_fence_after();
                         if (issue) {
                             const uint32_t at = (uint32_t)(st * (kStageBytes >> 4));
-                            const uint32_t bt = KEEP ? (uint32_t)(k * (kPartBytes >> 4)) : at;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                mma_bf16<2>(tmem + acc * kTile, da0 + at + i * ka, db0 + bt + i * kb, idesc,
+                                mma_bf16<2>(tmem + acc * kTile, da0 + at + i * ka, db0 + at + i * kb, idesc,
                                             k > k0 || i > 0);
                             mma_commit<2>(&s.empty[st]);
                         }
@@ -217,7 +181,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     aph ^= acc == 0;
                     k0 = k1;
                 }
-                if (KEEP && ok && issue && u + 1 < units && (u + 1) / a.row_tiles != held) mma_commit<2>(&s.used);
             }
         }
         __syncwarp();
@@ -251,9 +214,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_relaxed_cluster(tempty + acc * 8);
         };
         bool ok = true;
-        int stored = 0;                                         // boxes: they alternate by their number, not by the tile's
-        for (int u = u0; u < units && ok; u += du) {
-            const LinearUnit v = linear_unit<KEEP>(a, u);
+        for (int u = pair; u < units && ok; u += pairs) {
+            const LinearUnit v = linear_unit(a, u);
             const int64_t r = (int64_t)v.row * kTile + rank * kPart + quarter * 32 + lane;
             const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
             // the residual of 32 columns: where rows are aligned, asked for one step ahead of them
@@ -271,16 +233,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // Results leave through shared memory, in boxes of 32 rows x 128 bytes, where out can be a tensor map (each thread
             // storing 32 bytes a time along its row, a warp's store touches 32 lines: 32768 x 7168 of 256 took 115 us, 4.1
             // TB/s).  The swizzle keeps rows' 16 bytes apart.
-            unsigned char *own = KEEP ? s.buf[0] + (kKept + kKeepStages) * kPartBytes + (warp - 4) * 2 * kBoxBytes : s.rows[warp - 4];
+            unsigned char *own = s.rows[warp - 4];
             constexpr int kHalves = LONG ? 1 : 2;               // chunks of 32 columns in a box
             const auto finish = [&](int q, const uint32_t *t) {
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
                 if (n <= 0) return;                             // (for the whole warp)
                 const bool live = r < a.R;
-                unsigned char *rows = own + stored % kBoxes * kBoxBytes;
                 if (a.boxes && q % kHalves == 0) {
-                    if (lane == 0) bulk_wait_read<kBoxes - 1>(); // (what was in this box has been read)
+                    if (lane == 0) bulk_wait_read<0>();       // (what was in this box has been read)
                     __syncwarp();
                 }
                 float z[32];
@@ -318,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (a.boxes) {
-                    uint4 *to = reinterpret_cast<uint4 *>(rows + lane * 128);
+                    uint4 *to = reinterpret_cast<uint4 *>(own + lane * 128);
 #pragma unroll
                     for (int i = 0; i < (LONG ? 8 : 4); ++i) {
                         const int at = (LONG ? i : q % kHalves * 4 + i) ^ (lane & 7);
@@ -334,9 +295,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (q % kHalves == kHalves - 1 || a.C - c <= 32) {
                         fence_async_shared();
                         __syncwarp();
-                        stored += n_rows > 0;
                         if (lane == 0 && n_rows > 0) {
-                            tma_store_3d(&maps.out, (int)(c - q % kHalves * 32) * (LONG ? 4 : 2), (int)row0, v.split, rows);
+                            tma_store_3d(&maps.out, (int)(c - q % kHalves * 32) * (LONG ? 4 : 2), (int)row0, v.split, own);
                             bulk_commit();
                         }
                     }
@@ -345,16 +305,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (a.out_align >= 16) {
                         if (live) store_fp32(out + r * a.out_stride + c, z, n, a.out_align);
                     } else {
-                        put_row_fp32(rows, z);
-                        copy_out_fp32(rows, out + row0 * a.out_stride + c, a.out_stride, n_rows, n);
+                        put_row_fp32(own, z);
+                        copy_out_fp32(own, out + row0 * a.out_stride + c, a.out_stride, n_rows, n);
                     }
                 } else {
                     uint16_t *out = reinterpret_cast<uint16_t *>(a.out);
                     if (a.out_align >= 16) {
                         if (live) store_bf16(out + r * a.out_stride + c, z, n, a.out_align);
                     } else {
-                        put_row(rows, z);
-                        copy_out(rows, out + row0 * a.out_stride + c, a.out_stride, n_rows, n);
+                        put_row(own, z);
+                        copy_out(own, out + row0 * a.out_stride + c, a.out_stride, n_rows, n);
                     }
                 }
             };
@@ -420,24 +380,24 @@ cudaError_t operand_map(const LinearOperand &o, bool mn, CUtensorMap *map) {
     return encode_map(map, 2, o.p, dims, strides, box);
 }
 
-template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG, bool KEEP = false>
+template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG>
 cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st) {
     constexpr int bytes = sizeof(LinearShared);
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
     cached_per_device(ready, [&](int) {
-        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN, LONG, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         // the warpgroups' register shares are drawn from what the block was launched with
         cudaFuncAttributes f{};
-        if (!e) e = cudaFuncGetAttributes(&f, linear_kernel<SWIGLU, A_MN, B_MN, LONG, KEEP>);
+        if (!e) e = cudaFuncGetAttributes(&f, linear_kernel<SWIGLU, A_MN, B_MN, LONG>);
         if (!e && LONG && f.numRegs * 3 < kIssueRegs + 2 * kEndRegs) e = cudaErrorInvalidDeviceFunction;
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
     const int64_t units = (int64_t)a.row_tiles * a.col_tiles * a.splits;
     const int grid = (int)std::min<int64_t>(num_sms() & ~1, 2 * units);
-    return launch_in_order(a.order, linear_kernel<SWIGLU, A_MN, B_MN, LONG, KEEP>, dim3(grid), kThreads, bytes, 0, st, a, maps);
+    return launch_in_order(a.order, linear_kernel<SWIGLU, A_MN, B_MN, LONG>, dim3(grid), kThreads, bytes, 0, st, a, maps);
 }
 
 }  // namespace
@@ -445,6 +405,10 @@ cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st)
 // What a launch of this kernel takes, in us, fitted to measurements from a graph: 28 tiles of 4, 16, 32 and 112 steps
 // 7.1, 11.1, 15.4 and 36.8 us; 84 tiles of 32 steps 25.0; 3584 of 4 steps 106 (there the epilogue is what takes the
 // time, 2.2 us a tile).  A split contraction adds the parts' sum: their bytes at 5 TB/s and a launch.
+// The shorter of this and linear_few_time() says which kernel a call takes.  Each forced, in us (few rows' kernel |
+// this one), forward: 7168 -> 256 at 32, 512, 4096 rows 7.4 | 35, 10.8 | 36, 20.8 | 36; 7168 -> 2048 with SwiGLU at 1, 512,
+// 1024, 4096 rows 11.5 | 36, 32 | 37, 53 | 40, 207 | 140; 2048 -> 7168 at 128, 256, 512 rows 12.0 | 14.9, 15.2 | 15.0, 21.7 |
+// 15.6.  grad_x of 2048 -> 1024 at 515 and 2048 rows 10.8 | 9.9, 17.3 | 10.3; grad_w 10.6 | 9.3, 17.0 | 15.7.
 double linear_time(int64_t R, int64_t C, int64_t L, bool swiglu, int splits) {
     const int64_t cols = swiglu ? kPart : kTile, tiles = ((R + kTile - 1) / kTile) * ((C + cols - 1) / cols);
     const int64_t steps = ((L + kStep - 1) / kStep + splits - 1) / splits, turns = (tiles * splits + 75) / 76;
@@ -487,9 +451,6 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
         const cuuint32_t box[3] = {128, 32, 1};
         if (cudaError_t e = encode_map(&maps.out, 3, a.out, dims, strides, box)) return e;
     }
-    if (form == kFormGradX && !a.out32 && a.steps <= kKept && a.row_tiles >= kKeepRows &&
-        (int64_t)a.row_tiles * a.col_tiles >= 4 * 76)
-        return launch<false, false, true, false, true>(a, maps, st);
     if (form == kFormGradX)
         return a.out32 ? launch<false, false, true, true>(a, maps, st) : launch<false, false, true, false>(a, maps, st);
     if (form == kFormGradW)
