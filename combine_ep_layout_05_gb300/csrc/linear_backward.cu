@@ -28,7 +28,9 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     if (act == EP_ACT_GELU) {
         const float s = sigmoid_fast(2.f * kGeluA * (z + kGeluB * z * z * z));
-        return s * (1.f + z * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z));
+        const float d = s * (1.f + z * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z));
+        // (from 30 on s is 0 or 1, and z^2 may overflow)
+        return fabsf(z) > 30.f ? (z > 0.f ? 1.f : 0.f) : d;
     }
     return 1.f;
 }
@@ -100,8 +102,9 @@ __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(const ActGradArg
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float s = sigmoid_fast(z[i]), gi = g[i];
-                    g[i] = gi * up[i] * s * (1.f + z[i] * (1.f - s));
-                    up[i] = gi * z[i] * s;
+                    // (the slope first: far out it is 0, and products of the others may overflow)
+                    g[i] = gi * (s * (1.f + z[i] * (1.f - s)) * up[i]);
+                    up[i] = gi * (z[i] * s);
                     sum[0][i] += g[i];
                     sum[P - 1][i] += up[i];
                 }

@@ -328,3 +328,40 @@ def test_calls_behind_each_other_share_a_workspace(m, M, K, N, act):
             m.ep_linear_backward(g, x, w, *o, pre, act, ws)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for o, q in zip(want, got) for a, b in zip(o, q))
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+def test_backward_far_from_zero(m, act):
+    """Where an activation is its input or nothing, its gradient is the incoming one or nothing, however large the
+    pre-activations are: no product in between overflows into NaN."""
+    z = [s * v for v in (30.0, 32.0, 100.0, 1e4, 1e10, 2e19, 1e30, 3e38) for s in (1, -1)]
+    N, K = len(z), 64
+    z = torch.tensor(z, device=DEV).bfloat16()
+    gate = z if act != "swiglu" else torch.cat([z, torch.full_like(z, 3.0)])
+    pre = gate[None].contiguous()
+    wide = pre.shape[1]
+    g = torch.full((1, N), 1e20, device=DEV)
+    x, w = torch.ones(1, K, device=DEV).bfloat16(), torch.ones(wide, K, device=DEV).bfloat16()
+    gb = torch.empty(wide, device=DEV)
+    ws = torch.empty(m.ep_linear_backward_workspace_bytes(1, K, N, act), dtype=torch.uint8, device=DEV)
+    m.ep_linear_backward(g, x, w, grad_bias=gb, pre=pre, activation=act, workspace=ws)
+    zd, gd = z.double(), g[0].double()
+    slope = (zd > 0).double()
+    want = slope * gd * (3.0 if act == "swiglu" else 1.0)
+    assert bool(((gb[:N].double() - want).abs() <= 1e-5 * 3.0 * gd).all())     # (from 30 on the slopes' rests are below 31 e^-30 = 3e-12)
+    if act == "swiglu":
+        up = gd * slope * zd
+        fits = up < 3e38
+        assert bool(((gb[N:].double() - up).abs() <= 1e-5 * up + 1e-5 * gd)[fits].all())
+        assert not bool(torch.isnan(gb).any())
+
+
+def test_swiglu_backward_product_order(m):
+    """Beside a slope of zero, a gradient and an up row whose product is beyond fp32 leave zero."""
+    g = torch.full((1, 8), 1e20, device=DEV)
+    pre = torch.cat([torch.full((1, 8), -300.0, device=DEV), torch.full((1, 8), 1e30, device=DEV)], 1).bfloat16()
+    x, w = torch.ones(1, 64, device=DEV).bfloat16(), torch.ones(16, 64, device=DEV).bfloat16()
+    gb = torch.empty(16, device=DEV)
+    ws = torch.empty(m.ep_linear_backward_workspace_bytes(1, 64, 8, "swiglu"), dtype=torch.uint8, device=DEV)
+    m.ep_linear_backward(g, x, w, grad_bias=gb, pre=pre, activation="swiglu", workspace=ws)
+    assert bool((gb == 0).all())
