@@ -644,6 +644,8 @@ def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "
 
 
 def ep_linear_backward_workspace_bytes(rows: int, in_features: int, out_features: int, activation: str = "none") -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
     return _lib.ep_linear_backward_workspace_bytes(rows, in_features, out_features, ACTIVATIONS[activation])
 
 

@@ -136,31 +136,45 @@ class MoeLayer:
         ep.ep_route_backward(p, self.router, logits, self.idx, self.grad_weights, grad_logits, self.status, stream)
         return grad_logits
 
-    def _linear_backward(self, grad_out, x, w, grad_x, grad_w, pre, activation, stream):
-        wide = w.shape[0]
-        need = ep.ep_linear_backward_workspace_bytes(x.shape[0], x.shape[1], wide // 2 if activation == "swiglu" else wide,
-                                                     activation)
-        ws = getattr(self, "backward_workspace", None)
-        if ws is None or ws.numel() < need:
-            self.backward_workspace = ws = torch.empty(max(16, need), dtype=torch.uint8, device=x.device)
-        ep.ep_linear_backward(grad_out, x, w, grad_x=grad_x, grad_w=grad_w, pre=pre, activation=activation, workspace=ws,
-                              dev_status=self.status, stream=stream)
+    def _kept(self, name, make, stream):
+        """A buffer of the gradients: made by the first call, on its stream, and kept, so that neither a later call nor a
+        graph that holds its address finds it moved."""
+        if name not in self.__dict__:
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+                setattr(self, name, make())
+        return getattr(self, name)
+
+    def _workspace(self, name, w, activation, stream):
+        rows, out = self.p.num_tokens, w.shape[0] // 2 if activation == "swiglu" else w.shape[0]
+        return self._kept(name, lambda: torch.empty(
+            max(16, ep.ep_linear_backward_workspace_bytes(rows, w.shape[1], out, activation)), dtype=torch.uint8,
+            device=w.device), stream)
 
     def gate_grad(self, grad_logits, x, grad_x=None, grad_gate=None, stream=None):
         """Gradients of the logits' product, from router_grad's: grad_x [T, H] bf16 (the tokens', through the gate
         alone) and grad_gate [E, H] bf16 or fp32; None: not computed."""
-        self._linear_backward(grad_logits, x, self.gate, grad_x, grad_gate, None, "none", stream)
+        if self.gate is None:
+            raise ValueError("a layer without a gate has no gate_grad")
+        ep.ep_linear_backward(grad_logits, x, self.gate, grad_x=grad_x, grad_w=grad_gate,
+                              workspace=self._workspace("gate_workspace", self.gate, "none", stream),
+                              dev_status=self.status, stream=stream)
 
     def shared_grad(self, grad_out, x, grad_x=None, grad_gate_up=None, grad_down=None, stream=None):
         """After forward: gradients through the shared expert from grad_out [T, H] bf16: the tokens' (bf16) and its
         matrices' (bf16 or fp32); None: not computed."""
+        if self.shared_down is None:
+            raise ValueError("a layer without a shared expert has no shared_grad")
         grad_act = None
         if grad_x is not None or grad_gate_up is not None:
-            grad_act = torch.empty_like(self.shared_act)
-        self._linear_backward(grad_out, self.shared_act, self.shared_down, grad_act, grad_down, None, "none", stream)
+            grad_act = self._kept("shared_grad_act", lambda: torch.empty_like(self.shared_act), stream)
+        ep.ep_linear_backward(grad_out, self.shared_act, self.shared_down, grad_x=grad_act, grad_w=grad_down,
+                              workspace=self._workspace("shared_down_workspace", self.shared_down, "none", stream),
+                              dev_status=self.status, stream=stream)
         if grad_act is not None:
-            self._linear_backward(grad_act, x, self.shared_gate_up, grad_x, grad_gate_up, self.shared_pre, "swiglu",
-                                  stream)
+            ep.ep_linear_backward(grad_act, x, self.shared_gate_up, grad_x=grad_x, grad_w=grad_gate_up, pre=self.shared_pre,
+                                  activation="swiglu",
+                                  workspace=self._workspace("shared_up_workspace", self.shared_gate_up, "swiglu", stream),
+                                  dev_status=self.status, stream=stream)
 
 
 def demo(T: int = 256, H: int = 7168, I: int = 2048, E: int = 64, k: int = 8, R: int = 8) -> None:

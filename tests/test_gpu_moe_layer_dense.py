@@ -127,3 +127,53 @@ def test_layer_refuses(m):
     with pytest.raises(ValueError):
         MoeLayer(8, 256, 128, 4, 2, 2, z, s, d, s, shared_gate_up=torch.zeros(100, 256, device=DEV),
                  shared_down=torch.zeros(256, 64, device=DEV))
+
+
+def test_gradients_refuse_what_the_layer_lacks(m):
+    layer, x = make(8, 256, 128, 8, 2, 2, 0)
+    with pytest.raises(ValueError):
+        layer.shared_grad(x, x, torch.empty_like(x))
+    layer.gate = None
+    with pytest.raises(ValueError):
+        layer.gate_grad(layer.logits, x, torch.empty_like(x))
+
+
+def test_gradients_on_streams_and_in_a_graph(m):
+    """The gate's and the shared expert's gradients at the same time, on streams of their own, while the current stream
+    allocates and writes; then recorded, and replayed after other calls on the same layer."""
+    T, H, S = 700, 512, 264
+    layer, x = make(T, H, 128, 8, 2, 2, S, seed=4)
+    layer.forward(x)
+    gen = torch.Generator(DEV).manual_seed(11)
+    go = torch.randn(T, H, generator=gen, device=DEV).bfloat16()
+    gl = torch.randn(T, 8, generator=gen, device=DEV)
+    outs = lambda: [torch.zeros_like(x), torch.zeros(8, H, device=DEV), torch.zeros_like(x),
+                    torch.zeros(2 * S, H, device=DEV), torch.zeros(H, S, device=DEV)]
+
+    def both(o, a, b):
+        layer.gate_grad(gl, x, o[0], o[1], stream=a)
+        layer.shared_grad(go, x, *o[2:], stream=b)
+    got, want = outs(), outs()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (a, b):
+        s.wait_stream(torch.cuda.current_stream())
+    both(got, a, b)                                  # (the layer's first: its buffers are made here)
+    for _ in range(8):
+        torch.full((T, S), float("nan"), device=DEV, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream()
+    both(want, here, here)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(got, torch.cuda.current_stream(), torch.cuda.current_stream())
+    other = outs()
+    go2 = go.flip(0).contiguous()
+    layer.shared_grad(go2, x, *other[2:])
+    for t in got:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert m.ep_get_status(layer.status) == 0
