@@ -12,7 +12,8 @@
 //   grad_x   A = G [M, N], B = w [N, K]: B along its rows (columns of w)
 //   grad_w   A = G [M, N], B = x [M, K]: both along their rows
 // Nothing is transposed in memory: the tensor core reads either form from
-// shared memory, with boxes of 128 rows x 64 contraction or of 64 x 64.
+// shared memory, with boxes of 128 rows (A's of as many as a tile has) x 64
+// contraction or of 64 x 64.
 //
 // A CTA pair computes 256 x 256 outputs (SwiGLU: 256 x 128, the gate's rows in
 // the first CTA's B, the up rows in the second's): each CTA holds 128 rows of A
@@ -110,16 +111,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- boxes ----
         if (lane == 0) {
             const uint32_t full = cluster_addr(&s.full[0], 0);
+            // (rows of A that a tile lacks stay whatever they are: they reach no other row's sums, and nobody takes theirs)
+            const int bytes = 2 * (A_MN ? kStageBytes : a.half_rows * (kStep * 2) + kPartBytes);
             int st = 0, ph = 1, it = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
                 const LinearUnit v = linear_unit(a, u);
-                const int r0 = v.row * kTile + rank * kPart;
+                const int r0 = (v.row * 2 + rank) * (A_MN ? kPart : a.half_rows);
                 const int c0 = SWIGLU ? rank * (int)a.C + v.col * kPart : v.col * kTile + rank * kPart;
                 for (int k = v.first; k < v.last; ++k, ++it) {
                     ok = mbar_wait(&s.empty[st], ph, patience);
                     if (!ok) break;
-                    if (rank == 0) mbar_expect_tx(&s.full[st], 2 * kStageBytes);
+                    if (rank == 0) mbar_expect_tx(&s.full[st], bytes);
                     unsigned char *pa = s.buf[st];
                     const uint32_t bar = full + st * 8;
                     if (A_MN) {
@@ -216,7 +219,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int u = pair; u < units && ok; u += pairs) {
             const LinearUnit v = linear_unit(a, u);
-            const int64_t r = (int64_t)v.row * kTile + rank * kPart + quarter * 32 + lane;
+            const int held = A_MN ? kPart : a.half_rows;
+            const int64_t first = ((int64_t)v.row * 2 + rank) * held, r = first + quarter * 32 + lane;
+            const int64_t end = min(a.R, first + held);
             const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
             // the residual of 32 columns: where rows are aligned, asked for one step ahead of them
             uint32_t res[16];
@@ -224,23 +229,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (PLAIN) return;
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
-                if (a.residual && a.residual_align >= 16 && r < a.R && n > 0)
+                if (a.residual && a.residual_align >= 16 && r < end && n > 0)
                     load_bf16<32>(a.residual + r * a.residual_stride + c, res, n, a.residual_align);
             };
             ask(0);
             const int64_t row0 = r - lane;                      // the warp's rows, and how many exist
-            const int n_rows = (int)min(max(a.R - row0, (int64_t)0), (int64_t)32);
+            const int n_rows = (int)min(max(end - row0, (int64_t)0), (int64_t)32);
             // Results leave through shared memory, in boxes of 32 rows x 128 bytes, where out can be a tensor map (each thread
             // storing 32 bytes a time along its row, a warp's store touches 32 lines: 32768 x 7168 of 256 took 115 us, 4.1
             // TB/s).  The swizzle keeps rows' 16 bytes apart.
             unsigned char *own = s.rows[warp - 4];
+            const bool boxed = a.boxes && (n_rows == 32 || end == a.R);   // (a box of fewer rows would reach into the next tile)
             constexpr int kHalves = LONG ? 1 : 2;               // chunks of 32 columns in a box
             const auto finish = [&](int q, const uint32_t *t) {
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
                 if (n <= 0) return;                             // (for the whole warp)
-                const bool live = r < a.R;
-                if (a.boxes && q % kHalves == 0) {
+                const bool live = r < end;
+                if (boxed && q % kHalves == 0) {
                     if (lane == 0) bulk_wait_read<0>();       // (what was in this box has been read)
                     __syncwarp();
                 }
@@ -278,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (q + 1 < kChunks) ask(q + 1);
                     }
                 }
-                if (a.boxes) {
+                if (boxed) {
                     uint4 *to = reinterpret_cast<uint4 *>(own + lane * 128);
 #pragma unroll
                     for (int i = 0; i < (LONG ? 8 : 4); ++i) {
@@ -372,11 +378,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (a.order == kBeside) wait_for_launch_before();
 }
 
-// The operand as a tensor map of bytes.  Along the contraction: boxes of 128
+// The operand as a tensor map of bytes.  Along the contraction: boxes of `rows`
 // rows x 128 bytes; along its rows: boxes of 64 of the contraction x 128 bytes.
-cudaError_t operand_map(const LinearOperand &o, bool mn, CUtensorMap *map) {
+cudaError_t operand_map(const LinearOperand &o, bool mn, int rows, CUtensorMap *map) {
     const cuuint64_t dims[2] = {(cuuint64_t)o.cols * 2, (cuuint64_t)o.rows}, strides[1] = {(cuuint64_t)o.stride * 2};
-    const cuuint32_t box[2] = {128, (cuuint32_t)(mn ? kStep : kPart)};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(mn ? kStep : rows)};
     return encode_map(map, 2, o.p, dims, strides, box);
 }
 
@@ -432,13 +438,21 @@ int linear_splits(int64_t R, int64_t C, int64_t L) {
 cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const LinearOperand &B, cudaStream_t st) {
     const bool swiglu = form == kFormForward && a.act == EP_ACT_SWIGLU;
     const int cols = swiglu ? kPart : kTile;
-    a.row_tiles = (int)((a.R + kTile - 1) / kTile);
     a.col_tiles = (int)((a.C + cols - 1) / cols);
     a.steps = (int)((a.L + kStep - 1) / kStep);
     a.split_steps = (a.steps + a.splits - 1) / a.splits;
+    a.half_rows = kPart;
+    // One tile of columns: A is read from memory once and bounds the launch, so the last turn of the SMs should not read
+    // less than the others.  The turns stay as many and have equal rows (of one turn there is nothing to gain: 10000 rows
+    // of 7168 took 41.8 us so, 41.0 with full tiles).  In us, full tiles | equal turns, 7168 -> 64: 20000 rows 80 | 68, 40000
+    // rows 123 | 106, 65536 rows 166 | 157; -> 256: 85 | 77, 133 | 122, 181 | 176; 256 -> 256, 32768 rows: 10.4 | 10.4.
+    const int64_t halves = (a.R + kPart - 1) / kPart, turn = 2 * (num_sms() / 2), turns = (halves + turn - 1) / turn;
+    if (form != kFormGradW && a.col_tiles == 1 && a.splits == 1 && turns > 1)
+        a.half_rows = (int)((a.R + turns * turn - 1) / (turns * turn));
+    a.row_tiles = (int)((a.R + 2 * a.half_rows - 1) / (2 * a.half_rows));
     LinearMaps maps;
-    if (cudaError_t e = operand_map(A, form == kFormGradW, &maps.a)) return e;
-    if (cudaError_t e = operand_map(B, form != kFormForward, &maps.b)) return e;
+    if (cudaError_t e = operand_map(A, form == kFormGradW, a.half_rows, &maps.a)) return e;
+    if (cudaError_t e = operand_map(B, form != kFormForward, kPart, &maps.b)) return e;
     // (rows and their strides in multiples of 16 bytes; the parts of a split contraction are its third dimension)
     const int64_t size = a.out32 ? 4 : 2, stride = a.out_stride * size, part = (a.splits > 1 ? a.split_stride : a.out_stride) * size;
     // (not where the pre-activations or the residual need that memory)

@@ -330,6 +330,16 @@ def test_calls_behind_each_other_share_a_workspace(m, M, K, N, act):
         assert all(torch.equal(a, b) for o, q in zip(want, got) for a, b in zip(o, q))
 
 
+@pytest.mark.parametrize("M,K,N,act", [(20000, 136, 200, "none"), (19457, 200, 128, "swiglu"), (38913, 72, 64, "gelu"),
+                                       (39000, 64, 255, "silu")])
+def test_linear_turns_of_equal_rows(m, M, K, N, act):
+    """More rows than the SMs take at once, of one tile of columns: tiles that end within a box of results."""
+    check_forward(m, M, K, N, act, True, True, False, True)
+    check_forward(m, M, K, N, act, False, True, True, False, extra=8, seed=1)
+    check_forward(m, M, K, N, act, True, False, False, False, extra=1, seed=2)
+    check_backward(m, M, K, N, act, False, True, seed=3)
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
 def test_backward_far_from_zero(m, act):
     """Where an activation is its input or nothing, its gradient is the incoming one or nothing, however large the
