@@ -443,12 +443,13 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
     a.split_steps = (a.steps + a.splits - 1) / a.splits;
     a.half_rows = kPart;
     // One tile of columns: A is read from memory once and bounds the launch, so the last turn of the SMs should not read
-    // less than the others.  The turns stay as many and have equal rows (of one turn there is nothing to gain: 10000 rows
-    // of 7168 took 41.8 us so, 41.0 with full tiles).  In us, full tiles | equal turns, 7168 -> 64: 20000 rows 80 | 68, 40000
-    // rows 123 | 106, 65536 rows 166 | 157; -> 256: 85 | 77, 133 | 122, 181 | 176; 256 -> 256, 32768 rows: 10.4 | 10.4.
+    // much less than the others.  The turns stay as many and have equal rows; a turn of products takes as long, whatever
+    // rows a tile has, so this is for tiles of at most 3/4.  In us, full tiles | equal turns, 7168 -> 64: 20000 rows 80 | 68,
+    // 40000 123 | 106; -> 256: 85 | 77, 133 | 122.  With 27/32 of a tile, 32768 rows -> 256, 93 | 92 from a graph but 98.9 |
+    // 102.6 with a cold L2; in one turn 10000 rows 41.0 | 41.8.
     const int64_t halves = (a.R + kPart - 1) / kPart, turn = 2 * (num_sms() / 2), turns = (halves + turn - 1) / turn;
-    if (form != kFormGradW && a.col_tiles == 1 && a.splits == 1 && turns > 1)
-        a.half_rows = (int)((a.R + turns * turn - 1) / (turns * turn));
+    const int64_t equal = (a.R + turns * turn - 1) / (turns * turn);
+    if (form != kFormGradW && a.col_tiles == 1 && a.splits == 1 && turns > 1 && equal <= kPart * 3 / 4) a.half_rows = (int)equal;
     a.row_tiles = (int)((a.R + 2 * a.half_rows - 1) / (2 * a.half_rows));
     LinearMaps maps;
     if (cudaError_t e = operand_map(A, form == kFormGradW, a.half_rows, &maps.a)) return e;
