@@ -24,6 +24,12 @@
 // bytes are counted on the first CTA's barrier, wherever they land), 1 the
 // products (first CTA), 4 to 11 the epilogue: a thread owns a row of a half of
 // the columns.
+//
+// Measured, from a graph: 8192 rows of 7168 -> 2 x 2048 with SwiGLU and pre-activations 258 us
+// (1.87 PFLOP/s, 97% of the measured rate of library products; the tensor pipe is busy 87% of a cold launch), its two
+// gradients 249 us each; 32768 rows of 7168 -> 256 in fp32 92 us (5.5 TB/s): in the first of two turns the memory
+// bounds it, in the second the 32 KB a step that a CTA takes from L2 (0.27 us); their grad_x 100 us (470 MB written),
+// bound by shared memory, through which operands, products and results go (some 1.6 us of a tile's 2.1).
 #include <algorithm>
 
 #include "linear_device.cuh"
@@ -33,17 +39,18 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kStages = 6;                      // 192 KB of operands
+constexpr int kRing = 192 * 1024;               // bytes of operands: 6 steps of whole tiles, at most kMostStages of less
+constexpr int kMostStages = 16;
 constexpr int kTile = 2 * kPart;                // rows and columns of a pair's tile
 constexpr int kSegment = 8;                     // steps of a LONG sum that stay in tensor memory
 constexpr int kIssueRegs = 88, kEndRegs = 208;  // LONG: 88 + 2 * 208 = 3 * 168, the launch's registers
 constexpr int kGroup = 8;                       // row tiles that are walked together, for L2
 
 struct LinearShared {
-    unsigned char buf[kStages][2 * kPartBytes];  // A, then B
+    unsigned char ring[kRing];                  // steps: A, then B
     unsigned char rows[8][32 * 128];            // a warp's results on their way out: 32 rows of 128 bytes
-    uint64_t full[kStages];                     // (the first CTA's) both CTAs' operands
-    uint64_t empty[kStages];                    // a step's products are done
+    uint64_t full[kMostStages];                 // (the first CTA's) both CTAs' operands
+    uint64_t empty[kMostStages];                // a step's products are done
     uint64_t tfull[2];                          // an accumulator is complete
     uint64_t tempty[2];                         // (the first CTA's) taken out by both CTAs
     uint32_t tmem;
@@ -77,7 +84,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ LinearMaps maps) {
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
     LinearShared &s = *reinterpret_cast<LinearShared *>(raw);
-    constexpr int S = kStages, kStageBytes = sizeof(s.buf[0]);
+    // (gradients' tiles are whole)
+    const int S = B_MN ? kRing / (2 * kPartBytes) : a.stages, stage_bytes = B_MN ? 2 * kPartBytes : a.stage_bytes;
+    const int a_bytes = B_MN ? kPartBytes : a.a_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int64_t all = (int64_t)a.row_tiles * a.col_tiles * a.splits;     // (below 2^31: checked on the host)
@@ -112,18 +121,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint32_t full = cluster_addr(&s.full[0], 0);
             // (rows of A that a tile lacks stay whatever they are: they reach no other row's sums, and nobody takes theirs)
-            const int bytes = 2 * (A_MN ? kStageBytes : a.half_rows * (kStep * 2) + kPartBytes);
+            const int bytes = 2 * (kStep * 2) * ((B_MN ? kPart : a.half_rows) + (B_MN ? kPart : a.half_cols));
             int st = 0, ph = 1, it = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
                 const LinearUnit v = linear_unit(a, u);
-                const int r0 = (v.row * 2 + rank) * (A_MN ? kPart : a.half_rows);
-                const int c0 = SWIGLU ? rank * (int)a.C + v.col * kPart : v.col * kTile + rank * kPart;
+                const int r0 = (v.row * 2 + rank) * (B_MN ? kPart : a.half_rows);
+                const int c0 = SWIGLU ? rank * (int)a.C + v.col * kPart : v.col * kTile + rank * (B_MN ? kPart : a.half_cols);
                 for (int k = v.first; k < v.last; ++k, ++it) {
                     ok = mbar_wait(&s.empty[st], ph, patience);
                     if (!ok) break;
                     if (rank == 0) mbar_expect_tx(&s.full[st], bytes);
-                    unsigned char *pa = s.buf[st];
+                    unsigned char *pa = s.ring + st * stage_bytes;
                     const uint32_t bar = full + st * 8;
                     if (A_MN) {
                         tma_load_2d_pair(pa, &maps.a, r0 * 2, k * kStep, bar);
@@ -131,7 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else {
                         tma_load_2d_pair(pa, &maps.a, k * kStep * 2, r0, bar);
                     }
-                    unsigned char *pb = pa + kPartBytes;
+                    unsigned char *pb = pa + a_bytes;
                     if (B_MN) {
                         tma_load_2d_pair(pb, &maps.b, c0 * 2, k * kStep, bar);
                         tma_load_2d_pair(pb + kPartBytes / 2, &maps.b, c0 * 2 + 128, k * kStep, bar);
@@ -142,16 +151,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             // the products of a step follow its boxes
-            drain<S>(s.empty, it);
+            drain_ring(s.empty, S, it);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
         if (rank == 0) {
-            constexpr uint32_t idesc = mma_idesc_bf16(kTile, kTile, A_MN, B_MN);
+            const uint32_t idesc = mma_idesc_bf16(kTile, B_MN ? kTile : 2 * a.half_cols, A_MN, B_MN);
             const bool issue = elect_one();
-            const uint64_t da0 = A_MN ? smem_desc_mn(s.buf[0], kPartBytes / 2) : smem_desc(s.buf[0]);
-            const uint64_t db0 = B_MN ? smem_desc_mn(s.buf[0] + kPartBytes, kPartBytes / 2) : smem_desc(s.buf[0] + kPartBytes);
+            const uint64_t da0 = A_MN ? smem_desc_mn(s.ring, kPartBytes / 2) : smem_desc(s.ring);
+            const uint64_t db0 = B_MN ? smem_desc_mn(s.ring + a_bytes, kPartBytes / 2) : smem_desc(s.ring + a_bytes);
             // 16 of the contraction: 32 bytes along a row, or 16 lines of 128 bytes
             constexpr uint32_t ka = A_MN ? 2048 >> 4 : 32 >> 4, kb = B_MN ? 2048 >> 4 : 32 >> 4;
             int st = 0, ph = 0, acc = 0, aph = 1;
@@ -169,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         acquire_shared_of_cluster();
                         tmem_fence_after();
                         if (issue) {
-                            const uint32_t at = (uint32_t)(st * (kStageBytes >> 4));
+                            const uint32_t at = (uint32_t)(st * (stage_bytes >> 4));
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mma_bf16<2>(tmem + acc * kTile, da0 + at + i * ka, db0 + at + i * kb, idesc,
@@ -219,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int u = pair; u < units && ok; u += pairs) {
             const LinearUnit v = linear_unit(a, u);
-            const int held = A_MN ? kPart : a.half_rows;
+            const int held = B_MN ? kPart : a.half_rows;
             const int64_t first = ((int64_t)v.row * 2 + rank) * held, r = first + quarter * 32 + lane;
             const int64_t end = min(a.R, first + held);
             const int64_t c0 = (int64_t)v.col * (SWIGLU ? kPart : kTile) + half * kCols;
@@ -441,19 +450,27 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
     a.col_tiles = (int)((a.C + cols - 1) / cols);
     a.steps = (int)((a.L + kStep - 1) / kStep);
     a.split_steps = (a.steps + a.splits - 1) / a.splits;
-    a.half_rows = kPart;
-    // One tile of columns: A is read from memory once and bounds the launch, so the last turn of the SMs should not read
-    // much less than the others.  The turns stay as many and have equal rows; a turn of products takes as long, whatever
-    // rows a tile has, so this is for tiles of at most 3/4.  In us, full tiles | equal turns, 7168 -> 64: 20000 rows 80 | 68,
-    // 40000 123 | 106; -> 256: 85 | 77, 133 | 122.  With 27/32 of a tile, 32768 rows -> 256, 93 | 92 from a graph but 98.9 |
-    // 102.6 with a cold L2; in one turn 10000 rows 41.0 | 41.8.
-    const int64_t halves = (a.R + kPart - 1) / kPart, turn = 2 * (num_sms() / 2), turns = (halves + turn - 1) / turn;
-    const int64_t equal = (a.R + turns * turn - 1) / (turns * turn);
-    if (form != kFormGradW && a.col_tiles == 1 && a.splits == 1 && turns > 1 && equal <= kPart * 3 / 4) a.half_rows = (int)equal;
+    a.half_rows = a.half_cols = kPart;
+    // One tile of columns: A is read from memory once, and bounds the launch.  (1) The columns are as many as there are, which
+    // leaves room for more steps under way: 6000 and 20000 rows of 7168 -> 64, cold, in us, whole tiles | as many as there
+    // are: 41 | 37, 74 | 68.  (2) Where whole tiles would leave half of the SMs or more without work in the last turn, the turns
+    // are made equal in rows.  A turn of products takes as long, but the memory has the same work all the time.  Cold,
+    // 7168 -> 256, whole | equal: 20000 rows (the last turn has 3 of 76 pairs) 98 | 84, 28000 (34) 100 | 94, 44000 (20)
+    // 146 | 136, 65536 (28) 192 | 187; 32768 (52) 98.1 | 103.9.  One turn stays: 10000 rows 41.0 | 41.8.
+    if (form == kFormForward && a.col_tiles == 1) {
+        if (!swiglu) a.half_cols = (int)(std::max<int64_t>(a.C, 32) + 15) / 16 * 8;
+        const int64_t pairs = num_sms() / 2, tiles = (a.R + kTile - 1) / kTile, turns = (tiles + pairs - 1) / pairs;
+        if (turns > 1 && (tiles - (turns - 1) * pairs) * 2 <= pairs)
+            a.half_rows = (int)((a.R + 2 * turns * pairs - 1) / (2 * turns * pairs));
+    }
     a.row_tiles = (int)((a.R + 2 * a.half_rows - 1) / (2 * a.half_rows));
+    // (parts start at whole atoms of 8 rows)
+    a.a_bytes = (a.half_rows + 7) / 8 * 8 * kStep * 2;
+    a.stage_bytes = a.a_bytes + a.half_cols * kStep * 2;
+    a.stages = std::min(kMostStages, kRing / a.stage_bytes);
     LinearMaps maps;
     if (cudaError_t e = operand_map(A, form == kFormGradW, a.half_rows, &maps.a)) return e;
-    if (cudaError_t e = operand_map(B, form != kFormForward, kPart, &maps.b)) return e;
+    if (cudaError_t e = operand_map(B, form != kFormForward, a.half_cols, &maps.b)) return e;
     // (rows and their strides in multiples of 16 bytes; the parts of a split contraction are its third dimension)
     const int64_t size = a.out32 ? 4 : 2, stride = a.out_stride * size, part = (a.splits > 1 ? a.split_stride : a.out_stride) * size;
     // (not where the pre-activations or the residual need that memory)

@@ -87,7 +87,8 @@ struct LinearArgs {
     int out_align, pre_align, residual_align;   // see row_align
     int splits;              // parts of the contraction (at least 1; every part has steps)
     int row_tiles, col_tiles, split_steps, steps;           // by the launcher, as is
-    int half_rows;           // rows of a CTA in a tile of a pair
+    int half_rows, half_cols;    // rows and columns of a tile of a pair that a CTA brings
+    int a_bytes, stage_bytes, stages;   // a step's A, its operands, and how many of these
     bool boxes;              // whether results leave by tensor map
     int order;               // kFirst, kAfter or kBeside
     int64_t split_stride;    // elements between the partial sums of two splits

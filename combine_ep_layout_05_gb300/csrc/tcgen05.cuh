@@ -71,6 +71,13 @@ __device__ __forceinline__ void drain(uint64_t *bars, int n) {
         while (!mbar_try_wait(&bars[i % S], i / S & 1))
             if (clock64() - t0 > (1ll << 31)) return;
 }
+// the same, with a number of steps that the launch knows
+__device__ __forceinline__ void drain_ring(uint64_t *bars, int stages, int n) {
+    const long long t0 = clock64();
+    for (int i = max(n - stages, 0); i < n; ++i)
+        while (!mbar_try_wait(&bars[i % stages], i / stages & 1))
+            if (clock64() - t0 > (1ll << 31)) return;
+}
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
