@@ -14,6 +14,10 @@
 // The tensor core cuts its sums off rather than rounding them: over a contraction of
 // 7168 in one accumulator the result is 8e-6 off.  Every kChain steps go to an
 // accumulator of their own (as far as there are), and these are added in fp32.
+//
+// Measured, from a graph: 32 rows of 7168 -> 256 (a gate) 7.4 us, of which the launch, the tensor memory, the first
+// boxes and the exchange take 5; one row of 7168 -> 2 x 2048 with SwiGLU 11.5 us (59 MB, 5.1 TB/s); 512 rows of
+// 7168 -> 256 10.8 us.
 #include <algorithm>
 #include <cstddef>
 

@@ -1,29 +1,34 @@
-// A whole mixture-of-experts layer for a few tokens (ep_moe_few), in two
-// launches: routing, the cast of the tokens, the gate and up products, SwiGLU
-// and its cast; then the down products and the weighted sum.
+// A whole mixture-of-experts layer for a few tokens (ep_moe_few), in three
+// launches: routing and the cast of the tokens; the gate and up products, SwiGLU
+// and its cast; the down products and the weighted sum.
 //
 //   idx, w = route(logits);  a = e4m3(x);  h = e4m3(silu(a G_e^T) * (a U_e^T));
 //   out[t] = residual[t] + sum_j w[t, j] (h D_e^T)[t, j],   e = idx[t, j]
 //
 // With a few tokens the time is that of reading the chosen experts' matrices
-// once; what a layer made of separate launches adds is their latency and the
-// receive buffers between them.  So every CTA routes all tokens itself (a warp a
-// token; the logits are a few KB), lists the chosen experts, and starts on its
-// share of their matrices; no CTA waits for another.  As in the products for few rows an
+// once; what a layer made of separate calls adds is their latency and the
+// receive buffers between them.  So the launches overlap: each begins while the one before
+// it ends and does what needs nothing of it (tensor memory, barriers; the third, whose experts
+// are known by then, fills its stages with matrix rows), and the second asks for the third's first rows towards
+// L2.  Each CTA lists the chosen experts itself.  As in the products for few rows an
 // expert, 128 matrix rows are the tensor core's M and the expert's tokens its N
 // (16, 32, 48 or 64), every block of 128 channels is one accumulation in tensor
 // memory, and a thread owns a matrix row and scales and adds the blocks in fp32.
 //
-// First launch: the warps that bring the tokens' rows read the bf16 tokens and
-// cast them on the way to shared memory, so there is no cast tensor.  A unit of
-// work is 128 columns of h, which are one block of its cast.  Both products of
+// First launch: a CTA of each token routes it, the others cast the tokens (as ep_dispatch does, each rounding
+// included) and zero the counters.
+// Second launch: a unit of work is 128 columns of h, which are one block of its cast.  Both products of
 // those columns land in the same thread.
-// Second launch: a unit is 128 output columns of one expert.  Its products, in fp32, go
+// Third launch: a unit is 128 output columns of one expert.  Its products, in fp32, go
 // to y [T, k, H] in the workspace; a CTA has a run of units, column tile after
 // column tile; the one that brings a tile's last expert (a counter of units for each
-// tile, which the first launch zeroes) adds the tile's k rows
-// of each token in the order j = 0 .. k - 1.  So the sum does not depend on who comes
+// tile) adds the tile's k rows of each token in the order j = 0 .. k - 1.  So the sum does not depend on who comes
 // last, and y is never rounded.  y is T k H 4 bytes against the experts' 3 I H each.
+//
+// Measured, from a graph, 256 experts of 7168 x 2048, 8 a token: one token 72 us (352 MB, 4.8 TB/s; the latency of three
+// launches that fill and drain, 19 us at the smallest sizes), 32 tokens 0.97 to 0.99 ms (7.2 GB, 7.2 to 7.4 TB/s: at the memory's
+// rate); 61 tokens, 64 experts of 4096 x 1408, 6 a token 196 us (1.1 GB, 5.6 TB/s).  One cooperative launch for the last two took
+// 0 to 10% longer.
 #include <algorithm>
 #include <cstddef>
 
@@ -104,14 +109,6 @@ struct MoeShared {
         return at;
     }
 };
-
-// Waits for the copies (or products) of the last steps that were issued, as drain(), with a ring of `stages`
-__device__ __forceinline__ void drain_ring(uint64_t *bars, int stages, int n) {
-    const long long t0 = clock64();
-    for (int i = max(n - stages, 0); i < n; ++i)
-        while (!mbar_try_wait(&bars[i % stages], i / stages & 1))
-            if (clock64() - t0 > (1ll << 31)) return;
-}
 
 // Fills the lists from s.idx, by all threads of the block, in turns of whole warps; complete when it returns.  s.tokens
 // are zeros, and both are there for all threads.

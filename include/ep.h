@@ -576,7 +576,8 @@ size_t ep_moe_few_workspace_bytes(const ep_problem *p, int64_t intermediate);
 
 /*
  * ep_moe_few - a whole mixture-of-experts layer for up to 64 tokens (a decode
- * step), in two launches that read each chosen expert's matrices once.
+ * step), in three launches that overlap and read each chosen expert's matrices
+ * once.
  *
  * The same as ep_route, the FP8 cast of ep_dispatch, ep_expert_swiglu, an ep_expert_gemm
  * whose output stays fp32, and
