@@ -375,3 +375,28 @@ def test_swiglu_backward_product_order(m):
     ws = torch.empty(m.ep_linear_backward_workspace_bytes(1, 64, 8, "swiglu"), dtype=torch.uint8, device=DEV)
     m.ep_linear_backward(g, x, w, grad_bias=gb, pre=pre, activation="swiglu", workspace=ws)
     assert bool((gb == 0).all())
+
+
+@pytest.mark.parametrize("N", [8200, 8201])
+def test_offsets_past_32_bits(m, N):
+    """More than 2^31 outputs, pre-activations and gradients: the last rows are those of a call on them alone, which the
+    tests above hold to the formula."""
+    M, K, n = 262200, 64, 300
+    x, w, b, rand, _ = make(M, K, N, "relu", 3)
+    out, pre = torch.empty(M, N, dtype=torch.bfloat16, device=DEV), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    m.ep_linear(x, w, out, bias=b, pre=pre, activation="relu")
+    tail = x[-n:].contiguous()
+    for rows in (slice(M - n, M), slice(0, n)):
+        z = x[rows].double() @ w.double().t() + b.double()
+        ez = 2 * (K + 16) * U * (x[rows].double().abs() @ w.double().abs().t()) + 2 * U * z.abs()
+        assert within(pre[rows], z, ez)
+        assert within(out[rows], z.clamp_min(0), ez)
+    go, gx = out, torch.empty_like(x)               # (a gradient as large as the outputs)
+    ws = torch.empty(m.ep_linear_backward_workspace_bytes(M, K, N, "relu"), dtype=torch.uint8, device=DEV)
+    m.ep_linear_backward(go, x, w, grad_x=gx, pre=pre, activation="relu", workspace=ws)
+    gt = torch.empty_like(tail)
+    ws2 = torch.empty(m.ep_linear_backward_workspace_bytes(n, K, N, "relu"), dtype=torch.uint8, device=DEV)
+    m.ep_linear_backward(go[-n:].contiguous(), tail, w, grad_x=gt, pre=pre[-n:].contiguous(), activation="relu", workspace=ws2)
+    g = torch.where(pre[-n:].double() > 0, go[-n:].double(), 0.0)
+    tol = 2 * (N + 16) * U * (g.abs() @ w.double().abs())
+    assert within(gx[-n:], g @ w.double(), tol) and within(gt, g @ w.double(), tol)
