@@ -4,10 +4,12 @@
 //   out[r, c] = act(sum_l A(r, l) B(c, l) + bias[c]) + residual[r, c]
 //
 // bf16 operands, fp32 sums, one rounding at the end.  The tensor core cuts its
-// sums off rather than rounding them: after a contraction of 7168 they are 8e-6 off.  Beside
-// the rounding to bf16 that is nothing, and such sums stay in tensor memory; fp32
-// results are taken out every 512 of the contraction and added in registers (LONG).  Three forms of the same loop, which differ in the way
-// the operands lie in memory:
+// sums off rather than rounding them, by about a unit in the last place for every 16 of the contraction: a sum of numbers of
+// one sign lags behind by a share that grows with its length (measured: 2.6e-5 after 7168, 7.7e-5 after 16384, 3.3e-3
+// after 2^19).  Up to kMostChain steps (8192) that is a fiftieth of the rounding to bf16, and bf16 results stay in
+// tensor memory; longer contractions and all fp32 results are taken out every 512 and added in registers
+// (LONG: 2e-6 off, however long; 2^17 takes 587 us instead of 574, 2^14 the same).  Three forms of the same
+// loop, which differ in the way the operands lie in memory:
 //   forward  A = x [M, K], B = w [N, K]: both along the contraction
 //   grad_x   A = G [M, N], B = w [N, K]: B along its rows (columns of w)
 //   grad_w   A = G [M, N], B = x [M, K]: both along their rows
@@ -78,8 +80,9 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearArgs &a, int u) {
     return v;
 }
 
-// LONG: fp32 results.  Their sums are taken out of tensor memory every kSegment steps and added in registers.
-template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG>
+// LONG: sums are taken out of tensor memory every kSegment steps and added in registers; OUT32: fp32 results (always
+// LONG).
+template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG, bool OUT32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ LinearMaps maps) {
     extern __shared__ __align__(1024) unsigned char raw[];    // (the only shared memory: it starts at its window's start)
@@ -249,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // TB/s).  The swizzle keeps rows' 16 bytes apart.
             unsigned char *own = s.rows[warp - 4];
             const bool boxed = a.boxes && (n_rows == 32 || end == a.R);   // (a box of fewer rows would reach into the next tile)
-            constexpr int kHalves = LONG ? 1 : 2;               // chunks of 32 columns in a box
+            constexpr int kHalves = OUT32 ? 1 : 2;              // chunks of 32 columns in a box
             const auto finish = [&](int q, const uint32_t *t) {
                 const int64_t c = c0 + q * 32;
                 const int n = (int)min(a.C - c, (int64_t)32);
@@ -296,9 +299,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (boxed) {
                     uint4 *to = reinterpret_cast<uint4 *>(own + lane * 128);
 #pragma unroll
-                    for (int i = 0; i < (LONG ? 8 : 4); ++i) {
-                        const int at = (LONG ? i : q % kHalves * 4 + i) ^ (lane & 7);
-                        if (LONG)
+                    for (int i = 0; i < (OUT32 ? 8 : 4); ++i) {
+                        const int at = (OUT32 ? i : q % kHalves * 4 + i) ^ (lane & 7);
+                        if (OUT32)
                             to[at] = make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]),
                                                 __float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3]));
                         else
@@ -311,11 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         fence_async_shared();
                         __syncwarp();
                         if (lane == 0 && n_rows > 0) {
-                            tma_store_3d(&maps.out, (int)(c - q % kHalves * 32) * (LONG ? 4 : 2), (int)row0, v.split, own);
+                            tma_store_3d(&maps.out, (int)(c - q % kHalves * 32) * (OUT32 ? 4 : 2), (int)row0, v.split, own);
                             bulk_commit();
                         }
                     }
-                } else if (LONG) {
+                } else if (OUT32) {
                     float *out = reinterpret_cast<float *>(a.out) + v.split * a.split_stride;
                     if (a.out_align >= 16) {
                         if (live) store_fp32(out + r * a.out_stride + c, z, n, a.out_align);
@@ -395,24 +398,31 @@ cudaError_t operand_map(const LinearOperand &o, bool mn, int rows, CUtensorMap *
     return encode_map(map, 2, o.p, dims, strides, box);
 }
 
-template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG>
+template <bool SWIGLU, bool A_MN, bool B_MN, bool LONG, bool OUT32>
 cudaError_t launch(const LinearArgs &a, const LinearMaps &maps, cudaStream_t st) {
     constexpr int bytes = sizeof(LinearShared);
     static_assert(bytes <= 227 * 1024, "shared memory");
     static std::atomic<int> ready[kCacheDevices];
     cudaError_t e = cudaSuccess;
     cached_per_device(ready, [&](int) {
-        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(linear_kernel<SWIGLU, A_MN, B_MN, LONG, OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         // the warpgroups' register shares are drawn from what the block was launched with
         cudaFuncAttributes f{};
-        if (!e) e = cudaFuncGetAttributes(&f, linear_kernel<SWIGLU, A_MN, B_MN, LONG>);
+        if (!e) e = cudaFuncGetAttributes(&f, linear_kernel<SWIGLU, A_MN, B_MN, LONG, OUT32>);
         if (!e && LONG && f.numRegs * 3 < kIssueRegs + 2 * kEndRegs) e = cudaErrorInvalidDeviceFunction;
         return e == cudaSuccess ? 1 : 0;
     });
     if (e) return e;
     const int64_t units = (int64_t)a.row_tiles * a.col_tiles * a.splits;
     const int grid = (int)std::min<int64_t>(num_sms() & ~1, 2 * units);
-    return launch_in_order(a.order, linear_kernel<SWIGLU, A_MN, B_MN, LONG>, dim3(grid), kThreads, bytes, 0, st, a, maps);
+    return launch_in_order(a.order, linear_kernel<SWIGLU, A_MN, B_MN, LONG, OUT32>, dim3(grid), kThreads, bytes, 0, st, a, maps);
+}
+
+// the same, by how results are summed
+template <bool SWIGLU, bool A_MN, bool B_MN>
+cudaError_t launch_sums(const LinearArgs &a, bool longer, const LinearMaps &maps, cudaStream_t st) {
+    if (a.out32) return launch<SWIGLU, A_MN, B_MN, true, true>(a, maps, st);
+    return longer ? launch<SWIGLU, A_MN, B_MN, true, false>(a, maps, st) : launch<SWIGLU, A_MN, B_MN, false, false>(a, maps, st);
 }
 
 }  // namespace
@@ -483,13 +493,10 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
         const cuuint32_t box[3] = {128, 32, 1};
         if (cudaError_t e = encode_map(&maps.out, 3, a.out, dims, strides, box)) return e;
     }
-    if (form == kFormGradX)
-        return a.out32 ? launch<false, false, true, true>(a, maps, st) : launch<false, false, true, false>(a, maps, st);
-    if (form == kFormGradW)
-        return a.out32 ? launch<false, true, true, true>(a, maps, st) : launch<false, true, true, false>(a, maps, st);
-    if (swiglu)
-        return a.out32 ? launch<true, false, false, true>(a, maps, st) : launch<true, false, false, false>(a, maps, st);
-    return a.out32 ? launch<false, false, false, true>(a, maps, st) : launch<false, false, false, false>(a, maps, st);
+    const bool longer = a.split_steps > kMostChain;
+    if (form == kFormGradX) return launch_sums<false, false, true>(a, longer, maps, st);
+    if (form == kFormGradW) return launch_sums<false, true, true>(a, longer, maps, st);
+    return swiglu ? launch_sums<true, false, false>(a, longer, maps, st) : launch_sums<false, false, false>(a, longer, maps, st);
 }
 
 }  // namespace ep

@@ -13,6 +13,7 @@ namespace {
 constexpr int kStep = 64;                       // contraction of a step: 128 bytes of bf16
 constexpr int kPart = 128;                      // rows of an operand that a CTA holds
 constexpr int kPartBytes = kPart * kStep * 2;
+constexpr int kMostChain = 128;                 // steps that one accumulator sums, where the result is bf16
 
 constexpr float kGeluA = 0.7978845608028654f, kGeluB = 0.044715f;   // sqrt(2 / pi), and the cubic's factor
 

@@ -11,9 +11,10 @@
 // cluster, in the order of their ranks.  No workspace, no atomics, one order of the sums.
 // Two CTAs to an SM, so that one streams while the other starts or ends.
 //
-// The tensor core cuts its sums off rather than rounding them: over a contraction of
-// 7168 in one accumulator the result is 8e-6 off.  Every kChain steps go to an
-// accumulator of their own (as far as there are), and these are added in fp32.
+// The tensor core cuts its sums off rather than rounding them (linear.cu).  Every kChain steps go to an
+// accumulator of their own, and these are added in fp32.  Where accumulators do not suffice, an
+// accumulator takes more, at most kMostChain, for a bf16 result; for an fp32 result, or for longer ones, the
+// other kernel does the work.
 //
 // Measured, from a graph: 32 rows of 7168 -> 256 (a gate) 7.4 us, of which the launch, the tensor memory, the first
 // boxes and the exchange take 5; one row of 7168 -> 2 x 2048 with SwiGLU 11.5 us (59 MB, 5.1 TB/s); 512 rows of
@@ -340,8 +341,8 @@ FewPlan few_plan(int form, const LinearArgs &a, int &size, int64_t &tiles, doubl
         const double bytes = 2.0 * a.L * (outs * (swiglu ? 2 : 1)) * p.col_tiles;
         const double start = 5.0 + 0.006 * std::min<int64_t>(ctas, 304) + 0.0015 * c * p.rows;
         double t = turns * start + std::max(turns * step * p.split_steps, bytes / 6.8e6);
-        // a longer chain would cost fp32 results digits
-        if (a.out32 && p.chain > kChain) t += 1e6;
+        // a longer chain would cost the result digits
+        if (p.chain > (a.out32 ? kChain : kMostChain)) t += 1e9;
         if (t < time) {
             time = t;
             best = p;

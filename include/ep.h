@@ -528,6 +528,9 @@ int ep_selftest_expert_timeout(const ep_problem *p, int kernel, int64_t out_feat
  *   out[m, n] = silu(z[m, n]) * z[m, N + n].
  * pre (NULL: not written): bf16(z), what ep_linear_backward needs of an
  * activation.
+ * The tensor core cuts fp32 sums off, by up to 2^-27 for each term: a bf16 result, of which at most 8192 terms go into
+ * one accumulator, may lag by 6.1e-5 of the sum of the terms' magnitudes, an fp32 one (512 terms) by 3.8e-6, besides the
+ * rounding of the accumulators' sum.
  *
  * x [rows, in_features] bf16, row m at x + m * x_stride; w [out_features (x 2),
  * in_features] bf16, contiguous; bias fp32 or NULL; residual bf16 or NULL, with
