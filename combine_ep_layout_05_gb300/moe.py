@@ -138,9 +138,13 @@ class MoeLayer:
 
     def _kept(self, name, make, stream):
         """A buffer of the gradients: made by the first call, on its stream, and kept, so that neither a later call nor a
-        graph that holds its address finds it moved."""
+        graph that holds its address finds it moved.  (Made on another stream it could be memory that writes of that
+        stream are still on their way to.)"""
         if name not in self.__dict__:
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):    # a handle; 0 and 1: the default stream
+                device, handle = self.status.device, int(stream)
+                stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+            with torch.cuda.stream(stream):
                 setattr(self, name, make())
         return getattr(self, name)
 
