@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     }
+    __syncwarp();                                  // (lanes leave that loop at different turns; the barrier is the whole warp's)
     cluster_sync();                                // nobody reads this CTA's part any more
     if (warp == 1) {
         tmem_fence_after();
