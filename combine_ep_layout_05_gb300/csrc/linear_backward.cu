@@ -112,10 +112,11 @@ __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(const ActGradArg
             } else {
                 if (a.act != EP_ACT_NONE) {
                     load8(a.pre + m * a.N + c, n, vec & 2, z);
-                    // (a gradient of 0 beside an infinite slope's formula is left to the arithmetic; relu chooses)
+                    // (relu chooses, so that a gradient of infinity beside a slope of 0 leaves 0; a NaN stays)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        g[i] = a.act == EP_ACT_RELU ? (z[i] > 0.f ? g[i] : 0.f) : g[i] * act_slope(z[i], a.act);
+                        g[i] = a.act == EP_ACT_RELU ? (z[i] > 0.f ? g[i] : z[i] <= 0.f ? 0.f : z[i])
+                                                    : g[i] * act_slope(z[i], a.act);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum[0][i] += g[i];

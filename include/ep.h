@@ -554,7 +554,7 @@ size_t ep_linear_backward_workspace_bytes(int64_t rows, int64_t in_features, int
  * ep_linear_backward - gradients of ep_linear (the residual's is grad_out itself).
  *
  * G[m, n] = grad_out[m, n] * act'(pre[m, n]) in fp32 (EP_ACT_SWIGLU: 2 N columns,
- * gate and up), from the bf16 pre-activations that ep_linear wrote;
+ * gate and up), from the bf16 pre-activations that ep_linear wrote (NaN where they are NaN);
  *   grad_bias[n] = sum_m G[m, n];
  *   grad_x[m, i] = sum_n bf16(G[m, n]) * w[n, i], rounded once to bf16;
  *   grad_w[n, i] = sum_m bf16(G[m, n]) * x[m, i], rounded once if bf16.
