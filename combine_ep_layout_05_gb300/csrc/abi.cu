@@ -770,6 +770,25 @@ int ep_selftest_expert_timeout(const ep_problem *p, int kernel, int64_t out_feat
 
 namespace {
 
+// How a call does its work: by the kernel for few or for many rows (EP_LINEAR_*; -1: the faster one), with waits that
+// give up after `clocks` cycles.  Self-tests choose.
+struct Manner {
+    int kernel = -1;
+    int64_t clocks = ep::kWaitClocks;
+};
+bool self_test_manner(int kernel, int64_t clocks, const int32_t *dev_status) {
+    if (kernel != EP_LINEAR_FEW_ROWS && kernel != EP_LINEAR_MANY_ROWS)
+        return fail(EP_ERR_INVALID_ARG, "unknown kernel %d", kernel), false;
+    if (clocks < 1 || clocks > ep::kWaitClocks) return fail(EP_ERR_INVALID_ARG, "clocks must be in 1..2^32"), false;
+    if (!dev_status) return fail(EP_ERR_INVALID_ARG, "dev_status is NULL"), false;
+    return true;
+}
+
+// whether the kernel for few rows does a product that the other one does in `many` us
+bool by_few_rows(const Manner &how, int form, const ep::LinearArgs &a, double many) {
+    return how.kernel < 0 ? ep::linear_few_time(form, a) < many : how.kernel == EP_LINEAR_FEW_ROWS;
+}
+
 // A dense product's sizes
 struct LinearSizes {
     int64_t M, K, N, wide;      // wide: rows of w
@@ -819,21 +838,21 @@ BackwardParts backward_parts(const LinearSizes &d) {
 // launches before it, and how the next may.
 cudaError_t backward_product(int form, int64_t R, int64_t C, int64_t L, int splits, const ep::LinearOperand &A,
                              const ep::LinearOperand &B, bool out32, void *out, int64_t out_stride, float *parts,
-                             int &order, bool &parts_used, int32_t *dev_status, cudaStream_t st) {
+                             int &order, bool &parts_used, const Manner &how, int32_t *dev_status, cudaStream_t st) {
     ep::LinearArgs a{};
     a.R = R;
     a.C = C;
     a.L = L;
     a.splits = splits;
     a.dev_status = dev_status;
-    a.wait_clocks = ep::kWaitClocks;
+    a.wait_clocks = how.clocks;
     a.out32 = out32;
     a.out = out;
     a.out_stride = out_stride;
     a.out_align = ep::row_align(out, out_stride * (out32 ? 4 : 2));
     a.order = order;
     order = ep::kBeside;       // (what comes next does not read this product)
-    if (ep::linear_few_time(form, a) < ep::linear_time(R, C, L, false, splits))
+    if (by_few_rows(how, form, a, ep::linear_time(R, C, L, false, splits)))
         return ep::launch_linear_few(form, a, A, B, st);
     const bool split = splits > 1;
     if (split && parts_used && a.order == ep::kBeside) a.order = ep::kAfter;   // the parts before are being summed
@@ -848,15 +867,10 @@ cudaError_t backward_product(int form, int64_t R, int64_t C, int64_t L, int spli
     return ep::launch_sum_parts(ep::SumPartsArgs{parts, splits, R, C, out32, out, out_stride, false}, st);
 }
 
-}  // namespace
-
-extern "C" {
-
-int ep_linear(int64_t rows, int64_t in_features, int64_t out_features, int activation, const uint16_t *x,
-              int64_t x_stride, const uint16_t *w, const float *bias, const uint16_t *residual,
-              int64_t residual_stride, int out_dtype, void *out, int64_t out_stride, uint16_t *pre,
-              int32_t *dev_status, ep_stream_t stream) {
-    g_err[0] = 0;
+int linear_call(const Manner &how, int64_t rows, int64_t in_features, int64_t out_features, int activation,
+                const uint16_t *x, int64_t x_stride, const uint16_t *w, const float *bias, const uint16_t *residual,
+                int64_t residual_stride, int out_dtype, void *out, int64_t out_stride, uint16_t *pre,
+                int32_t *dev_status, ep_stream_t stream) {
     LinearSizes d;
     if (!linear_sizes(rows, in_features, out_features, activation, d)) return EP_ERR_INVALID_ARG;
     if (out_dtype != EP_BF16 && out_dtype != EP_FP32) return fail(EP_ERR_INVALID_ARG, "out must be EP_BF16 or EP_FP32");
@@ -890,27 +904,20 @@ int ep_linear(int64_t rows, int64_t in_features, int64_t out_features, int activ
     a.pre_align = ep::row_align(pre, (activation == EP_ACT_SWIGLU ? d.N : d.wide) * 2);
     a.splits = 1;
     a.dev_status = dev_status;
-    a.wait_clocks = ep::kWaitClocks;
+    a.wait_clocks = how.clocks;
     const ep::LinearOperand X{x, d.M, d.K, x_stride}, W{w, d.wide, d.K, d.K};
-    const bool few = ep::linear_few_time(ep::kFormForward, a) <
-                     ep::linear_time(d.M, d.N, d.K, activation == EP_ACT_SWIGLU, 1);
+    const bool few = by_few_rows(how, ep::kFormForward, a,
+                                 ep::linear_time(d.M, d.N, d.K, activation == EP_ACT_SWIGLU, 1));
     cudaError_t e = few ? ep::launch_linear_few(ep::kFormForward, a, X, W, (cudaStream_t)stream)
                         : ep::launch_linear(ep::kFormForward, a, X, W, (cudaStream_t)stream);
     return e ? cuda_fail(e, "ep_linear launch") : EP_OK;
 }
 
-size_t ep_linear_backward_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features, int activation) {
-    g_err[0] = 0;
-    LinearSizes d;
-    return linear_sizes(rows, in_features, out_features, activation, d) ? backward_parts(d).total : 0;
-}
-
-int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, int activation, int grad_dtype,
-                       const void *grad_out, int64_t grad_stride, const uint16_t *x, int64_t x_stride,
-                       const uint16_t *w, const uint16_t *pre, uint16_t *grad_x, int64_t grad_x_stride,
-                       int grad_w_dtype, void *grad_w, float *grad_bias, void *workspace, size_t workspace_bytes,
-                       int32_t *dev_status, ep_stream_t stream) {
-    g_err[0] = 0;
+int linear_backward_call(const Manner &how, int64_t rows, int64_t in_features, int64_t out_features, int activation,
+                         int grad_dtype, const void *grad_out, int64_t grad_stride, const uint16_t *x,
+                         int64_t x_stride, const uint16_t *w, const uint16_t *pre, uint16_t *grad_x,
+                         int64_t grad_x_stride, int grad_w_dtype, void *grad_w, float *grad_bias, void *workspace,
+                         size_t workspace_bytes, int32_t *dev_status, ep_stream_t stream) {
     LinearSizes d;
     if (!linear_sizes(rows, in_features, out_features, activation, d)) return EP_ERR_INVALID_ARG;
     const bool grad32 = grad_dtype == EP_FP32, w32 = grad_w_dtype == EP_FP32;
@@ -973,11 +980,64 @@ int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, 
                               direct ? grad_stride : b.g_stride};
     if (grad_x)
         e = backward_product(ep::kFormGradX, d.M, d.K, d.wide, b.splits_x, G, ep::LinearOperand{w, d.wide, d.K, d.K},
-                             false, grad_x, grad_x_stride, parts, order, parts_used, dev_status, st);
+                             false, grad_x, grad_x_stride, parts, order, parts_used, how, dev_status, st);
     if (!e && grad_w)
         e = backward_product(ep::kFormGradW, d.wide, d.K, d.M, b.splits_w, G, ep::LinearOperand{x, d.M, d.K, x_stride},
-                             w32, grad_w, d.K, parts, order, parts_used, dev_status, st);
+                             w32, grad_w, d.K, parts, order, parts_used, how, dev_status, st);
     return e ? cuda_fail(e, "ep_linear_backward launch") : EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ep_linear(int64_t rows, int64_t in_features, int64_t out_features, int activation, const uint16_t *x,
+              int64_t x_stride, const uint16_t *w, const float *bias, const uint16_t *residual,
+              int64_t residual_stride, int out_dtype, void *out, int64_t out_stride, uint16_t *pre,
+              int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    return linear_call({}, rows, in_features, out_features, activation, x, x_stride, w, bias, residual,
+                       residual_stride, out_dtype, out, out_stride, pre, dev_status, stream);
+}
+
+size_t ep_linear_backward_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features, int activation) {
+    g_err[0] = 0;
+    LinearSizes d;
+    return linear_sizes(rows, in_features, out_features, activation, d) ? backward_parts(d).total : 0;
+}
+
+int ep_linear_backward(int64_t rows, int64_t in_features, int64_t out_features, int activation, int grad_dtype,
+                       const void *grad_out, int64_t grad_stride, const uint16_t *x, int64_t x_stride,
+                       const uint16_t *w, const uint16_t *pre, uint16_t *grad_x, int64_t grad_x_stride,
+                       int grad_w_dtype, void *grad_w, float *grad_bias, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    return linear_backward_call({}, rows, in_features, out_features, activation, grad_dtype, grad_out, grad_stride, x,
+                                x_stride, w, pre, grad_x, grad_x_stride, grad_w_dtype, grad_w, grad_bias, workspace,
+                                workspace_bytes, dev_status, stream);
+}
+
+int ep_selftest_linear(int kernel, int64_t clocks, int64_t rows, int64_t in_features, int64_t out_features,
+                       int activation, const uint16_t *x, int64_t x_stride, const uint16_t *w, const float *bias,
+                       const uint16_t *residual, int64_t residual_stride, int out_dtype, void *out,
+                       int64_t out_stride, uint16_t *pre, int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    if (!self_test_manner(kernel, clocks, dev_status)) return EP_ERR_INVALID_ARG;
+    return linear_call({kernel, clocks}, rows, in_features, out_features, activation, x, x_stride, w, bias, residual,
+                       residual_stride, out_dtype, out, out_stride, pre, dev_status, stream);
+}
+
+int ep_selftest_linear_backward(int kernel, int64_t clocks, int64_t rows, int64_t in_features, int64_t out_features,
+                                int activation, int grad_dtype, const void *grad_out, int64_t grad_stride,
+                                const uint16_t *x, int64_t x_stride, const uint16_t *w, const uint16_t *pre,
+                                uint16_t *grad_x, int64_t grad_x_stride, int grad_w_dtype, void *grad_w,
+                                float *grad_bias, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                ep_stream_t stream) {
+    g_err[0] = 0;
+    if (!self_test_manner(kernel, clocks, dev_status)) return EP_ERR_INVALID_ARG;
+    return linear_backward_call({kernel, clocks}, rows, in_features, out_features, activation, grad_dtype, grad_out,
+                                grad_stride, x, x_stride, w, pre, grad_x, grad_x_stride, grad_w_dtype, grad_w,
+                                grad_bias, workspace, workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"
@@ -1008,23 +1068,11 @@ bool moe_few_parts(const ep::Dims &d, int64_t I, MoeFewParts &b) {
     return true;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t ep_moe_few_workspace_bytes(const ep_problem *p, int64_t intermediate) {
-    g_err[0] = 0;
-    ep::Dims d;
-    MoeFewParts b;
-    return make_dims(p, d) && moe_few_parts(d, intermediate, b) ? b.total : 0;
-}
-
-int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, const uint16_t *x, int logits_dtype,
-               const void *logits, int64_t logits_row_stride, const float *bias, const uint8_t *gate_up,
-               const float *gate_up_scales, const uint8_t *down, const float *down_scales, const uint16_t *residual,
-               uint16_t *out, int64_t *topk_idx, float *topk_weights, void *workspace, size_t workspace_bytes,
-               int32_t *dev_status, ep_stream_t stream) {
-    g_err[0] = 0;
+int moe_few_call(int64_t clocks, const ep_problem *p, const ep_router *r, int64_t intermediate, const uint16_t *x,
+                 int logits_dtype, const void *logits, int64_t logits_row_stride, const float *bias,
+                 const uint8_t *gate_up, const float *gate_up_scales, const uint8_t *down, const float *down_scales,
+                 const uint16_t *residual, uint16_t *out, int64_t *topk_idx, float *topk_weights, void *workspace,
+                 size_t workspace_bytes, int32_t *dev_status, ep_stream_t stream) {
     ep::Dims d;
     MoeFewParts b;
     if (!make_dims(p, d) || !moe_few_parts(d, intermediate, b)) return EP_ERR_INVALID_ARG;
@@ -1064,9 +1112,44 @@ int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, co
     a.parts = (float *)(ws += b.arrived);
     a.split = (unsigned *)(ws + b.parts);
     a.out = out;
-    a.wait_clocks = ep::kWaitClocks;
+    a.wait_clocks = clocks;
     cudaError_t e = ep::launch_moe_few(a, (cudaStream_t)stream);
     return e ? cuda_fail(e, "ep_moe_few launch") : EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ep_moe_few_workspace_bytes(const ep_problem *p, int64_t intermediate) {
+    g_err[0] = 0;
+    ep::Dims d;
+    MoeFewParts b;
+    return make_dims(p, d) && moe_few_parts(d, intermediate, b) ? b.total : 0;
+}
+
+int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, const uint16_t *x, int logits_dtype,
+               const void *logits, int64_t logits_row_stride, const float *bias, const uint8_t *gate_up,
+               const float *gate_up_scales, const uint8_t *down, const float *down_scales, const uint16_t *residual,
+               uint16_t *out, int64_t *topk_idx, float *topk_weights, void *workspace, size_t workspace_bytes,
+               int32_t *dev_status, ep_stream_t stream) {
+    g_err[0] = 0;
+    return moe_few_call(ep::kWaitClocks, p, r, intermediate, x, logits_dtype, logits, logits_row_stride, bias,
+                        gate_up, gate_up_scales, down, down_scales, residual, out, topk_idx, topk_weights, workspace,
+                        workspace_bytes, dev_status, stream);
+}
+
+int ep_selftest_moe_few(int64_t clocks, const ep_problem *p, const ep_router *r, int64_t intermediate,
+                        const uint16_t *x, int logits_dtype, const void *logits, int64_t logits_row_stride,
+                        const float *bias, const uint8_t *gate_up, const float *gate_up_scales, const uint8_t *down,
+                        const float *down_scales, const uint16_t *residual, uint16_t *out, int64_t *topk_idx,
+                        float *topk_weights, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                        ep_stream_t stream) {
+    g_err[0] = 0;
+    if (!self_test_manner(EP_LINEAR_FEW_ROWS, clocks, dev_status)) return EP_ERR_INVALID_ARG;
+    return moe_few_call(clocks, p, r, intermediate, x, logits_dtype, logits, logits_row_stride, bias, gate_up,
+                        gate_up_scales, down, down_scales, residual, out, topk_idx, topk_weights, workspace,
+                        workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"

@@ -369,6 +369,7 @@ cudaError_t launch_linear_few(int form, const LinearArgs &a, const LinearOperand
     int64_t tiles;
     double time;
     const FewPlan p = few_plan(form, a, size, tiles, time);
+    if (tiles * size >= (int64_t)1 << 31) return cudaErrorInvalidConfiguration;    // (a self-test; otherwise the other kernel's)
     const bool r_mn = form == kFormGradW, c_mn = form != kFormForward;
     FewMaps maps;
     const auto map = [](const LinearOperand &o, int rows, CUtensorMap *m) {

@@ -28,6 +28,7 @@ EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_KEY_LOGIT, EP_KEY_SCORE = 0, 1
 EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_SWIGLU = 0, 1, 2, 3, 4
 EP_EXPERT_FEW_ROWS, EP_EXPERT_MANY_ROWS = 0, 1
+EP_LINEAR_FEW_ROWS, EP_LINEAR_MANY_ROWS = 0, 1
 EP_WIRE_MXFP8, EP_WIRE_NVFP4 = 1, 2
 WIRES = {"mxfp8": EP_WIRE_MXFP8, "nvfp4": EP_WIRE_NVFP4}
 
@@ -45,7 +46,8 @@ EXPORTS = ("ep_last_error_string", "ep_get_status", "ep_recv_rows", "ep_layout_w
            "ep_selftest_wait_timeout", "ep_combine_quantize", "ep_combine_wire", "ep_stage_rows",
            "ep_dispatch_two_level", "ep_combine_two_level", "ep_route", "ep_route_backward",
            "ep_combine_backward", "ep_expert_gemm", "ep_expert_swiglu", "ep_selftest_expert_timeout", "ep_linear",
-           "ep_linear_backward_workspace_bytes", "ep_linear_backward", "ep_moe_few_workspace_bytes", "ep_moe_few")
+           "ep_linear_backward_workspace_bytes", "ep_linear_backward", "ep_moe_few_workspace_bytes", "ep_moe_few",
+           "ep_selftest_linear", "ep_selftest_linear_backward", "ep_selftest_moe_few")
 
 
 class EpError(RuntimeError):
@@ -156,6 +158,9 @@ def _load():
     lib.ep_moe_few_workspace_bytes.restype = sz
     lib.ep_moe_few.argtypes = [pp, rp, i64, P, i, P, i64, P, P, P, P, P, P, P, P, P, P, sz, P, P]
     lib.ep_moe_few.restype = i
+    for fn, more in ((lib.ep_linear, [i, i64]), (lib.ep_linear_backward, [i, i64]), (lib.ep_moe_few, [i64])):
+        test = getattr(lib, fn.__name__.replace("ep_", "ep_selftest_", 1))
+        test.argtypes, test.restype = more + fn.argtypes, i
     return lib
 
 
@@ -629,6 +634,11 @@ def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "
               stream=None) -> None:
     """out [M, N] (bf16 or fp32) = act(x [M, K] @ w.T + bias) + residual; w [N, K], with "swiglu" [2 N, K] (gate rows
     first), bias fp32, residual [M, N] bf16 (may be out itself), pre [M, w's rows] bf16 receives the pre-activations."""
+    return _call("ep_linear", _lib.ep_linear,
+                 _linear_args(x, w, out, bias, residual, pre, activation, dev_status, stream))
+
+
+def _linear_args(x, w, out, bias=None, residual=None, pre=None, activation="none", dev_status=None, stream=None):
     M, K, N, wide = _linear_sizes(x, w, activation)
     dev = _device_of(x, "x")
     if out is None:
@@ -636,11 +646,10 @@ def ep_linear(x, w, out, bias=None, residual=None, pre=None, activation: str = "
     xp, xs = _rows(x, "x", M, K, dev)
     op, os_ = _rows(out, "out", M, N, dev, _F16 + _F32)
     rp, rs = _rows(residual, "residual", M, N, dev)
-    args = (M, K, N, ACTIVATIONS[activation], xp, xs, _shaped(w, "w", (wide, K), _F16, dev),
+    return (M, K, N, ACTIVATIONS[activation], xp, xs, _shaped(w, "w", (wide, K), _F16, dev),
             _shaped(bias, "bias", (wide,), _F32, dev), rp, rs, EP_FP32 if out.dtype == torch.float32 else EP_BF16, op, os_,
             _shaped(pre, "pre", (M, wide), _F16, dev), _buffer(dev_status, "dev_status", torch.int32, 1, dev),
             _stream_here(stream, dev))
-    return _call("ep_linear", _lib.ep_linear, args)
 
 
 def ep_linear_backward_workspace_bytes(rows: int, in_features: int, out_features: int, activation: str = "none") -> int:
@@ -654,6 +663,13 @@ def ep_linear_backward(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None,
     """Gradients of ep_linear from grad_out [M, N] (bf16 or fp32): grad_x [M, K] bf16, grad_w (w's shape, bf16 or fp32)
     and grad_bias fp32, each left out if None; pre as ep_linear wrote it (not needed for "none"); workspace uint8 of
     ep_linear_backward_workspace_bytes()."""
+    return _call("ep_linear_backward", _lib.ep_linear_backward,
+                 _linear_backward_args(grad_out, x, w, grad_x, grad_w, grad_bias, pre, activation, workspace, dev_status,
+                                       stream))
+
+
+def _linear_backward_args(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None, pre=None, activation="none",
+                          workspace=None, dev_status=None, stream=None):
     M, K, N, wide = _linear_sizes(x, w, activation)
     dev = _device_of(x, "x")
     if grad_out is None:
@@ -662,12 +678,11 @@ def ep_linear_backward(grad_out, x, w, grad_x=None, grad_w=None, grad_bias=None,
     gp, gs = _rows(grad_out, "grad_out", M, N, dev, _F16 + _F32)
     gxp, gxs = _rows(grad_x, "grad_x", M, K, dev)
     code = lambda t: EP_FP32 if t is not None and t.dtype == torch.float32 else EP_BF16
-    args = (M, K, N, ACTIVATIONS[activation], code(grad_out), gp, gs, xp, xs, _shaped(w, "w", (wide, K), _F16, dev),
+    return (M, K, N, ACTIVATIONS[activation], code(grad_out), gp, gs, xp, xs, _shaped(w, "w", (wide, K), _F16, dev),
             _shaped(pre, "pre", (M, wide), _F16, dev), gxp, gxs, code(grad_w),
             _shaped(grad_w, "grad_w", (wide, K), _F16 + _F32, dev), _shaped(grad_bias, "grad_bias", (wide,), _F32, dev),
             _buffer(workspace, "workspace", torch.uint8, None, dev), workspace.numel() if workspace is not None else 0,
             _buffer(dev_status, "dev_status", torch.int32, 1, dev), _stream_here(stream, dev))
-    return _call("ep_linear_backward", _lib.ep_linear_backward, args)
 
 
 def ep_moe_few_workspace_bytes(p: ep_problem, intermediate: int) -> int:
@@ -679,6 +694,13 @@ def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_sc
     """The layer of up to 64 tokens x [T, H] bf16: routes logits [T, E] (as ep_route, into topk_idx and topk_weights),
     runs the chosen experts (gate_up [E, 2 I, H] and down [E, H, I], e4m3 codes with fp32 scales for 128 x 128 blocks)
     and writes out [T, H] bf16 = their weighted sum + residual; workspace uint8 of ep_moe_few_workspace_bytes()."""
+    return _call("ep_moe_few", _lib.ep_moe_few,
+                 _moe_few_args(p, r, x, logits, bias, gate_up, gate_up_scales, down, down_scales, out, topk_idx, topk_weights,
+                               workspace, residual, dev_status, stream))
+
+
+def _moe_few_args(p, r, x, logits, bias, gate_up, gate_up_scales, down, down_scales, out, topk_idx, topk_weights, workspace,
+                  residual=None, dev_status=None, stream=None):
     T, H, E, n = p.num_tokens, p.hidden, p.num_experts, p.num_tokens * p.num_topk
     N, K = _expert_shape(p, gate_up, "gate_up")
     I = N // 2
@@ -688,7 +710,7 @@ def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_sc
     ptr, stride, dt = _logits(logits, p, "logits")
     if logits.get_device() != dev:
         raise ValueError(f"logits is on {logits.device}, the current device is cuda:{dev}")
-    args = (ctypes.byref(p), ctypes.byref(r), I, _shaped(x, "x", (T, H), _F16, dev), dt, ptr, stride,
+    return (ctypes.byref(p), ctypes.byref(r), I, _shaped(x, "x", (T, H), _F16, dev), dt, ptr, stride,
             _buffer(bias, "bias", torch.float32, E, dev), _shaped(gate_up, "gate_up", (E, N, H), u8, dev),
             _shaped(gate_up_scales, "gate_up_scales", (E, N // 128, H // 128), _F32, dev),
             _shaped(down, "down", (E, H, I), u8, dev),
@@ -697,7 +719,23 @@ def ep_moe_few(p: ep_problem, r: ep_router, x, logits, bias, gate_up, gate_up_sc
             _buffer(topk_idx, "topk_idx", torch.int64, n, dev), _buffer(topk_weights, "topk_weights", torch.float32, n, dev),
             _buffer(workspace, "workspace", torch.uint8, None, dev), workspace.numel() if workspace is not None else 0,
             _buffer(dev_status, "dev_status", torch.int32, 1, dev), _stream_here(stream, dev))
-    return _call("ep_moe_few", _lib.ep_moe_few, args)
+
+
+def ep_selftest_linear(kernel: int, clocks: int, *args, **kwargs) -> None:
+    """ep_linear (its arguments follow) by the kernel for few or many rows (EP_LINEAR_*), with waits that give up after
+    `clocks` cycles and raise EP_STATUS_TIMEOUT."""
+    return _call("ep_selftest_linear", _lib.ep_selftest_linear, (int(kernel), int(clocks), *_linear_args(*args, **kwargs)))
+
+
+def ep_selftest_linear_backward(kernel: int, clocks: int, *args, **kwargs) -> None:
+    """The same of ep_linear_backward."""
+    return _call("ep_selftest_linear_backward", _lib.ep_selftest_linear_backward,
+                 (int(kernel), int(clocks), *_linear_backward_args(*args, **kwargs)))
+
+
+def ep_selftest_moe_few(clocks: int, *args, **kwargs) -> None:
+    """The same of ep_moe_few, which has one kernel."""
+    return _call("ep_selftest_moe_few", _lib.ep_selftest_moe_few, (int(clocks), *_moe_few_args(*args, **kwargs)))
 
 
 def ep_selftest_wait_timeout(words, polls: int, dev_status, stream=None) -> None:

@@ -67,6 +67,7 @@ enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
 enum { EP_KEY_LOGIT = 0, EP_KEY_SCORE = 1 };
 enum { EP_ACT_NONE = 0, EP_ACT_RELU = 1, EP_ACT_SILU = 2, EP_ACT_GELU = 3, EP_ACT_SWIGLU = 4 };
 enum { EP_EXPERT_FEW_ROWS = 0, EP_EXPERT_MANY_ROWS = 1 };   /* ep_selftest_expert_timeout only */
+enum { EP_LINEAR_FEW_ROWS = 0, EP_LINEAR_MANY_ROWS = 1 };   /* ep_selftest_linear and _backward only */
 
 /* How ep_route turns a token's logits into experts and weights.  A router
  * trained with a bias on its softmax scores, or with groups scored by sums of
@@ -603,6 +604,33 @@ int ep_moe_few(const ep_problem *p, const ep_router *r, int64_t intermediate, co
                const float *gate_up_scales, const uint8_t *down, const float *down_scales, const uint16_t *residual,
                uint16_t *out, int64_t *topk_idx, float *topk_weights, void *workspace, size_t workspace_bytes,
                int32_t *dev_status, ep_stream_t stream);
+
+/*
+ * ep_selftest_linear, ep_selftest_linear_backward, ep_selftest_moe_few -
+ * failure-detection self-tests: the calls of the same names with waits that give up
+ * after `clocks` cycles (1 .. 2^32, their own limit), the products by the kernel for
+ * few or for many rows (EP_LINEAR_*), whichever is faster.
+ *
+ * A launch whose waits give up raises EP_STATUS_TIMEOUT in *dev_status (not NULL),
+ * leaves any part of its outputs unwritten or wrong and returns with nothing in flight.
+ * What follows on the stream is not affected.
+ */
+int ep_selftest_linear(int kernel, int64_t clocks, int64_t rows, int64_t in_features, int64_t out_features,
+                       int activation, const uint16_t *x, int64_t x_stride, const uint16_t *w, const float *bias,
+                       const uint16_t *residual, int64_t residual_stride, int out_dtype, void *out,
+                       int64_t out_stride, uint16_t *pre, int32_t *dev_status, ep_stream_t stream);
+int ep_selftest_linear_backward(int kernel, int64_t clocks, int64_t rows, int64_t in_features, int64_t out_features,
+                                int activation, int grad_dtype, const void *grad_out, int64_t grad_stride,
+                                const uint16_t *x, int64_t x_stride, const uint16_t *w, const uint16_t *pre,
+                                uint16_t *grad_x, int64_t grad_x_stride, int grad_w_dtype, void *grad_w,
+                                float *grad_bias, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                ep_stream_t stream);
+int ep_selftest_moe_few(int64_t clocks, const ep_problem *p, const ep_router *r, int64_t intermediate,
+                        const uint16_t *x, int logits_dtype, const void *logits, int64_t logits_row_stride,
+                        const float *bias, const uint8_t *gate_up, const float *gate_up_scales, const uint8_t *down,
+                        const float *down_scales, const uint16_t *residual, uint16_t *out, int64_t *topk_idx,
+                        float *topk_weights, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                        ep_stream_t stream);
 
 #ifdef __cplusplus
 }
