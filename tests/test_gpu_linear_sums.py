@@ -84,3 +84,41 @@ def test_bf16_results_do_not_lag(m, K, most):
     want = x.double() @ w.double().t()
     # (roundings are independent, at most 2^-8 each: of their mean over 2^22, 5 standard deviations of 2^-8 / 3^0.5 / 2^11)
     assert abs(float(((out.double() - want) / want).mean())) <= lag(K, most) + 5 * 2.0 ** -8 / 3 ** 0.5 / 2 ** 11
+
+
+@pytest.mark.parametrize("kernel", ["EP_LINEAR_FEW_ROWS", "EP_LINEAR_MANY_ROWS"])
+@pytest.mark.parametrize("M,N,K", [(16, 256, 7168), (16, 256, 65536), (48, 200, 4096)])
+def test_fp32_results_do_not_lag(m, kernel, M, N, K):
+    """Every output, not the mean: a whole contraction of 7168 in one accumulator would be 2.6e-5 behind."""
+    gen = torch.Generator(DEV).manual_seed(3)
+    x, w = ((torch.rand(r, K, generator=gen, device=DEV) / 2 + 0.5).bfloat16() for r in (M, N))
+    out = torch.empty(M, N, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    m.ep_selftest_linear(getattr(m, kernel), 1 << 32, x, w, out, dev_status=st)
+    assert m.ep_get_status(st) == 0
+    want = x.double() @ w.double().t()
+    assert bool(((out.double() - want).abs() <= lag(K) * want).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(2433, 256, 7168), (2432, 256, 7168), (700, 2048, 7168), (1, 256, 1 << 18)])
+def test_fp32_results_do_not_lag_by_choice(m, M, N, K):
+    """The same by whichever kernel the call takes."""
+    gen = torch.Generator(DEV).manual_seed(4)
+    x, w = ((torch.rand(r, K, generator=gen, device=DEV) / 2 + 0.5).bfloat16() for r in (M, N))
+    out = torch.empty(M, N, device=DEV)
+    m.ep_linear(x, w, out)
+    want = x.double() @ w.double().t()
+    assert bool(((out.double() - want).abs() <= lag(K) * want).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(65536, 64, 512), (65536, 1024, 1024), (9000, 8, 64)])
+def test_fp32_matrix_gradients_do_not_lag(m, M, N, K):
+    gen = torch.Generator(DEV).manual_seed(5)
+    g, x = ((torch.rand(M, c, generator=gen, device=DEV) / 2 + 0.5).bfloat16() for c in (N, K))
+    gw, gb = torch.empty(N, K, device=DEV), torch.empty(N, device=DEV)
+    ws = torch.empty(m.ep_linear_backward_workspace_bytes(M, K, N), dtype=torch.uint8, device=DEV)
+    m.ep_linear_backward(g, x, torch.empty(N, K, dtype=torch.bfloat16, device=DEV), grad_w=gw, grad_bias=gb, workspace=ws)
+    want = g.double().t() @ x.double()
+    assert bool(((gw.double() - want).abs() <= lag(M) * want).all())
+    # (fp32 sums of at most M / 8 rows of a block and a lane, rounded to nearest)
+    assert bool(((gb.double() - g.double().sum(0)).abs() <= (M / 8 + 32) * 2.0 ** -25 * g.double().sum(0)).all())
