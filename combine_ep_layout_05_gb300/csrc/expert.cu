@@ -203,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
                 }
                 if (!ok) break;
             }
-            drain<S>(s.boxes, it);
+            drain(s.boxes, S, it);
             __syncwarp();
         } else if (warp == 1) {
             // ---- products (the loop is the whole warp's, so that its values are uniform; one lane issues) ----
@@ -446,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpertThreads, 1)
     __syncthreads();
     cluster_sync();    // the other CTA's threads arrive here no more, and its boxes have landed
     if (warp == 1) {
-        drain<S>(s.done, s.issued);      // products read both CTAs' shared memory and arrive in both
+        drain(s.done, S, s.issued);      // products read both CTAs' shared memory and arrive in both
         __syncwarp();
         tmem_fence_after();
         tmem_free<2>(tmem);

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (++st == S) { st = 0; ph ^= 1; }
                     }
                 }
-                drain<S>(s.boxes, it);
+                drain(s.boxes, S, it);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     aph ^= acc == 0;
                 }
             }
-            drain<S>(s.done, it);
+            drain(s.done, S, it);
             __syncwarp();
         } else if (warp == 2) {
             // ---- word of the operands: to the products, and to the accumulation, which reads the scales and the rows'

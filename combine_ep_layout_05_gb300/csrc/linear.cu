@@ -154,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             // the products of a step follow its boxes
-            drain_ring(s.empty, S, it);
+            drain(s.empty, S, it);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -20,20 +20,16 @@ constexpr int kGradThreads = 256;
 constexpr int kLanes = 8;                       // rows a block works on at once
 constexpr int kCols = kGradThreads / kLanes * 8;
 
-// d act(z) / dz, of the one-input activations
+// d act(z) / dz, of silu and gelu
 __device__ __forceinline__ float act_slope(float z, int act) {
-    if (act == EP_ACT_RELU) return z > 0.f ? 1.f : 0.f;
     if (act == EP_ACT_SILU) {
         const float s = sigmoid_fast(z);
         return s * (1.f + z * (1.f - s));
     }
-    if (act == EP_ACT_GELU) {
-        const float s = sigmoid_fast(2.f * kGeluA * (z + kGeluB * z * z * z));
-        const float d = s * (1.f + z * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z));
-        // (from 30 on s is 0 or 1, and z^2 may overflow)
-        return fabsf(z) > 30.f ? (z > 0.f ? 1.f : 0.f) : d;
-    }
-    return 1.f;
+    const float s = sigmoid_fast(2.f * kGeluA * (z + kGeluB * z * z * z));
+    const float d = s * (1.f + z * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z));
+    // (from 30 on s is 0 or 1, and z^2 may overflow)
+    return fabsf(z) > 30.f ? (z > 0.f ? 1.f : 0.f) : d;
 }
 
 // 8 consecutive numbers of a row, of which n exist (the rest read as 0)

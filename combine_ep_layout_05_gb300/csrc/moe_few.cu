@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_prefetch_3d(&map_next, kb * kBlock, v.tile * kBlock, v.e);
                     }
                 }
-                drain_ring(bar.boxes, S, it);
+                drain(bar.boxes, S, it);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -394,23 +394,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++acc == accs) { acc = 0; aph ^= 1; }
                 }
             }
-            drain_ring(bar.done, S, it);
+            drain(bar.done, S, it);
             __syncwarp();
         } else if (warp == 2) {
             // ---- word of the operands: to the products, and to the accumulation, which reads the scales with
             // ordinary loads (the commit's arrival tells of the products) ----
             if (lane == 0) {
                 int st = 0, ph = 0;
-                bool ok = true;
-                {
-                    for (int64_t at = whole_run.at; at < whole_run.end; ++at) {
-                        ok = mbar_wait(&bar.rows_full[st], ph, patience) && mbar_wait(&bar.boxes[st], ph, patience);
-                        if (!ok) break;
-                        fence_async_shared();
-                        mbar_arrive(&bar.done[st]);
-                        mbar_arrive(&bar.full[st]);
-                        if (++st == S) { st = 0; ph ^= 1; }
-                    }
+                for (int64_t at = whole_run.at; at < whole_run.end; ++at) {
+                    if (!mbar_wait(&bar.rows_full[st], ph, patience) || !mbar_wait(&bar.boxes[st], ph, patience)) break;
+                    fence_async_shared();
+                    mbar_arrive(&bar.done[st]);
+                    mbar_arrive(&bar.full[st]);
+                    if (++st == S) { st = 0; ph ^= 1; }
                 }
             }
             __syncwarp();

@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kRouteWarps = 4;
 
-// The same for work that needs no order (the gradient): W lanes share a row of
+// load_lane for work that needs no order (the gradient): W lanes share a row of
 // E elements in turns, of 16 bytes where E is a multiple of them, else of one
 // element.  Only E decides which, so that the order of the sums does not depend
 // on where a row lies; vec: the rows are aligned to 16 bytes.
@@ -81,9 +81,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, La
     const int k = (int)a.k, lo = map.first(lane), held = map.count(lane);
     const L *row = reinterpret_cast<const L *>(a.logits) + t * a.stride;
     float x[V], b[V];
-    uint32_t key[V];
     load_lane<L, V>(row, lo, held, vec, x);
-    bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = 0.f;
     if (a.bias) load_lane<float, V>(a.bias, lo, held, vec && ((uintptr_t)a.bias & 15) == 0, b);

@@ -64,18 +64,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
 // of copies and products that have been issued and so end by themselves.
 // Every CTA does, so that nothing is in flight when it leaves, whether it gave
 // up or not.  All steps together get a second (2^31 cycles).
-template <int S>
-__device__ __forceinline__ void drain(uint64_t *bars, int n) {
+__device__ __forceinline__ void drain(uint64_t *bars, int S, int n) {
     const long long t0 = clock64();
     for (int i = n > S ? n - S : 0; i < n; ++i)
         while (!mbar_try_wait(&bars[i % S], i / S & 1))
-            if (clock64() - t0 > (1ll << 31)) return;
-}
-// the same, with a number of steps that the launch knows
-__device__ __forceinline__ void drain_ring(uint64_t *bars, int stages, int n) {
-    const long long t0 = clock64();
-    for (int i = max(n - stages, 0); i < n; ++i)
-        while (!mbar_try_wait(&bars[i % stages], i / stages & 1))
             if (clock64() - t0 > (1ll << 31)) return;
 }
 
