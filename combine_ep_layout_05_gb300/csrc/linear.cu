@@ -431,9 +431,12 @@ cudaError_t launch_sums(const LinearArgs &a, bool longer, const LinearMaps &maps
 // 7.1, 11.1, 15.4 and 36.8 us; 84 tiles of 32 steps 25.0; 3584 of 4 steps 106 (there the epilogue is what takes the
 // time, 2.2 us a tile).  A split contraction adds the parts' sum: their bytes at 5 TB/s and a launch.
 // The shorter of this and linear_few_time() says which kernel a call takes.  Each forced, in us (few rows' kernel |
-// this one), forward: 7168 -> 256 at 32, 512, 4096 rows 7.4 | 35, 10.8 | 36, 20.8 | 36; 7168 -> 2048 with SwiGLU at 1, 512,
-// 1024, 4096 rows 11.5 | 36, 32 | 37, 53 | 40, 207 | 140; 2048 -> 7168 at 128, 256, 512 rows 12.0 | 14.9, 15.2 | 15.0, 21.7 |
-// 15.6.  grad_x of 2048 -> 1024 at 515 and 2048 rows 10.8 | 9.9, 17.3 | 10.3; grad_w 10.6 | 9.3, 17.0 | 15.7.
+// this one), forward, bf16 results: 7168 -> 256 at 16, 512, 4096 rows 7.1 | 35, 10.6 | 36, 20.6 | 36; 7168 -> 2048 with SwiGLU
+// at 1, 512, 1024, 4096 rows 11.2 | 36, 31.7 | 37, 54 | 38, 207 | 137; 2048 -> 7168 at 128, 256, 512 rows 11.8 | 14.9, 15.1 |
+// 15.0, 22.2 | 15.6.  fp32 results: 7168 -> 256 at 16, 512, 2048 rows 7.1 | 36, 10.6 | 36, 15.6 | 37; where the few rows' kernel
+// would have to keep more than kChain steps in an accumulator, this one takes the call although it is slower: 4096 rows 25 |
+// 37 (from 2433 rows on), 256 rows of the SwiGLU 24 | 37, 2048 of 1024 -> 1024 13.5 | 15.9.  grad_x of 2048 -> 1024 at 515 and
+// 2048 rows 10.8 | 9.9, 17.3 | 10.3; grad_w 10.6 | 9.3, 17.0 | 15.7.
 double linear_time(int64_t R, int64_t C, int64_t L, bool swiglu, int splits) {
     const int64_t cols = swiglu ? kPart : kTile, tiles = ((R + kTile - 1) / kTile) * ((C + cols - 1) / cols);
     const int64_t steps = ((L + kStep - 1) / kStep + splits - 1) / splits, turns = (tiles * splits + 75) / 76;
@@ -466,7 +469,7 @@ cudaError_t launch_linear(int form, LinearArgs a, const LinearOperand &A, const 
     // are: 41 | 37, 74 | 68.  (2) Where whole tiles would leave half of the SMs or more without work in the last turn, the turns
     // are made equal in rows.  A turn of products takes as long, but the memory has the same work all the time.  Cold,
     // 7168 -> 256, whole | equal: 20000 rows (the last turn has 3 of 76 pairs) 98 | 84, 28000 (34) 100 | 94, 44000 (20)
-    // 146 | 136, 65536 (28) 192 | 187; 32768 (52) 98.1 | 103.9.  One turn stays: 10000 rows 41.0 | 41.8.
+    // 146 | 136, 65536 (28) 192 | 187; 32768 (52) 98.1 | 103.9.  A single turn is not cut: its 112 steps take as long either way.
     if (form == kFormForward && a.col_tiles == 1) {
         if (!swiglu) a.half_cols = (int)(std::max<int64_t>(a.C, 32) + 15) / 16 * 8;
         const int64_t pairs = num_sms() / 2, tiles = (a.R + kTile - 1) / kTile, turns = (tiles + pairs - 1) / pairs;

@@ -16,9 +16,9 @@
 // accumulator takes more, at most kMostChain, for a bf16 result; for an fp32 result, or for longer ones, the
 // other kernel does the work.
 //
-// Measured, from a graph: 32 rows of 7168 -> 256 (a gate) 7.4 us, of which the launch, the tensor memory, the first
-// boxes and the exchange take 5; one row of 7168 -> 2 x 2048 with SwiGLU 11.5 us (59 MB, 5.1 TB/s); 512 rows of
-// 7168 -> 256 10.8 us.
+// Measured, from a graph, operands in L2: 32 rows of 7168 -> 256 (a gate) 7.0 us, of which the launch, the tensor memory, the
+// first boxes and the exchange take 5; 512 rows 10.6 us; one row of 7168 -> 2 x 2048 with SwiGLU 11.2 us.  Where the
+// SwiGLU's matrix comes from memory, as in a decode step, it takes 17.2 us (59 MB, 3.4 TB/s).
 #include <algorithm>
 #include <cstddef>
 

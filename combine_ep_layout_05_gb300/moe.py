@@ -91,7 +91,8 @@ class MoeLayer:
     def forward(self, x, logits=None, stream=None, out=None):
         """x [T, H] bf16 and gate logits [T, E] (bf16 or fp32; None: the gate's, kept in self.logits) -> [T, H] bf16.
         self.idx, self.weights and (not few) self.pipe.buf.tokens_per_expert hold the routing;
-        ep_get_status(self.status) tells of bad logits."""
+        ep_get_status(self.status) tells of bad logits.  With a shared expert the output is a bf16 number added to another
+        in fp32 and rounded: few: the shared expert's output, to the routed sum; else the routed sum, to the shared expert's."""
         if logits is None:
             if self.gate is None:
                 raise ValueError("a layer without a gate needs logits")
@@ -156,7 +157,8 @@ class MoeLayer:
 
     def gate_grad(self, grad_logits, x, grad_x=None, grad_gate=None, stream=None):
         """Gradients of the logits' product, from router_grad's: grad_x [T, H] bf16 (the tokens', through the gate
-        alone) and grad_gate [E, H] bf16 or fp32; None: not computed."""
+        alone) and grad_gate [E, H] bf16 or fp32; None: not computed.  An fp32 grad_logits is rounded to bf16 as the
+        products' operand, once, for an fp32 grad_gate too."""
         if self.gate is None:
             raise ValueError("a layer without a gate has no gate_grad")
         ep.ep_linear_backward(grad_logits, x, self.gate, grad_x=grad_x, grad_w=grad_gate,
