@@ -559,8 +559,8 @@ size_t ep_linear_backward_workspace_bytes(int64_t rows, int64_t in_features, int
  *   grad_bias[n] = sum_m G[m, n];
  *   grad_x[m, i] = sum_n bf16(G[m, n]) * w[n, i], rounded once to bf16;
  *   grad_w[n, i] = sum_m bf16(G[m, n]) * x[m, i], rounded once if bf16.
- * G is rounded to bf16 as an operand of the tensor core; a bf16 grad_out
- * without an activation goes in exactly.  Sums are fp32.  An output that is NULL is not
+ * G is rounded to bf16 as an operand of the tensor core, for fp32 results too; a bf16
+ * grad_out without an activation goes in exactly.  Sums are fp32.  An output that is NULL is not
  * computed.  grad_out [rows, out_features] bf16 or fp32 (grad_dtype); pre NULL
  * without an activation; grad_x bf16, row stride grad_x_stride; grad_w
  * [out_features (x 2), in_features] bf16 or fp32 (grad_w_dtype), contiguous, 16-byte
